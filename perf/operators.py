@@ -94,7 +94,8 @@ def draw(rng):
         if op == "route":
             c = _route("", M, E, k, method, renorm, groups, kept, rng.randint(0, 1), scale, dtype)
         else:
-            c = _grad("", M, E, k, method, renorm, scale, dtype)
+            # one renormalised weight is constant: its gradient is zero
+            c = _grad("", M, E, max(k, 2) if renorm else k, method, renorm, scale, dtype)
     elif op == "quant":
         c = _quant("", _log(rng, 1, 8192), 16 * _log(rng, 2, 448), rng.random() < 0.5)
     else:
