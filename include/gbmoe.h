@@ -117,6 +117,61 @@ GBMOE_API moe_status_t moe_route_bf16(const void* router_logits, int64_t M, int3
                                       float* topk_weights, int32_t* topk_ids,
                                       moe_stream_t stream);
 
+/* moe_route_biased: moe_route with a per-expert bias for load balance.  The
+ * bias takes part in the choice of experts and groups and not in their
+ * weights:
+ *   c_e = p_e + score_bias[e];  groups scored by their largest c (mode 0) or
+ *   by the sum of their two largest c (mode 1);  ids = TopK(c), by descending
+ *   c, ties to the lower id;  weights from the chosen experts' p as moe_route.
+ * c is compared as in 64-bit arithmetic (experts whose c agree there are
+ * ties).  An expert with logit -inf is masked: it is chosen only after every
+ * other expert of the kept groups, with weight 0, and a token whose chosen
+ * experts are all masked has weights of 0.  A NaN score is chosen as late;
+ * its weight, and with renormalised weights the token's, are NaN; in a
+ * softmax row a NaN or +inf logit makes every score NaN.  The ids are valid
+ * and distinct whatever the logits hold.
+ * The pages have no counterpart to this entry point: it is the routing of
+ * models whose experts are balanced by such a bias.
+ *  router_logits  device fp32 or (logits_bf16 = 1) bf16 [M, E]
+ *  score_bias     device fp32 [E]
+ * Everything else, and the limits, as moe_route; M < 2^31; pointers aligned
+ * to their elements.
+ */
+GBMOE_API moe_status_t moe_route_biased(const void* router_logits, int32_t logits_bf16,
+                                        const float* score_bias, int64_t M, int32_t E,
+                                        int32_t top_k, int32_t routing_method,
+                                        int32_t renormalize, int32_t k_group,
+                                        int32_t group_count, int32_t group_select_mode,
+                                        float routed_scaling_factor, float* topk_weights,
+                                        int32_t* topk_ids, moe_stream_t stream);
+
+/* moe_route_backward: the gradient of the routing weights with respect to
+ * the router logits, for chosen experts that are held fixed (groups and bias
+ * only choose; they have no gradient).  With w the weights moe_route or
+ * moe_route_biased gives for these ids,
+ *   grad_logits[t, e] = sum_j grad_weights[t, j] * dw[t, j] / dlogits[t, e].
+ * Sigmoid, and softmax with renormalize: only the chosen experts' entries
+ * are nonzero; softmax without: every entry.  Every entry is written.  An
+ * expert named twice in a token counts twice.  Masked logits (-inf) have a
+ * gradient of 0.
+ * The pages have no counterpart to this entry point.
+ *  grad_weights   device fp32 [M, top_k]
+ *  router_logits  device fp32 or (logits_bf16 = 1) bf16 [M, E]
+ *  topk_ids       device int32 [M, top_k]; an id outside [0, E) takes no part
+ *                 (its weight counts as 0) and sets MOE_ERR_BAD_EXPERT_ID
+ *  grad_logits    device [M, E] of the logits' type, written; must not
+ *                 overlap the inputs
+ *  error_word     device int32 or NULL
+ * Pointers aligned to their elements.  Limits: 1 <= E <= 1024,
+ * 1 <= top_k <= 64, M < 2^31.
+ */
+GBMOE_API moe_status_t moe_route_backward(const float* grad_weights, const void* router_logits,
+                                          int32_t logits_bf16, const int32_t* topk_ids,
+                                          int64_t M, int32_t E, int32_t top_k,
+                                          int32_t routing_method, int32_t renormalize,
+                                          float routed_scaling_factor, void* grad_logits,
+                                          int32_t* error_word, moe_stream_t stream);
+
 /* ---------------------------------------------------------- router GEMM --
  * moe_router_logits: the router scores ahead of routing,
  *   s_t = W_g^T x_t + b_g        ("fused_moe.py 分析" (FlagDoc), section 1.1)
@@ -381,6 +436,50 @@ GBMOE_API moe_status_t moe_forward_fp8(const void* hidden, const float* topk_wei
  */
 GBMOE_API moe_status_t moe_quant_rows_fp8(const void* x, int64_t M, int32_t H, void* q8,
                                           float* scale, moe_stream_t stream);
+
+/* ----------------------------------------------------------- dense FP8 --
+ * The linear layers beside the experts (a shared expert, projections) in the
+ * block-wise scheme of MOE_FP8_SCALE_BLOCK ("fused_moe.py 分析", FP8 W8A8):
+ * activations with one scale per row and group of 128 along K, weights with
+ * one per 128 x 128 block, the FP8 dot product of each 128-wide K block times
+ * both, summed over the blocks in fp32.
+ *
+ * moe_quant_groups_fp8: the activations' quantisation.  With z = x, or for
+ * swiglu = 1 z = SiLU(x[:, :K]) * x[:, K:] in fp32 (gate columns first, as
+ * in w13), for each row and each group of 128 columns (the last may be
+ * shorter):
+ *   scale = fp32(max|z| / 448), 1 where all are zero;
+ *   q8 = e4m3(fp32(z / scale)), round to nearest even, saturating.
+ * A NaN makes its group's scale and codes NaN; an infinity its scale
+ * infinite, its own code NaN and the others 0.
+ *  x      device bf16 [M, K], or [M, 2K] for swiglu
+ *  q8     device E4M3 bytes [M, K], written
+ *  scale  device fp32 [M, ceil(K / 128)], written
+ * x and q8 16-byte aligned.  Limits: K a multiple of 16 up to 2^24, M < 2^31.
+ */
+GBMOE_API moe_status_t moe_quant_groups_fp8(const void* x, int64_t M, int32_t K, int32_t swiglu,
+                                            void* q8, float* scale, moe_stream_t stream);
+
+/* moe_matmul_fp8: out[m, n] = sum_b a_scale[m, b] * ws(b, n / 128) *
+ * (sum over k in block b of a[m, k] * w(k, n)) + bias[n].
+ *  a         device E4M3 bytes [M, K];  a_scale device fp32 [M, ceil(K/128)]
+ *  w         w_transposed = 0: device E4M3 bytes [K, N] with w_scale fp32
+ *            [ceil(K/128), ceil(N/128)], the experts' orientation;
+ *            w_transposed = 1: [N, K] with [ceil(N/128), ceil(K/128)].  One
+ *            stored weight so serves y = x W and the gradient's dx = dy W^T.
+ *  bias      device bf16 [N] or NULL
+ *  out       device bf16 [M, N], or fp32 with out_f32 = 1; must not overlap
+ *            the inputs
+ *  error_word device int32 or NULL: set to MOE_ERR_TIMEOUT if a pipeline
+ *            wait ran out of time (the output is then incomplete)
+ * a, w, bias and out 16-byte aligned.  Limits: K a multiple of 16 up to 2^24,
+ * N a multiple of 16 up to 2^22, M < 2^31.
+ */
+GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const void* w,
+                                      const float* w_scale, int32_t w_transposed,
+                                      const void* bias, int64_t M, int32_t K, int32_t N,
+                                      int32_t out_f32, void* out, int32_t* error_word,
+                                      moe_stream_t stream);
 
 /* ---------------------------------------------- weight-only quantised --
  * Expert weights stored quantised, activations bf16.  Defines: "fused_moe.py

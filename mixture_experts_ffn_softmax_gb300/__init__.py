@@ -92,9 +92,19 @@ def moe_route(router_logits: torch.Tensor, top_k: int, routing_method: str = "so
               renormalize: bool = False, k_group: int = 1, group_count: int = 1,
               group_select_mode: int = 0, routed_scaling_factor: float = 1.0,
               topk_weights: Optional[torch.Tensor] = None,
-              topk_ids: Optional[torch.Tensor] = None, stream=None):
+              topk_ids: Optional[torch.Tensor] = None, stream=None,
+              score_bias: Optional[torch.Tensor] = None):
     """router_logits fp32 or bf16 [M, E] -> (topk_weights fp32 [M, k],
-    topk_ids int32 [M, k])."""
+    topk_ids int32 [M, k]).
+
+    score_bias: fp32 [E] added to the scores for the choice of experts and
+    groups, not for the weights (moe_route_biased in gbmoe.h: ids by
+    descending biased score, compared as in 64 bits; logits of -inf mask
+    their experts)."""
+    if score_bias is not None:
+        return _route_biased(router_logits, score_bias, top_k, routing_method, renormalize,
+                             k_group, group_count, group_select_mode, routed_scaling_factor,
+                             topk_weights, topk_ids, stream)
     assert router_logits.dtype in (torch.float32, torch.bfloat16) and router_logits.dim() == 2
     M, E = router_logits.shape
     dev = router_logits.device
@@ -108,6 +118,106 @@ def moe_route(router_logits: torch.Tensor, top_k: int, routing_method: str = "so
               float(routed_scaling_factor), _ptr(topk_weights), _ptr(topk_ids),
               _stream(stream)), "moe_route")
     return topk_weights, topk_ids
+
+
+def _tensor(t, name: str, dtypes, shape, device, optional: bool = False):
+    """Checks an argument of the functions that take them as they come:
+    type, shape, contiguity, and the device of the call."""
+    if t is None and optional:
+        return
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a tensor of {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _call(fn, where: str, device: torch.device, stream, outs, *args):
+    """Calls an entry point on `stream` (default: the current one) with
+    `device` current; tensors allocated for the call are recorded on a stream
+    of the caller's."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
+    if device.index != (_current_device or torch.cuda.current_device)():
+        with torch.cuda.device(device):
+            return _call(fn, where, device, stream, outs, *args)
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
+        for t in outs:
+            t.record_stream(stream)
+    st = fn(*args, _stream(stream))
+    if st != MOE_OK:
+        _check(st, where)
+
+
+_LOGITS = (torch.float32, torch.bfloat16)
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _matrix(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-dimensional tensor")
+    return t.shape
+
+
+def _out(t, name: str, dtype, shape, device, new: list):
+    """The caller's output tensor after its checks, or a new one (noted in
+    `new`)."""
+    if t is not None:
+        _tensor(t, name, (dtype,), shape, device)
+        return t
+    t = torch.empty(shape, dtype=dtype, device=device)
+    new.append(t)
+    return t
+
+
+def _route_biased(router_logits, score_bias, top_k, routing_method, renormalize, k_group,
+                  group_count, group_select_mode, routed_scaling_factor, topk_weights, topk_ids,
+                  stream):
+    M, E = _matrix(router_logits, "router_logits")
+    dev = router_logits.device
+    _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
+    _tensor(score_bias, "score_bias", _F32, (E,), dev)
+    new = []
+    topk_weights = _out(topk_weights, "topk_weights", torch.float32, (M, top_k), dev, new)
+    topk_ids = _out(topk_ids, "topk_ids", torch.int32, (M, top_k), dev, new)
+    _call(lib().moe_route_biased, "moe_route_biased", dev, stream, new, router_logits.data_ptr(),
+          int(router_logits.dtype == torch.bfloat16), score_bias.data_ptr(), M, E, top_k,
+          ROUTING[routing_method], int(bool(renormalize)), k_group, group_count,
+          group_select_mode, float(routed_scaling_factor), topk_weights.data_ptr(),
+          topk_ids.data_ptr())
+    return topk_weights, topk_ids
+
+
+def moe_route_backward(grad_weights: torch.Tensor, router_logits: torch.Tensor,
+                       topk_ids: torch.Tensor, routing_method: str = "softmax",
+                       renormalize: bool = False, routed_scaling_factor: float = 1.0,
+                       grad_logits: Optional[torch.Tensor] = None,
+                       error_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_route's weights: grad_weights fp32 [M, k] for the
+    experts topk_ids int32 [M, k] -> grad_logits [M, E] in the logits' type.
+    The choice of experts is held fixed.  error_word: int32 [1], set where an
+    id is outside [0, E) (such items take no part)."""
+    M, E = _matrix(router_logits, "router_logits")
+    k = _matrix(topk_ids, "topk_ids")[1]
+    dev = router_logits.device
+    _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
+    _tensor(topk_ids, "topk_ids", _I32, (M, k), dev)
+    _tensor(grad_weights, "grad_weights", _F32, (M, k), dev)
+    _tensor(error_word, "error_word", _I32, (1,), dev, optional=True)
+    new = []
+    grad_logits = _out(grad_logits, "grad_logits", router_logits.dtype, (M, E), dev, new)
+    _call(lib().moe_route_backward, "moe_route_backward", dev, stream, new,
+          grad_weights.data_ptr(), router_logits.data_ptr(),
+          int(router_logits.dtype == torch.bfloat16), topk_ids.data_ptr(), M, E, k,
+          ROUTING[routing_method], int(bool(renormalize)), float(routed_scaling_factor),
+          grad_logits.data_ptr(), None if error_word is None else error_word.data_ptr())
+    return grad_logits
 
 
 def moe_router_logits(hidden: torch.Tensor, w_gate: torch.Tensor,
@@ -241,6 +351,87 @@ def moe_quant_rows_fp8(x: torch.Tensor, q8: Optional[torch.Tensor] = None,
     return q8, scale
 
 
+FP8_BLOCK = 128
+
+
+def moe_quant_groups_fp8(x: torch.Tensor, swiglu: bool = False,
+                         q8: Optional[torch.Tensor] = None,
+                         scale: Optional[torch.Tensor] = None, stream=None):
+    """E4M3 quantisation of x bf16 [M, K] with a scale per row and group of
+    128 columns -> (codes [M, K] torch.float8_e4m3fn, scale fp32
+    [M, ceil(K/128)]).  swiglu: x is [M, 2K], and SiLU(x[:, :K]) * x[:, K:]
+    is what is quantised."""
+    M, cols = _matrix(x, "x")
+    dev = x.device
+    _tensor(x, "x", _BF16, (M, cols), dev)
+    if swiglu and cols % 2:
+        raise ValueError("swiglu needs an even number of columns")
+    K = cols // 2 if swiglu else cols
+    new = []
+    if q8 is None or q8.dtype != torch.uint8:
+        q8 = _out(q8, "q8", torch.float8_e4m3fn, (M, K), dev, new)
+    else:
+        _tensor(q8, "q8", _FP8, (M, K), dev)
+    scale = _out(scale, "scale", torch.float32, (M, -(-K // FP8_BLOCK)), dev, new)
+    _call(lib().moe_quant_groups_fp8, "moe_quant_groups_fp8", dev, stream, new, x.data_ptr(), M, K,
+          int(bool(swiglu)), q8.data_ptr(), scale.data_ptr())
+    return q8, scale
+
+
+def moe_matmul_fp8(a_q: torch.Tensor, a_scale: torch.Tensor, w_q: torch.Tensor,
+                   w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   transposed: bool = False, out_dtype: torch.dtype = torch.bfloat16,
+                   out: Optional[torch.Tensor] = None,
+                   error_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Dense product of E4M3 matrices with block scales -> [M, N] in out_dtype
+    (bf16 or fp32; `out` decides where given).  a_q [M, K] with a_scale fp32
+    [M, ceil(K/128)] (moe_quant_groups_fp8); w_q [K, N] with w_scale fp32
+    [ceil(K/128), ceil(N/128)], or transposed: w_q [N, K] with
+    [ceil(N/128), ceil(K/128)].  bias bf16 [N]."""
+    M, K = _matrix(a_q, "a_q")
+    rows, cols = _matrix(w_q, "w_q")
+    N = rows if transposed else cols
+    dev = a_q.device
+    KB, NB = -(-K // FP8_BLOCK), -(-N // FP8_BLOCK)
+    _tensor(a_q, "a_q", _FP8, (M, K), dev)
+    _tensor(a_scale, "a_scale", _F32, (M, KB), dev)
+    _tensor(w_q, "w_q", _FP8, (N, K) if transposed else (K, N), dev)
+    _tensor(w_scale, "w_scale", _F32, (NB, KB) if transposed else (KB, NB), dev)
+    _tensor(bias, "bias", _BF16, (N,), dev, optional=True)
+    _tensor(error_word, "error_word", _I32, (1,), dev, optional=True)
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _LOGITS:
+        raise ValueError("the output is torch.bfloat16 or torch.float32")
+    new = []
+    out = _out(out, "out", out_dtype, (M, N), dev, new)
+    _call(lib().moe_matmul_fp8, "moe_matmul_fp8", dev, stream, new, a_q.data_ptr(),
+          a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), int(bool(transposed)),
+          None if bias is None else bias.data_ptr(), M, K, N, int(out_dtype == torch.float32),
+          out.data_ptr(), None if error_word is None else error_word.data_ptr())
+    return out
+
+
+def moe_shared_expert_fp8(hidden: torch.Tensor, w13_q: torch.Tensor, w2_q: torch.Tensor,
+                          w13_scale: torch.Tensor, w2_scale: torch.Tensor,
+                          w13_bias: Optional[torch.Tensor] = None,
+                          w2_bias: Optional[torch.Tensor] = None, transposed: bool = False,
+                          out: Optional[torch.Tensor] = None,
+                          error_word: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """A SwiGLU expert that every token takes, in FP8 with block scales:
+    hidden bf16 [M, H] -> [M, H] bf16.  w13_q [H, 2I] and w2_q [I, H], the
+    experts' orientation of moe_forward_fp8 without E (transposed: [2I, H] and
+    [H, I]), with scales per 128 x 128 block.  hidden is quantised, multiplied,
+    SiLU(gate) * up quantised, and multiplied again."""
+    x_q, x_s = moe_quant_groups_fp8(hidden, stream=stream)
+    h = moe_matmul_fp8(x_q, x_s, w13_q, w13_scale, w13_bias, transposed, error_word=error_word,
+                       stream=stream)
+    z_q, z_s = moe_quant_groups_fp8(h, swiglu=True, stream=stream)
+    return moe_matmul_fp8(z_q, z_s, w2_q, w2_scale, w2_bias, transposed, out=out,
+                          error_word=error_word, stream=stream)
+
+
 WQ_FORMATS = {"int4": 0, "int8": 1, "mxfp4": 2, "mxfp6_e3m2": 3, "mxfp6_e2m3": 4}
 
 
@@ -366,10 +557,12 @@ def fused_moe(hidden: torch.Tensor, router_logits: torch.Tensor, w13: torch.Tens
               w2: torch.Tensor, top_k: int, w13_bias=None, w2_bias=None, k_group: int = 1,
               group_count: int = 1, group_select_mode: int = 0, routing_method: str = "softmax",
               renormalize: bool = False, routed_scaling_factor: float = 1.0, workspace=None,
-              out=None, stream=None):
-    """The whole layer: route, then forward (the MindIE-SD `fused_moe` shape)."""
+              out=None, stream=None, score_bias=None):
+    """The whole layer: route, then forward (the MindIE-SD `fused_moe` shape).
+    score_bias: as moe_route."""
     w, ids = moe_route(router_logits, top_k, routing_method, renormalize, k_group, group_count,
-                       group_select_mode, routed_scaling_factor, stream=stream)
+                       group_select_mode, routed_scaling_factor, stream=stream,
+                       score_bias=score_bias)
     return moe_forward(hidden, w, ids, w13, w2, w13_bias, w2_bias, workspace, out, stream=stream)
 
 
@@ -377,13 +570,14 @@ def moe_layer(hidden: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2:
               top_k: int, b_gate=None, w13_bias=None, w2_bias=None, k_group: int = 1,
               group_count: int = 1, group_select_mode: int = 0,
               routing_method: str = "softmax", renormalize: bool = False,
-              routed_scaling_factor: float = 1.0, workspace=None, out=None, stream=None):
-    """The layer from the hidden states: router logits (x W_g + b_g), routing,
-    then the expert forward."""
+              routed_scaling_factor: float = 1.0, workspace=None, out=None, stream=None,
+              score_bias=None):
+    """The layer from the hidden states: router logits (x W_g + b_g), routing
+    (score_bias: as moe_route), then the expert forward."""
     logits = moe_router_logits(hidden, w_gate, b_gate, stream=stream)
     return fused_moe(hidden, logits, w13, w2, top_k, w13_bias, w2_bias, k_group, group_count,
                      group_select_mode, routing_method, renormalize, routed_scaling_factor,
-                     workspace, out, stream)
+                     workspace, out, stream, score_bias)
 
 
 def workspace_error_word(workspace: torch.Tensor) -> int:
@@ -485,7 +679,8 @@ def profiler_stop():
     return {arr[i].name.decode(): (arr[i].launches, arr[i].total_ms) for i in range(n.value)}
 
 
-__all__ = ["moe_route", "moe_router_logits", "moe_layer", "moe_align", "moe_forward",
+__all__ = ["moe_route", "moe_route_backward", "moe_quant_groups_fp8", "moe_matmul_fp8",
+           "moe_shared_expert_fp8", "moe_router_logits", "moe_layer", "moe_align", "moe_forward",
            "moe_forward_host", "HostStaging", "set_gather_mode", "set_pdl", "set_wq_decode",
            "set_item_rows", "set_host_out_direct", "set_small_path",
            "moe_forward_batched", "moe_forward_fp8", "workspace_size_fp8", "moe_quant_rows_fp8",

@@ -58,6 +58,13 @@ SIGNATURES = {
                           c_vp, c_vp, c_vp]),
     "moe_route_bf16": (c_i32, [c_vp, c_i64, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32,
                                c_f32, c_vp, c_vp, c_vp]),
+    "moe_route_biased": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32, c_i32, c_i32,
+                                 c_i32, c_i32, c_f32, c_vp, c_vp, c_vp]),
+    "moe_route_backward": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32, c_i32,
+                                   c_f32, c_vp, c_vp, c_vp]),
+    "moe_quant_groups_fp8": (c_i32, [c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "moe_matmul_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32,
+                               c_vp, c_vp, c_vp]),
     "moe_router_logits": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp]),
     "moe_forward_opts": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp,
                                  c_vp, c_vp, c_vp, c_sz, ctypes.POINTER(ForwardOpts), c_vp,

@@ -142,6 +142,7 @@ moe_status_t check_device(int* num_sms) {
   return MOE_OK;
 }
 
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr size_t kRegionAlign = 1024;
@@ -369,6 +370,60 @@ moe_status_t moe_route_bf16(const void* router_logits, int64_t M, int32_t E, int
   return route_impl(router_logits, 1, M, E, top_k, routing_method, renormalize, k_group,
                     group_count, group_select_mode, routed_scaling_factor, topk_weights,
                     topk_ids, stream);
+}
+
+moe_status_t moe_route_biased(const void* router_logits, int32_t logits_bf16,
+                              const float* score_bias, int64_t M, int32_t E, int32_t top_k,
+                              int32_t routing_method, int32_t renormalize, int32_t k_group,
+                              int32_t group_count, int32_t group_select_mode,
+                              float routed_scaling_factor, float* topk_weights,
+                              int32_t* topk_ids, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (moe_status_t st = route_check(M, E, top_k, routing_method, k_group, group_count,
+                                    group_select_mode, routed_scaling_factor))
+    return st;
+  if (logits_bf16 != 0 && logits_bf16 != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "logits_bf16=%d", logits_bf16);
+  if (M >= (int64_t(1) << 31)) return set_error(MOE_ERR_INVALID_ARG, "M too large");
+  if (M == 0) return MOE_OK;
+  if (!router_logits || !score_bias || !topk_weights || !topk_ids)
+    return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned_to(router_logits, logits_bf16 ? 2 : 4) || !aligned_to(score_bias, 4) ||
+      !aligned_to(topk_weights, 4) || !aligned_to(topk_ids, 4))
+    return set_error(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
+  if (moe_status_t st = check_device(nullptr)) return st;
+  RouteArgs a{router_logits, M, E, top_k, routing_method, renormalize ? 1 : 0, k_group,
+              group_count, group_select_mode, routed_scaling_factor, topk_weights, topk_ids,
+              logits_bf16};
+  return launch_route_biased(a, score_bias, stream);
+}
+
+moe_status_t moe_route_backward(const float* grad_weights, const void* router_logits,
+                                int32_t logits_bf16, const int32_t* topk_ids, int64_t M,
+                                int32_t E, int32_t top_k, int32_t routing_method,
+                                int32_t renormalize, float routed_scaling_factor,
+                                void* grad_logits, int32_t* error_word, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (M >= 0 && (top_k < 1 || top_k > 64))
+    return set_error(MOE_ERR_INVALID_ARG, "top_k=%d outside [1, 64]", top_k);
+  // a token may name an expert twice, so top_k is not bounded by E here
+  if (moe_status_t st = route_check(M, E, 1, routing_method, 1, 1, 0, routed_scaling_factor))
+    return st;
+  if (logits_bf16 != 0 && logits_bf16 != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "logits_bf16=%d", logits_bf16);
+  if (M >= (int64_t(1) << 31)) return set_error(MOE_ERR_INVALID_ARG, "M too large");
+  if (M == 0) return MOE_OK;
+  if (!grad_weights || !router_logits || !topk_ids || !grad_logits)
+    return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  const int eb = logits_bf16 ? 2 : 4;
+  if (!aligned_to(grad_weights, 4) || !aligned_to(router_logits, eb) || !aligned_to(topk_ids, 4) ||
+      !aligned_to(grad_logits, eb) || !aligned_to(error_word, 4))
+    return set_error(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
+  if (moe_status_t st = check_device(nullptr)) return st;
+  RouteBackwardArgs a{grad_weights, router_logits, logits_bf16, topk_ids, M, E, top_k,
+                      routing_method, renormalize ? 1 : 0, routed_scaling_factor, grad_logits,
+                      error_word};
+  return launch_route_backward(a, stream);
 }
 
 // ---------------------------------------------------------- router GEMM --
@@ -1051,6 +1106,51 @@ moe_status_t moe_quant_rows_fp8(const void* x, int64_t M, int32_t H, void* q8, f
   QuantTokensArgs qa{static_cast<const bf16*>(x), nullptr, M, 1, H, static_cast<uint8_t*>(q8),
                      scale, nullptr};
   return launch_quant_tokens_fp8(qa, stream);
+}
+
+// --------------------------------------------------------- dense FP8 --
+moe_status_t moe_quant_groups_fp8(const void* x, int64_t M, int32_t K, int32_t swiglu, void* q8,
+                                  float* scale, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (M < 0 || M >= (int64_t(1) << 31)) return set_error(MOE_ERR_INVALID_ARG, "M=%lld", (long long)M);
+  if (K < 16 || K % 16 != 0 || K > (1 << 24))
+    return set_error(MOE_ERR_INVALID_ARG, "K=%d not a positive multiple of 16 up to 2^24", K);
+  if (swiglu != 0 && swiglu != 1) return set_error(MOE_ERR_INVALID_ARG, "swiglu=%d", swiglu);
+  if (M == 0) return MOE_OK;
+  if (!x || !q8 || !scale) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(q8) || !aligned_to(scale, 4))
+    return set_error(MOE_ERR_INVALID_ARG, "x and q8 must be 16-byte aligned");
+  if (moe_status_t st = check_device(nullptr)) return st;
+  const QuantGroupsArgs a{static_cast<const bf16*>(x), M, K, swiglu, static_cast<uint8_t*>(q8),
+                          scale};
+  return launch_quant_groups_fp8(a, stream);
+}
+
+moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const void* w,
+                            const float* w_scale, int32_t w_transposed, const void* bias,
+                            int64_t M, int32_t K, int32_t N, int32_t out_f32, void* out,
+                            int32_t* error_word, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (M < 0 || M >= (int64_t(1) << 31)) return set_error(MOE_ERR_INVALID_ARG, "M=%lld", (long long)M);
+  if (K < 16 || K % 16 != 0 || K > (1 << 24))
+    return set_error(MOE_ERR_INVALID_ARG, "K=%d not a positive multiple of 16 up to 2^24", K);
+  if (N < 16 || N % 16 != 0 || N > (1 << 22))
+    return set_error(MOE_ERR_INVALID_ARG, "N=%d not a positive multiple of 16 up to 2^22", N);
+  if (w_transposed != 0 && w_transposed != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "w_transposed=%d", w_transposed);
+  if (out_f32 != 0 && out_f32 != 1) return set_error(MOE_ERR_INVALID_ARG, "out_f32=%d", out_f32);
+  if (M == 0) return MOE_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out) || (bias && !aligned16(bias)) ||
+      !aligned_to(a_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(error_word, 4))
+    return set_error(MOE_ERR_INVALID_ARG,
+                     "a, w, bias and out must be 16-byte aligned, scales to 4 bytes");
+  int sms = 0;
+  if (moe_status_t st = check_device(&sms)) return st;
+  const MatmulFp8Args g{static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(w),
+                        w_scale, static_cast<const bf16*>(bias), M, K, N, w_transposed, out_f32,
+                        out, error_word, sms};
+  return launch_matmul_fp8(g, stream);
 }
 
 // ------------------------------------------- weight-only quantised --

@@ -119,6 +119,47 @@ struct RouteArgs {
   int32_t logits_bf16 = 0;
 };
 moe_status_t launch_route(const RouteArgs& a, cudaStream_t s);
+// The same with a bias fp32 [E] added to the scores for the choice of
+// experts only (route_bias.cu), and the gradient of the weights.
+moe_status_t launch_route_biased(const RouteArgs& a, const float* bias, cudaStream_t s);
+struct RouteBackwardArgs {
+  const float* grad_weights;  // [M, k]
+  const void* logits;         // fp32 or bf16 [M, E]
+  int32_t logits_bf16;
+  const int32_t* ids;         // [M, k]
+  int64_t M;
+  int32_t E, top_k, method, renormalize;
+  float scale;
+  void* grad_logits;          // [M, E], the logits' type
+  int32_t* error_word;
+};
+moe_status_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s);
+
+// Dense FP8 (fp8_dense.cu): quantisation per (row, group of 128 columns),
+// scales [M, ceil(K/128)]; swiglu: of SiLU(x[:, :K]) * x[:, K:].
+struct QuantGroupsArgs {
+  const bf16* x;  // [M, K], or [M, 2K] for swiglu
+  int64_t M;
+  int32_t K, swiglu;
+  uint8_t* q8;    // [M, K]
+  float* scale;   // [M, ceil(K/128)]
+};
+moe_status_t launch_quant_groups_fp8(const QuantGroupsArgs& a, cudaStream_t s);
+// out [M, N] = block-scaled a [M, K] times w, w [K, N] with scales
+// [ceil(K/128), ceil(N/128)], or transposed: [N, K] and [ceil(N/128), ceil(K/128)].
+struct MatmulFp8Args {
+  const uint8_t* a;
+  const float* a_scale;  // [M, ceil(K/128)]
+  const uint8_t* w;
+  const float* w_scale;
+  const bf16* bias;      // [N] or null
+  int64_t M;
+  int32_t K, N, transposed, out_f32;
+  void* out;             // bf16 or fp32 [M, N]
+  int32_t* error_word;
+  int32_t num_sms;
+};
+moe_status_t launch_matmul_fp8(const MatmulFp8Args& a, cudaStream_t s);
 
 struct AlignArgs {
   const int32_t* ids;   // [R] expert id per item

@@ -1,0 +1,397 @@
+"""GPU parity of the routing with a bias (ids equal to the 64-bit oracle's,
+weights within fp32 rounding) and of the routing gradient."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_softmax_gb300 as pkg
+import oracle
+from mixture_experts_ffn_softmax_gb300 import workloads as wl
+
+from helpers import check_out
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24     # half a step of fp32, relative
+
+
+def weight_rtol(logits, E):
+    """Relative error of a weight: expf within 2 U32 of its argument's value
+    and its argument l - max rounded (|l - max| U32), twice (numerator and
+    sum); the sums of at most E / 32 + 5 positive terms per path; the
+    division, the scale and the reciprocal forms, 8 roundings at most."""
+    fin = np.where(np.abs(logits) < 1e30, logits, 0.0)   # masked ones take no part
+    return (2 * (2 + np.abs(fin).max() * 2) + E / 32 + 6 + 8) * U32
+
+
+def check_biased(logits, bias, a):
+    w, ids = pkg.moe_route(logits, a["k"], a["method"], a["renorm"], a["kg"], a["G"], a["mode"],
+                           a["scale"], score_bias=bias)
+    torch.cuda.synchronize()
+    l = logits.double().cpu().numpy()
+    rw, rids = oracle.route_biased(l, bias.double().cpu().numpy(), a["k"], a["method"],
+                                   a["renorm"], a["kg"], a["G"], a["mode"], a["scale"])
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    err = np.abs(w.cpu().double().numpy() - rw)
+    # 1e-44: weights below the smallest fp32 numbers
+    assert (err <= weight_rtol(l, l.shape[1]) * np.abs(rw) + 1e-44).all(), err.max()
+    return w, ids
+
+
+def args(k=2, method="softmax", renorm=False, kg=1, G=1, mode=0, scale=1.0):
+    return dict(k=k, method=method, renorm=renorm, kg=kg, G=G, mode=mode, scale=scale)
+
+
+CASES = [
+    # (M, E, args)
+    (1, 1, args(1)),
+    (3, 3, args(2, "sigmoid", scale=2.5)),
+    (5, 7, args(7, "softmax", True)),
+    (1, 8, args(2, "softmax", True)),
+    (129, 8, args(2, "softmax", True)),
+    (33, 16, args(4, "sigmoid")),
+    (65, 24, args(3, "softmax", False, 2, 3, 1)),
+    (31, 32, args(8, "softmax", False, 3, 4, 1, 0.5)),
+    (17, 33, args(5, "sigmoid")),
+    (40, 60, args(6, "sigmoid", True, 2, 5, 1)),
+    (64, 64, args(64, "softmax", True)),
+    (64, 64, args(33, "sigmoid")),
+    (37, 96, args(6, "softmax", True, 2, 3)),
+    (50, 128, args(8, "softmax", False)),
+    (51, 128, args(8, "sigmoid", True, 4, 16, 1)),
+    (70, 160, args(7, "sigmoid", False, 3, 5, 1, 2.5)),
+    (1, 256, args(8, "sigmoid", True, 4, 8, 1, 2.5)),
+    (300, 256, args(8, "sigmoid", True, 4, 8, 1, 2.5)),
+    (300, 256, args(8, "softmax", True, 4, 8, 0, 2.5)),
+    (40, 256, args(16, "sigmoid", True, 1, 16, 0)),
+    (21, 384, args(6, "sigmoid", True, 1, 1, 0)),
+    (20, 512, args(16, "sigmoid", True, 2, 64, 1)),
+    (20, 512, args(64, "softmax", False, 128, 256, 1)),
+    (9, 1000, args(20, "softmax", True, 4, 10, 1)),
+    (9, 1024, args(33, "softmax", True)),
+    (9, 1024, args(8, "sigmoid", False, 5, 16, 0, 3.0)),
+    (7, 1024, args(64, "sigmoid", False, 512, 1024, 0)),
+]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("M,E,a", CASES)
+def test_route_biased(M, E, a, dtype):
+    g = torch.Generator(device="cuda").manual_seed(M * 1031 + E)
+    logits = torch.randn(M, E, generator=g, device="cuda").to(getattr(torch, dtype))
+    bias = torch.randn(E, generator=g, device="cuda") * (0.1 if a["method"] == "sigmoid" else
+                                                         1.0 / E)
+    check_biased(logits, bias, a)
+
+
+@pytest.mark.parametrize("method,spread", [("sigmoid", 0.02), ("softmax", 0.0005)])
+def test_route_biased_many_tokens(method, spread):
+    """Enough tokens that neighbouring scores closer than fp32 rounding occur
+    by chance."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    logits = torch.randn(4096, 256, generator=g, device="cuda")
+    bias = torch.randn(256, generator=g, device="cuda") * spread
+    check_biased(logits, bias, args(8, method, True, 4, 8, 1, 2.5))
+
+
+@pytest.mark.parametrize("method", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("kg,G,mode", [(1, 1, 0), (2, 4, 1), (3, 8, 0)])
+def test_route_biased_ties_and_near_ties(method, kg, G, mode):
+    """Exact ties (equal logits and biases), ties of the fp32 scores whose
+    64-bit values differ, and saturated scores that agree in 64 bits too."""
+    E, k = 64, 8
+    rng = np.random.default_rng(3)
+    rows = [np.zeros(E), rng.integers(-1, 2, E).astype(float),
+            1.0 + rng.integers(0, 4, E) * 2.0 ** -23,         # neighbouring fp32 logits
+            rng.permutation(E) * 2.0 ** -22 + 2.0,
+            20.0 + rng.integers(0, 3, E),                     # sigmoid rounds to 1 in fp32
+            50.0 + rng.integers(0, 3, E),                     # and in 64 bits
+            -rng.integers(90, 120, E).astype(float), -700.0 - rng.integers(0, 40, E)]
+    logits = torch.tensor(np.stack(rows * 3), dtype=torch.float32, device="cuda")
+    for bias in (np.zeros(E), rng.integers(0, 2, E) * 0.5, rng.integers(0, 2, E) * 2.0 ** -25):
+        b = torch.tensor(bias, dtype=torch.float32, device="cuda")
+        check_biased(logits, b, args(k, method, True, kg, G, mode))
+        if method == "softmax":
+            check_biased(logits, b, args(k, method, False, kg, G, mode))
+
+
+@pytest.mark.parametrize("E,kg,G,mode", [(16, 1, 1, 0), (64, 2, 4, 1), (256, 4, 8, 1), (96, 1, 3, 0)])
+@pytest.mark.parametrize("method,renorm", [("sigmoid", True), ("softmax", True), ("softmax", False)])
+def test_route_biased_masked_experts(E, kg, G, mode, method, renorm):
+    """Masked experts (-inf, and the type's lowest value) in all numbers up to
+    every expert of the row, with biases that would otherwise choose them."""
+    rng = np.random.default_rng(E)
+    k = 6
+    logits = rng.normal(size=(40, E)).astype(np.float32)
+    for t in range(40):
+        out = rng.permutation(E)[:[0, E // 2, E - 7, E - 2, E][t % 5]]
+        logits[t, out] = -np.inf if t % 2 else np.finfo(np.float32).min
+    logits[38] = -np.inf
+    bias = torch.tensor(rng.normal(size=E), dtype=torch.float32, device="cuda")
+    check_biased(torch.tensor(logits, device="cuda"), bias, args(k, method, renorm, kg, G, mode))
+
+
+@pytest.mark.parametrize("method", ["sigmoid", "softmax"])
+def test_route_biased_non_finite_scores(method):
+    """Whatever the logits hold, ids are valid and distinct; other tokens keep
+    their results; a NaN is chosen last."""
+    E, k = 64, 8
+    g = torch.Generator(device="cuda").manual_seed(9)
+    logits = torch.randn(12, E, generator=g, device="cuda")
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1
+    w0, i0 = pkg.moe_route(logits, k, method, True, 2, 4, 1, score_bias=bias)
+    bad = logits.clone()
+    bad[1, 5] = float("nan")
+    bad[3] = float("nan")
+    bad[5, 60] = float("inf")
+    bad[7] = float("inf")
+    w, ids = pkg.moe_route(bad, k, method, True, 2, 4, 1, score_bias=bias)
+    for t in range(12):
+        r = ids[t].tolist()
+        assert len(set(r)) == k and all(0 <= e < E for e in r)
+        if t not in (1, 3, 5, 7):
+            assert torch.equal(w[t], w0[t]) and torch.equal(ids[t], i0[t])
+    if method == "sigmoid":
+        assert 5 not in ids[1].tolist() and torch.isfinite(w[1]).all()
+        assert torch.isnan(w[3]).all()
+        assert torch.isfinite(w[5]).all() and torch.isfinite(w[7]).all()
+    else:
+        assert torch.isnan(w[[1, 3, 5, 7]]).any(1).all()
+
+
+def test_route_biased_empty_and_untouched_rows():
+    bias = torch.zeros(16, device="cuda")
+    w, ids = pkg.moe_route(torch.zeros(0, 16, device="cuda"), 4, score_bias=bias)
+    assert w.shape == (0, 4) and ids.shape == (0, 4)
+    # views of a larger buffer (element-aligned only): the rows around stay
+    for M, E, k in ((3, 15, 3), (5, 33, 5), (2, 256, 7)):
+        for dt in (torch.float32, torch.bfloat16):
+            buf = torch.randn((M + 2) * E + 1, device="cuda").to(dt)
+            logits = buf[E + 1:E + 1 + M * E].view(M, E)
+            W = torch.full(((M + 2) * k,), -5.0, device="cuda")
+            I = torch.full(((M + 2) * k,), -5, dtype=torch.int32, device="cuda")
+            b = torch.randn(E + 1, device="cuda")[1:] * 0.1
+            pkg.moe_route(logits, k, "sigmoid", topk_weights=W[k:k + M * k].view(M, k),
+                          topk_ids=I[k:k + M * k].view(M, k), score_bias=b)
+            w, ids = check_biased(logits.contiguous().clone(), b.clone(), args(k, "sigmoid"))
+            assert torch.equal(W[k:-k].view(M, k), w) and torch.equal(I[k:-k].view(M, k), ids)
+            assert (W[:k] == -5).all() and (W[-k:] == -5).all()
+            assert (I[:k] == -5).all() and (I[-k:] == -5).all()
+
+
+def test_route_biased_zero_bias_is_the_plain_route():
+    spec = wl.SMALL_SPECS["deepseek_small"]
+    d = wl.make_moe_inputs(spec, device="cuda", weights=False)
+    a = (spec.top_k, spec.routing_method, spec.renormalize, spec.k_group, spec.group_count,
+         spec.group_select_mode, spec.routed_scaling_factor)
+    w0, i0 = pkg.moe_route(d["router_logits"], *a)
+    w, i = pkg.moe_route(d["router_logits"], *a,
+                         score_bias=torch.zeros(spec.E, device="cuda"))
+    assert torch.equal(i, i0)
+    assert (w - w0).abs().max() <= 1e-5
+
+
+# ------------------------------------------------------------- gradient --
+BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
+        (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
+
+
+def check_backward(gw, logits, ids, method, renorm, scale):
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = pkg.moe_route_backward(gw, logits, ids, method, renorm, scale, error_word=err)
+    torch.cuda.synchronize()
+    assert got.dtype == logits.dtype and err.item() == 0
+    l = logits.double().cpu().numpy()
+    ref = oracle.route_backward(gw.double().cpu().numpy(), l, ids.cpu().numpy(), method, renorm,
+                                scale)
+    # one rounding of the result; before it, terms of at most
+    # scale * max|gw| * (1 + k) with the relative error of a weight each
+    out = (2.0 ** -8 if logits.dtype == torch.bfloat16 else U32)
+    size = scale * gw.abs().max().item() * (1 + ids.shape[1])
+    tol = out * np.abs(ref) + 2 * weight_rtol(l, l.shape[1]) * size
+    diff = np.abs(got.double().cpu().numpy() - ref)
+    assert (diff <= tol).all(), (diff - tol).max()
+    return got, ref
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("method,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+@pytest.mark.parametrize("M,E,k", BACK)
+def test_route_backward(M, E, k, method, renorm, dtype):
+    g = torch.Generator(device="cuda").manual_seed(M + E)
+    logits = torch.randn(M, E, generator=g, device="cuda").to(getattr(torch, dtype))
+    ids = torch.argsort(torch.rand(M, E, generator=g, device="cuda"), 1)[:, :k].int().contiguous()
+    gw = torch.randn(M, k, generator=g, device="cuda")
+    got, ref = check_backward(gw, logits, ids, method, renorm, 1.5)
+    if dtype == "float32" and k > 1:
+        # and as a whole, to the accuracy of its terms
+        n = np.linalg.norm(ref)
+        assert np.linalg.norm(got.double().cpu().numpy() - ref) <= 1e-5 * max(n, 1e-30)
+
+
+@pytest.mark.parametrize("method,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+def test_route_backward_by_differences(method, renorm):
+    """Against differences of the routing itself: the loss sum(gw * w) of
+    moe_route's weights when one logit moves by h (choice unchanged).  The
+    weights are within weight_rtol, so the quotient's error is at most
+    2 k |gw| rtol / (2 h) + O(h^2)."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    M, E, k, h = 6, 12, 3, 2.0 ** -6
+    logits = torch.randn(M, E, generator=g, device="cuda") * 2
+    bias = torch.randn(E, generator=g, device="cuda") * 0.01
+    _, ids = pkg.moe_route(logits, k, method, renorm, score_bias=bias)
+    gw = torch.randn(M, k, generator=g, device="cuda")
+    got = pkg.moe_route_backward(gw, logits, ids, method, renorm)
+    steps = []
+    for e in range(E):
+        loss = []
+        for s in (h, -h):
+            l = logits.clone()
+            l[:, e] += s
+            w, i = pkg.moe_route(l, k, method, renorm, score_bias=bias)
+            # the weights in the order of the unmoved choice; rows whose choice moved are left out
+            same = (i.sort(1).values == ids.sort(1).values).all(1)
+            dense = torch.zeros(M, E, device="cuda").scatter_(1, i.long(), w)
+            loss.append(((gw * dense.gather(1, ids.long())).sum(1), same))
+        steps.append(((loss[0][0] - loss[1][0]) / (2 * h), loss[0][1] & loss[1][1]))
+    rtol = weight_rtol(logits.cpu().numpy(), E)
+    size = gw.abs().sum(1).max().item()
+    tol = size * rtol / h + size * h * h      # third derivatives of a weight are below 1 (1/6 used up to 6)
+    checked = 0
+    for e, (d, same) in enumerate(steps):
+        assert ((d - got[:, e]).abs()[same] <= tol).all()
+        checked += int(same.sum())
+    assert checked >= M * E // 2
+
+
+def test_route_backward_repeated_ids_and_bad_ids():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    M, E, k = 40, 24, 6
+    logits = torch.randn(M, E, generator=g, device="cuda")
+    gw = torch.randn(M, k, generator=g, device="cuda")
+    ids = torch.randint(0, 4, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    for method, renorm in (("softmax", False), ("softmax", True), ("sigmoid", True)):
+        check_backward(gw, logits, ids, method, renorm, 2.0)
+        bad = ids.clone()
+        bad[3, 1], bad[5] = -1, E
+        bad[7, 0] = 2 ** 31 - 1
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = pkg.moe_route_backward(gw, logits, bad, method, renorm, 2.0, error_word=err)
+        ref = oracle.route_backward(gw.double().cpu().numpy(), logits.double().cpu().numpy(),
+                                    bad.cpu().numpy(), method, renorm, 2.0)
+        np.testing.assert_allclose(out.cpu().numpy(), ref, atol=1e-4)
+        assert err.item() == 4 and (out[5] == 0).all()
+
+
+def test_route_backward_masked_and_extreme_logits():
+    g = torch.Generator(device="cuda").manual_seed(4)
+    M, E, k = 8, 32, 4
+    logits = torch.randn(M, E, generator=g, device="cuda")
+    logits[0] = float("-inf")
+    logits[1, ::2] = float("-inf")
+    logits[2] = -300.0 + logits[2]
+    logits[3] = 200.0 + logits[3]
+    logits[4] = torch.finfo(torch.float32).min
+    gw = torch.randn(M, k, generator=g, device="cuda")
+    ids = torch.arange(k, dtype=torch.int32, device="cuda").repeat(M, 1)
+    for method, renorm in (("softmax", False), ("softmax", True), ("sigmoid", True)):
+        out = pkg.moe_route_backward(gw, logits, ids, method, renorm)
+        assert torch.isfinite(out).all(), (method, renorm)
+        assert (out[0] == 0).all() and (out[1, ::2] == 0).all()
+        # softmax does not change when every logit moves
+        if method == "softmax":
+            moved = logits.clone()
+            moved[2] += 300.0
+            moved[3] -= 200.0
+            ref = oracle.route_backward(gw.double().cpu().numpy()[1:4],
+                                        logits.double().cpu().numpy()[1:4],
+                                        ids.cpu().numpy()[1:4], method, renorm)
+            np.testing.assert_allclose(out[1:4].cpu().numpy(), ref, atol=1e-5)
+        else:
+            # far below zero, sigmoid's ratios are the softmax's
+            ref = oracle.route_backward(gw.double().cpu().numpy()[2:3],
+                                        logits.double().cpu().numpy()[2:3],
+                                        ids.cpu().numpy()[2:3], "softmax", True)
+            np.testing.assert_allclose(out[2:3].cpu().numpy(), ref, atol=1e-5)
+
+
+def test_route_backward_views_and_empty():
+    assert pkg.moe_route_backward(torch.zeros(0, 2, device="cuda"), torch.zeros(0, 8, device="cuda"),
+                                  torch.zeros(0, 2, dtype=torch.int32, device="cuda")).shape == (0, 8)
+    for M, E, k in ((3, 15, 3), (5, 33, 5), (3, 256, 7)):
+        for dt in (torch.float32, torch.bfloat16):
+            buf = torch.randn((M + 2) * E + 1, device="cuda").to(dt)
+            logits = buf[E + 1:E + 1 + M * E].view(M, E)
+            out = torch.full(((M + 2) * E + 1,), -5.0, device="cuda", dtype=dt)
+            gw = torch.randn(M * k + 1, device="cuda")[1:].view(M, k)
+            ids = torch.argsort(torch.rand(M, E, device="cuda"), 1)[:, :k].int().contiguous()
+            pkg.moe_route_backward(gw, logits, ids, grad_logits=out[E + 1:E + 1 + M * E].view(M, E))
+            got, _ = check_backward(gw.clone(), logits.clone(), ids, "softmax", False, 1.0)
+            assert torch.equal(out[E + 1:E + 1 + M * E].view(M, E), got)
+            assert (out[:E + 1] == -5).all() and (out[E + 1 + M * E:] == -5).all()
+
+
+# ------------------------------------------------- streams, graphs, threads --
+def test_route_ops_on_other_streams_in_graphs_and_threads():
+    a = (8, "sigmoid", True, 4, 8, 1, 2.5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    logits = torch.randn(500, 256, generator=g, device="cuda")
+    bias = torch.randn(256, generator=g, device="cuda") * 0.05
+    gw = torch.randn(500, 8, generator=g, device="cuda")
+    w, ids = pkg.moe_route(logits, *a, score_bias=bias)
+    gl = pkg.moe_route_backward(gw, logits, ids, "sigmoid", True, 2.5)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    w2, ids2 = pkg.moe_route(logits, *a, score_bias=bias, stream=s)
+    gl2 = pkg.moe_route_backward(gw, logits, ids2, "sigmoid", True, 2.5, stream=s)
+    s.synchronize()
+    assert torch.equal(w, w2) and torch.equal(ids, ids2) and torch.equal(gl, gl2)
+    graph = torch.cuda.CUDAGraph()
+    static = torch.zeros_like(logits)
+    with torch.cuda.graph(graph):
+        w3, ids3 = pkg.moe_route(static, *a, score_bias=bias)
+        gl3 = pkg.moe_route_backward(gw, static, ids3, "sigmoid", True, 2.5)
+    for _ in range(2):
+        static.copy_(logits)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(w, w3) and torch.equal(ids, ids3) and torch.equal(gl, gl3)
+        static.zero_()
+    bad = []
+
+    def run():
+        st = torch.cuda.Stream()
+        for _ in range(20):
+            x = pkg.moe_route(logits, *a, score_bias=bias, stream=st)
+            y = pkg.moe_route_backward(gw, logits, x[1], "sigmoid", True, 2.5, stream=st)
+            st.synchronize()
+            if not (torch.equal(x[1], ids) and torch.equal(y, gl)):
+                bad.append(1)
+    ts = [threading.Thread(target=run) for _ in range(3)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad
+
+
+def test_layer_with_score_bias():
+    """The layer entry points route with the bias."""
+    spec = wl.SMALL_SPECS["deepseek_small"]
+    d = wl.make_moe_inputs(spec, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    bias = torch.randn(spec.E, generator=g, device="cuda") * 0.2
+    a = dict(k_group=spec.k_group, group_count=spec.group_count,
+             group_select_mode=spec.group_select_mode, routing_method=spec.routing_method,
+             renormalize=spec.renormalize, routed_scaling_factor=spec.routed_scaling_factor)
+    w_gate = torch.randn(spec.H, spec.E, generator=g, device="cuda").to(torch.bfloat16) * 0.1
+    y = pkg.moe_layer(d["hidden"], w_gate, d["w13"], d["w2"], spec.top_k, score_bias=bias, **a)
+    logits = pkg.moe_router_logits(d["hidden"], w_gate)
+    y2 = pkg.fused_moe(d["hidden"], logits, d["w13"], d["w2"], spec.top_k, score_bias=bias, **a)
+    assert torch.equal(y, y2)
+    rw, rids = oracle.route_biased(logits.double().cpu().numpy(), bias.double().cpu().numpy(),
+                                   spec.top_k, spec.routing_method, spec.renormalize, spec.k_group,
+                                   spec.group_count, spec.group_select_mode,
+                                   spec.routed_scaling_factor)
+    ref = oracle.forward(wl.to_f64(d["hidden"]), rw, rids, wl.to_f64(d["w13"]), wl.to_f64(d["w2"]))
+    check_out(y.double().cpu().numpy(), ref, "layer with score bias")
