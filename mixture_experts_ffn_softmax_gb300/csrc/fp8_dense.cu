@@ -8,6 +8,7 @@
 // The experts' GEMMs of that scheme are in gemm.cu; here the product is one
 // matrix's, for the linear layers beside the experts.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp8q.cuh"
@@ -78,108 +79,17 @@ __global__ void __launch_bounds__(kQgWarps * 32)
   }
 }
 
-__device__ __forceinline__ float e4m3_f32(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
 struct DenseParams {
-  const uint8_t* a;
   const float* a_scale;
-  const uint8_t* w;
   const float* w_scale;
   const bf16* bias;
   void* out;
   int64_t M;
-  int K, N, transposed, out_f32;
+  int K, N, out_f32;
   int32_t* error_word;
 };
 
-// 64 x 64 tile, 256 threads, 4 x 4 outputs each.
-__global__ void __launch_bounds__(256) dense_fp8_simt_kernel(DenseParams P) {
-  pdl_begin();
-  __shared__ float sa[16][65], sw[16][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int n0 = static_cast<int>(blockIdx.y) * 64;
-  const int KB = ceil_div(P.K, 128), NB = ceil_div(P.N, 128);
-  float acc[4][4] = {}, part[4][4] = {};
-  for (int k0 = 0; k0 < P.K; k0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      const int r = i >> 4, kk = i & 15;
-      const int64_t m = m0 + r;
-      sa[kk][r] = m < P.M ? e4m3_f32(P.a[m * P.K + k0 + kk]) : 0.f;
-      const int n = P.transposed ? r : i & 63, k = P.transposed ? kk : i >> 6;
-      float v = 0.f;
-      if (n0 + n < P.N)
-        v = e4m3_f32(P.transposed ? P.w[static_cast<int64_t>(n0 + n) * P.K + k0 + k]
-                                  : P.w[static_cast<int64_t>(k0 + k) * P.N + n0 + n]);
-      sw[k][n] = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          part[i][j] = fmaf(sa[kk][ty * 4 + i], sw[kk][tx * 4 + j], part[i][j]);
-    __syncthreads();
-    if ((k0 & 127) == 112 || k0 + 16 == P.K) {
-      const int b = k0 >> 7, nb = n0 >> 7;
-      const float ws = P.transposed ? P.w_scale[nb * KB + b] : P.w_scale[b * NB + nb];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty * 4 + i;
-        const float as = m < P.M ? P.a_scale[m * KB + b] : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[i][j] = fmaf(part[i][j], as * ws, acc[i][j]);
-          part[i][j] = 0.f;
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
-      if (m >= P.M || n >= P.N) continue;
-      const float v = acc[i][j] + (P.bias ? __bfloat162float(P.bias[n]) : 0.f);
-      if (P.out_f32)
-        static_cast<float*>(P.out)[m * P.N + n] = v;
-      else
-        static_cast<bf16*>(P.out)[m * P.N + n] = __float2bfloat16(v);
-    }
-  }
-}
-
-// ---- large products: CTA pairs, tcgen05 cta_group::2 ----
-// Tile 256 x 256 of the output per pair, each CTA holding 128 rows; a stage
-// is 128 of K (one scale block): 128 rows of A and half of B's columns per
-// CTA.  Each K block is an accumulation of its own in one of two TMEM
-// accumulators (256 columns each), scaled and added into registers by eight
-// warps (32 rows x 128 columns each) while the other accumulator is filled.
-constexpr int kDpThreads = 128 + 256;     // TMA warp, MMA warp (and two idle), 8 promotion warps
-// Registers: the launch holds 168 per thread; the first warpgroup returns
-// what it does not need and the promotion warps, with 128 sums each, take it
-// (128 x 40 + 256 x 224 <= 384 x 168).
-constexpr int kDpRegsLaunch = 168, kDpRegsFew = 40, kDpRegsMany = 224;
-static_assert(128 * kDpRegsFew + 256 * kDpRegsMany <= kDpThreads * kDpRegsLaunch,
-              "register split within the launch's registers");
-constexpr int kDpStages = 6;
-constexpr int kDpStage = 2 * 16384;       // A 128 x 128 bytes, B 128 x 128 bytes
-constexpr size_t kDpSmem = 1024 + kDpStages * kDpStage;
-constexpr int kDpGroupM = 8;              // row tiles of a raster group
-
-struct DpCtl {
-  uint64_t full[kDpStages], empty[kDpStages];
-  uint64_t tmem_full[2], tmem_empty[2];
-  uint32_t tmem_base;
-  int32_t abort;
-};
-
+// ---- shared by both products ----
 // Waits for phase `parity` of `bar`; gives up after kWaitLimitNs (error word,
 // abort flag) or when another role of the CTA has given up.
 __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, int32_t* abort,
@@ -199,18 +109,14 @@ __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, int32
 
 // Waits for the warp's TMEM loads, the registers tied to the wait so that
 // nothing reads them before it.
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
-
 // Arrives on an mbarrier of a CTA of the cluster without ordering this
 // thread's other memory operations: what the accumulator's next writer has
 // to follow are TMEM loads, which the tcgen05 fences order.  The releasing
@@ -220,6 +126,54 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
+
+// Pairs of fp32 sums as one 64-bit register pair (fma.rn.f32x2: each rounded
+// as fmaf); kept packed, so that no pair is taken apart and put together again
+// in every block.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ void fma_pair(uint64_t& c, uint32_t a0, uint32_t a1, uint64_t b) {
+  asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\tfma.rn.f32x2 %0, a, %3, %0;\n\t}"
+      : "+l"(c)
+      : "r"(a0), "r"(a1), "l"(b));
+}
+
+// ---- many rows: CTA pairs ----
+// Tile of 256 rows by 256 columns on a CTA pair (tcgen05 cta_group::2), each
+// CTA holding 128 rows.  A stage is 128 of K, one scale block: 128 rows of A
+// and 128 columns of the weight per CTA.  Each K block is an accumulation of
+// its own in one of two TMEM accumulators (256 columns each), scaled and added
+// into registers by eight warps (32 rows x 128 columns each) while the other
+// accumulator is filled.
+constexpr int kDpThreads = 128 + 256;  // TMA, 2 MMA, scale warp; 8 promotion warps
+// Registers: the launch holds 168 per thread; the first warpgroup returns
+// what it does not need and the promotion warps, with 128 sums each, take it.
+constexpr int kDpRegsLaunch = 168, kDpRegsFew = 72, kDpRegsMany = 208;
+static_assert(128 * kDpRegsFew + 256 * kDpRegsMany <= kDpThreads * kDpRegsLaunch,
+              "register split within the launch's registers");
+constexpr int kDpStages = 5;
+constexpr int kDpStage = 2 * 16384;    // A 128 x 128 bytes, weight 128 x 128 bytes
+constexpr int kDpStaging = 8 * 4096;   // per promotion warp 32 rows x 128 bytes of output
+constexpr int kDpScales = 4;           // scale slots (K blocks)
+constexpr int kDpGroupM = 8;           // row tiles of a raster group
+constexpr size_t kDpSmem = 1024 + kDpStages * kDpStage + kDpStaging;
+
+struct DpCtl {
+  uint64_t full[kDpStages], empty[kDpStages];
+  uint64_t tmem_full[2], tmem_empty[2];
+  float a_scale[kDpScales][128], w_scale[kDpScales][2];  // rows, column blocks of a K block
+  uint32_t tmem_base;
+  int32_t abort;
+};
+static_assert(kDpSmem + sizeof(DpCtl) <= 232448, "shared memory budget");
 
 struct TileMN {
   int m, n;
@@ -238,56 +192,57 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// 16 columns of one output row: bias, rounding, 16-byte stores.
-__device__ __forceinline__ void store16(const DenseParams& P, int64_t m, int n, const float* v) {
-  float o[16];
+// One 128-byte row piece of the output (64 bf16 or 32 fp32 columns) into row
+// `lane` of a 128-byte-swizzled staging block.
+template <bool F32>
+__device__ __forceinline__ void stage_row(uint8_t* buf, int lane, const uint64_t* v) {
+  // (opaque: the eight addresses would otherwise be kept in registers all
+  // through the promotion loop)
+  asm volatile("" : "+r"(lane));
 #pragma unroll
-  for (int j = 0; j < 16; ++j) o[j] = v[j];
-  if (P.bias != nullptr) {
+  for (int j = 0; j < 8; ++j) {  // 16-byte units
+    uint32_t u[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float b[8];
-      qg_unpack(__ldg(reinterpret_cast<const uint4*>(P.bias + n) + h), b);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[8 * h + j] += b[j];
+    for (int i = 0; i < (F32 ? 2 : 4); ++i) {
+      const float2 o = unpair(v[(F32 ? 2 : 4) * j + i]);
+      if constexpr (F32) {
+        u[2 * i] = __float_as_uint(o.x);
+        u[2 * i + 1] = __float_as_uint(o.y);
+      } else {
+        u[i] = pack2(o.x, o.y);
+      }
     }
-  }
-  if (P.out_f32) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(P.out) + m * P.N + n);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-  } else {
-    uint4* d = reinterpret_cast<uint4*>(static_cast<bf16*>(P.out) + m * P.N + n);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      d[j] = make_uint4(pack2(o[8 * j], o[8 * j + 1]), pack2(o[8 * j + 2], o[8 * j + 3]),
-                        pack2(o[8 * j + 4], o[8 * j + 5]), pack2(o[8 * j + 6], o[8 * j + 7]));
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
 template <bool TR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
     dense_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA,
-                          const __grid_constant__ CUtensorMap tmB, const DenseParams P) {
+                          const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ CUtensorMap tmO, const DenseParams P) {
   pdl_begin();
   extern __shared__ uint8_t smem_raw[];
   __shared__ DpCtl ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   uint8_t* tiles = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* staging = tiles + kDpStages * kDpStage;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDpStages; ++i) {
       ptx::mbar_init(&ctl.full[i], 1);
       ptx::mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ctl.tmem_full[i], 1);
-      ptx::mbar_init(&ctl.tmem_empty[i], 2 * 8);  // the promotion warps of both CTAs
+      ptx::mbar_init(&ctl.tmem_full[i], 2);        // the MMA's commit, the scale warp
+      ptx::mbar_init(&ctl.tmem_empty[i], 2 * 8);   // the promotion warps of both CTAs
     }
     ctl.abort = 0;
     ptx::fence_barrier_init();
     ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmB);
+    ptx::prefetch_tmap(&tmO);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(&ctl.tmem_base, 512);
@@ -302,6 +257,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
   const int mt = static_cast<int>(ceil_div<int64_t>(P.M, 256)), nt = ceil_div(P.N, 256);
   const int total = mt * nt;
   const int unit = static_cast<int>(blockIdx.x >> 1), units = static_cast<int>(gridDim.x >> 1);
+  const int64_t blocks =  // K blocks of this pair
+      unit < total ? static_cast<int64_t>((total - 1 - unit) / units + 1) * KB : 0;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDpRegsFew));
@@ -318,33 +275,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
             ok = false;
             break;
           }
+          uint8_t* sa = tiles + stage * kDpStage;
+          uint8_t* sb = sa + 16384;
           // both CTAs' copies complete on the even CTA's barrier
           const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0);
           if (rank == 0) ptx::mbar_arrive_expect_tx(&ctl.full[stage], 2 * kDpStage);
-          uint8_t* sa = tiles + stage * kDpStage;
           ptx::tma_load_2d_pair(sa, &tmA, full0, kb * 128, row);
-          if constexpr (TR)
-            ptx::tma_load_2d_pair(sa + 16384, &tmB, full0, kb * 128, col);
-          else
-            ptx::tma_load_2d_pair(sa + 16384, &tmB, full0, col, kb * 128);
+          ptx::tma_load_2d_pair(sb, &tmB, full0, TR ? kb * 128 : col, TR ? col : kb * 128);
           if (++stage == kDpStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, 256, false, !TR);
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!dense_wait(&ctl.tmem_empty[acc], acc_phase ^ 1u, &ctl.abort, P.error_word) ||
-              !dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word)) {
-            ok = false;
+    } else if (warp <= 2) {
+      // one issuing thread per accumulator: while one is held up by the MMAs
+      // queued ahead of its own, the other's waits and commits go on
+      // (8192 x 7168 x 4096: 194 us with one thread for both, 180 with two)
+      if (lane == 0 && rank == 0) {
+        const uint32_t acc = warp - 1;
+        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, 256, false, !TR);
+        int stage = acc;  // blocks acc, acc + 2, ...
+        uint32_t phase = 0, turn = 0;
+        for (int64_t g = acc; g < blocks; g += 2) {
+          if (!dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word) ||
+              !dense_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word))
             break;
-          }
+          turn ^= 1u;
           ptx::tc_fence_after();
           const uint32_t sa = ptx::smem_u32(tiles + stage * kDpStage), sb = sa + 16384;
 #pragma unroll
@@ -354,15 +311,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
                                    : ptx::smem_desc_sw128(sb + ks * 4096, 16384, 1024);
             ptx::mma_e4m3_pair(tmem + acc * 256, ad, bd, idesc, ks != 0);
           }
-          ptx::mma_commit_pair(&ctl.empty[stage], 0x3);
+          // (the accumulator's barrier first: the other order took a K-rows
+          // weight from 182 to 206 us at 8192 x 7168 x 4096)
           ptx::mma_commit_pair(&ctl.tmem_full[acc], 0x3);
-          if (++stage == kDpStages) {
-            stage = 0;
+          ptx::mma_commit_pair(&ctl.empty[stage], 0x3);
+          stage += 2;
+          if (stage >= kDpStages) {
+            stage -= kDpStages;
             phase ^= 1u;
           }
-          if (++acc == 2) {
-            acc = 0;
-            acc_phase ^= 1u;
+        }
+      }
+    } else {
+      // scales of the promotion warps' next blocks: four rows per lane, of two K
+      // blocks at a time and loaded two blocks ahead (across tiles too).  In
+      // the promotion warps, short of registers to hold them, these loads'
+      // latency came into every group of blocks.
+      float nx[4][2], nw[2];  // (w: lanes 0 and 1, one column block each)
+      auto load2 = [&](int t, int kb0) {
+        const TileMN tl = dense_tile(t, mt, nt);
+        const int64_t m = static_cast<int64_t>(tl.m) * 256 + rank * 128 + lane;
+        const int nb = min(tl.n * 2 + (lane & 1), NB - 1);
+        const float* pw = P.w_scale + (TR ? static_cast<int64_t>(nb) * KB : nb);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int kb = min(kb0 + j, KB - 1);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            nx[r][j] = __ldg(P.a_scale + min(m + 32 * r, P.M - 1) * KB + kb);
+          nw[j] = __ldg(pw + (TR ? kb : static_cast<int64_t>(kb) * NB));
+        }
+      };
+      if (unit < total) load2(unit, 0);
+      uint32_t g = 0;  // K blocks so far
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        for (int kb = 0; kb < KB && ok; kb += 2) {
+          float c[4][2], cw[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) c[r][j] = nx[r][j];
+            cw[j] = nw[j];
+          }
+          if (kb + 2 < KB)
+            load2(t, kb + 2);
+          else if (t + units < total)
+            load2(t + units, 0);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (kb + j >= KB) break;
+            // block g - 2 complete means that block g - 4, whose slot this is,
+            // has left the accumulators and the slot: the MMA of g - 2 waited
+            // for its release
+            bool got = true;
+            if (g >= 2)
+              got = dense_wait(&ctl.tmem_full[g & 1], (g >> 1 & 1) ^ 1u, &ctl.abort, P.error_word);
+            if (!__all_sync(0xffffffffu, got)) {
+              ok = false;
+              break;
+            }
+            const int slot = g % kDpScales;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ctl.a_scale[slot][lane + 32 * r] = c[r][j];
+            if (lane < 2) ctl.w_scale[slot][lane] = cw[j];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ctl.tmem_full[g & 1]);
+            ++g;
           }
         }
       }
@@ -372,92 +387,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tmem_empty[0]), 0);
-    // scales of four K blocks at a time, loaded four blocks ahead (across
-    // tiles too): a load in the block that uses it would put an L2 round trip
-    // into every block
-    auto load4 = [&](int t, int kb0, float (&sa)[4], float (&sw)[4]) {
-      const TileMN tl = dense_tile(t, mt, nt);
-      const int64_t m = static_cast<int64_t>(tl.m) * 256 + rank * 128 + q * 32 + lane;
-      const int nb = min(tl.n * 2 + half, NB - 1);
-      const float* pa = P.a_scale + (m < P.M ? m : P.M - 1) * KB;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int kb = min(kb0 + j, KB - 1);
-        sa[j] = __ldg(pa + kb);
-        sw[j] = __ldg(P.w_scale + (TR ? static_cast<int64_t>(nb) * KB + kb
-                                      : static_cast<int64_t>(kb) * NB + nb));
-      }
-    };
-    float na[4], nw[4];
-    if (unit < total) load4(unit, 0, na, nw);
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    uint8_t* buf = staging + (warp - 4) * 4096;
+    uint32_t g = 0;  // K blocks so far
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
-      float sum[128];
+      uint64_t sum[64];  // 128 columns
+      const int n0 = dense_tile(t, mt, nt).n * 256 + half * 128;
+      if (P.bias != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 128; ++j) sum[j] = 0.f;
-      float c[4];
-      for (int kb = 0; kb < KB; ++kb) {
-        if ((kb & 3) == 0) {
+        for (int j = 0; j < 128; j += 8) {  // (N is a multiple of 16)
+          float b[8] = {};
+          if (n0 + j < P.N) qg_unpack(__ldg(reinterpret_cast<const uint4*>(P.bias + n0 + j)), b);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) c[j] = na[j] * nw[j];
-          if (kb + 4 < KB)
-            load4(t, kb + 4, na, nw);
-          else if (t + units < total)
-            load4(t + units, 0, na, nw);
+          for (int i = 0; i < 8; i += 2) sum[(j + i) / 2] = pair_of(b[i], b[i + 1]);
         }
-        const float sc = c[0];
-        c[0] = c[1];
-        c[1] = c[2];
-        c[2] = c[3];
-        const bool got = dense_wait(&ctl.tmem_full[acc], acc_phase, &ctl.abort, P.error_word);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) sum[j] = 0;
+      }
+      for (int kb = 0; kb < KB; ++kb, ++g) {
+        const uint32_t acc = g & 1;
+        const bool got =
+            dense_wait(&ctl.tmem_full[acc], g >> 1 & 1, &ctl.abort, P.error_word);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
         const uint32_t ta = lane_addr + acc * 256;
-        uint32_t v[2][32];
-        ptx::tmem_ld_32cols(ta, v[0]);
+        uint32_t v[2][16];
+        ptx::tmem_ld_16cols(ta, v[0]);
+        const int slot = g % kDpScales;
+        const float f = ctl.a_scale[slot][q * 32 + lane] * ctl.w_scale[slot][half];
+        const uint64_t sc = pair_of(f, f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          tmem_wait32(v[i & 1]);
-          if (i < 3) {
-            ptx::tmem_ld_32cols(ta + 32 * (i + 1), v[(i + 1) & 1]);
+        for (int i = 0; i < 8; ++i) {
+          tmem_wait16(v[i & 1]);
+          if (i < 7) {
+            ptx::tmem_ld_16cols(ta + 16 * (i + 1), v[(i + 1) & 1]);
           } else {  // the accumulator is in registers
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_relaxed(empty0 + acc * 8);
           }
 #pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            ptx::fma2(sum[32 * i + j], sum[32 * i + j + 1], __uint_as_float(v[i & 1][j]),
-                      __uint_as_float(v[i & 1][j + 1]), sc);
-        }
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
+          for (int j = 0; j < 16; j += 2)
+            fma_pair(sum[8 * i + j / 2], v[i & 1][j], v[i & 1][j + 1], sc);
         }
       }
       if (!ok) break;
-      const TileMN tl = dense_tile(t, mt, nt);
-      const int64_t m = static_cast<int64_t>(tl.m) * 256 + rank * 128 + q * 32 + lane;
-      const int n0 = tl.n * 256 + half * 128;
-      if (m < P.M) {
+      // the tile's rows through the warp's staging block, 128 bytes of each
+      // at a time, and out by TMA (which clips what lies past M and N): lanes
+      // storing their own rows would take a sector per lane and store, 6000
+      // cycles per tile
+      const int m = dense_tile(t, mt, nt).m * 256 + static_cast<int>(rank) * 128 + q * 32;
+      auto put = [&](auto f32) {
+        constexpr bool F32 = decltype(f32)::value;
+        constexpr int W = F32 ? 32 : 64;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n0 + 16 * i < P.N) store16(P, m, n0 + 16 * i, sum + 16 * i);
-      }
+        for (int i = 0; i < 128 / W; ++i) {
+          const int n = n0 + i * W;
+          if (n < P.N && m < P.M) {
+            if (lane == 0) ptx::bulk_wait_read0();
+            __syncwarp();
+            stage_row<F32>(buf, lane, sum + i * W / 2);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::tma_store_2d(&tmO, buf, n, m);
+              ptx::bulk_commit();
+            }
+          }
+        }
+      };
+      if (P.out_f32)
+        put(std::true_type{});
+      else
+        put(std::false_type{});
     }
+    if (lane == 0) ptx::bulk_wait0();
   }
   __syncwarp();
   ptx::cluster_sync();
+  // the last stages' commits, which nothing else waits for, have to arrive
+  // before the barriers' memory goes
+  if (threadIdx.x < 2 && blocks > static_cast<int>(threadIdx.x)) {
+    const int64_t g = blocks - 1 - threadIdx.x;
+    dense_wait(&ctl.empty[g % kDpStages], static_cast<uint32_t>(g / kDpStages) & 1u, &ctl.abort,
+               P.error_word);
+  }
   if (*reinterpret_cast<volatile int32_t*>(&ctl.abort)) {
     // copies and MMAs in flight get time to land before their memory goes
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
+  __syncwarp();
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
@@ -465,7 +489,258 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
   }
 }
 
-// Tensor maps of A [M, K] and of the weight, boxes of 128 x 128 bytes.
+
+// ---- few rows: the weight's columns as the MMA's rows, K split over a cluster ----
+// The weight's bytes bound these products, so that every SM has to stream
+// them: a CTA takes 128 weight columns (the MMA's M) and one of S parts of K
+// for T rows of A (the MMA's N), the S CTAs of a cluster add their sums through
+// distributed shared memory in a fixed order.  TMEM lane = weight column, TMEM
+// column = row of A, so a thread's sums are one output column for T rows and
+// the output is written along its rows.
+constexpr int kDsThreads = 64 + 128;   // TMA warp, MMA warp, 4 promotion warps
+constexpr int kDsScaleBlocks = 16;     // K blocks whose scales are held at a time
+template <int T>
+struct DsGeo {
+  static constexpr int STAGE = 16384 + T * 128;
+  static constexpr int STAGES = T <= 32 ? 9 : T == 64 ? 7 : 5;
+  static constexpr int ACCS = T == 128 ? 4 : 8;  // TMEM accumulators of T columns
+  static constexpr int COLS = ACCS * T;
+  static constexpr int PART = 132;               // padded row of the partial sums, floats
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE;
+  static_assert(T * PART * 4 <= STAGES * STAGE, "partial sums in the ring's memory");
+};
+template <int T>
+struct DsCtl {
+  uint64_t full[DsGeo<T>::STAGES], empty[DsGeo<T>::STAGES];
+  uint64_t tmem_full[DsGeo<T>::ACCS], tmem_empty[DsGeo<T>::ACCS];
+  uint64_t scale_free, scale_ready;
+  alignas(16) float scale[kDsScaleBlocks][T];  // row scale times the block's weight scale
+  uint32_t tmem_base;
+  int32_t abort;
+};
+static_assert(DsGeo<16>::SMEM + sizeof(DsCtl<16>) <= 232448 &&
+                  DsGeo<32>::SMEM + sizeof(DsCtl<32>) <= 232448 &&
+                  DsGeo<64>::SMEM + sizeof(DsCtl<64>) <= 232448 &&
+                  DsGeo<128>::SMEM + sizeof(DsCtl<128>) <= 232448,
+              "shared memory budget");
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int T, bool TR>
+__global__ void __launch_bounds__(kDsThreads, 1)
+    dense_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmB, const DenseParams P,
+                           const int S) {
+  using G = DsGeo<T>;
+  pdl_begin();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ DsCtl<T> ctl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(ptx::cluster_ctarank());  // the part of K
+  uint8_t* tiles = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::STAGES; ++i) {
+      ptx::mbar_init(&ctl.full[i], 1);
+      ptx::mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < G::ACCS; ++i) {
+      ptx::mbar_init(&ctl.tmem_full[i], 1);
+      ptx::mbar_init(&ctl.tmem_empty[i], 4);
+    }
+    ptx::mbar_init(&ctl.scale_free, 4);
+    ptx::mbar_init(&ctl.scale_ready, 4);
+    ctl.abort = 0;
+    ptx::fence_barrier_init();
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&ctl.tmem_base, G::COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+
+  const int KB = ceil_div(P.K, 128), NB = ceil_div(P.N, 128);
+  const int nb = static_cast<int>(blockIdx.x) / S;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * T;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / S);
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word)) break;
+        uint8_t* sw = tiles + stage * G::STAGE;
+        ptx::mbar_arrive_expect_tx(&ctl.full[stage], G::STAGE);
+        ptx::tma_load_2d(sw, &tmB, &ctl.full[stage], TR ? kb * 128 : nb * 128,
+                         TR ? nb * 128 : kb * 128);
+        ptx::tma_load_2d(sw + 16384, &tmA, &ctl.full[stage], kb * 128, static_cast<int>(m0));
+        if (++stage == G::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, T, !TR, false);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, turn = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!dense_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word) ||
+            !dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word))
+          break;
+        ptx::tc_fence_after();
+        const uint32_t sw = ptx::smem_u32(tiles + stage * G::STAGE), sx = sw + 16384;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t wd = TR ? ptx::smem_desc_sw128(sw + ks * 32, 16, 1024)
+                                 : ptx::smem_desc_sw128(sw + ks * 4096, 16384, 1024);
+          ptx::mma_e4m3(tmem + acc * T, wd, ptx::smem_desc_sw128(sx + ks * 32, 16, 1024), idesc,
+                        ks != 0);
+        }
+        ptx::mma_commit(&ctl.empty[stage]);
+        ptx::mma_commit(&ctl.tmem_full[acc]);
+        if (++stage == G::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++acc == G::ACCS) {
+          acc = 0;
+          turn ^= 1u;
+        }
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    const int p = threadIdx.x - 64;      // 0 .. 127, for the scales
+    const int col = q * 32 + lane;       // weight column of the tile
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint64_t sum[T / 2];
+#pragma unroll
+    for (int j = 0; j < T / 2; ++j) sum[j] = 0;
+    // all four promotion warps meet (a bounded wait, unlike a named barrier)
+    auto meet = [&](uint64_t* bar, uint32_t parity) {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar);
+      const bool got = dense_wait(bar, parity, &ctl.abort, P.error_word);
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    int acc = 0;
+    uint32_t turn = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int slot = (kb - kb0) % kDsScaleBlocks;
+      if (slot == 0) {
+        // the next blocks' scales, by all four warps; rows past M count as 0
+        const uint32_t chunk = static_cast<uint32_t>(kb - kb0) / kDsScaleBlocks;
+        if (chunk > 0 && !meet(&ctl.scale_free, (chunk - 1) & 1)) {
+          ok = false;
+          break;
+        }
+#pragma unroll 4
+        for (int i = p; i < kDsScaleBlocks * T; i += 128) {
+          const int b = i % kDsScaleBlocks, r = i / kDsScaleBlocks;
+          float s = 0.f;
+          if (kb + b < kb1 && m0 + r < P.M)
+            s = __ldg(P.a_scale + (m0 + r) * KB + kb + b) *
+                __ldg(P.w_scale + (TR ? static_cast<int64_t>(nb) * KB + kb + b
+                                      : static_cast<int64_t>(kb + b) * NB + nb));
+          ctl.scale[b][r] = s;
+        }
+        if (!meet(&ctl.scale_ready, chunk & 1)) {
+          ok = false;
+          break;
+        }
+      }
+      const bool got = dense_wait(&ctl.tmem_full[acc], turn, &ctl.abort, P.error_word);
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(ctl.scale[slot]);
+#pragma unroll
+      for (int c = 0; c < T; c += 16) {
+        uint32_t v[16];
+        ptx::tmem_ld_16cols(lane_addr + acc * T + c, v);
+        tmem_wait16(v);
+        if (c + 16 == T) {  // the accumulator is in registers
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl.tmem_empty[acc]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const ulonglong2 s4 = sc[(c + j) / 4];
+          fma_pair(sum[(c + j) / 2], v[j], v[j + 1], s4.x);
+          fma_pair(sum[(c + j) / 2 + 1], v[j + 2], v[j + 3], s4.y);
+        }
+      }
+      if (++acc == G::ACCS) {
+        acc = 0;
+        turn ^= 1u;
+      }
+    }
+    // every stage of the ring has been read (the last block's MMA is done):
+    // its memory takes the partial sums, [row of A][column]
+    float* part = reinterpret_cast<float*>(tiles);
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < T; j += 2) {
+        const float2 v = unpair(sum[j / 2]);
+        part[j * G::PART + col] = v.x;
+        part[(j + 1) * G::PART + col] = v.y;
+      }
+    }
+  }
+  __syncwarp();
+  ptx::cluster_sync();
+  if (warp >= 2) {
+    // rows rank, rank + S, ... of the tile: the parts in order, bias, output
+    const int col = threadIdx.x - 64;
+    const int n = nb * 128 + col;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(T), P.M - m0));
+    const float b = P.bias != nullptr && n < P.N ? __bfloat162float(P.bias[n]) : 0.f;
+    const uint32_t mine = ptx::smem_u32(tiles) + col * 4;
+    if (n < P.N) {
+#pragma unroll 4
+      for (int r = rank; r < rows; r += S) {
+        float v = b;
+        for (int s = 0; s < S; ++s)
+          v += ld_cluster_f32(ptx::mapa_shared(mine + r * (G::PART * 4), s));
+        const int64_t o = (m0 + r) * P.N + n;
+        if (P.out_f32)
+          static_cast<float*>(P.out)[o] = v;
+        else
+          static_cast<bf16*>(P.out)[o] = __float2bfloat16(v);
+      }
+    }
+  }
+  if (*reinterpret_cast<volatile int32_t*>(&ctl.abort)) {
+    // copies and MMAs in flight get time to land before their memory goes
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  ptx::cluster_sync();  // (no CTA leaves while another reads its sums)
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, G::COLS);
+  }
+}
+
+// Tensor maps of A [M, K], in boxes of a_rows x 128 bytes, and of the weight,
+// in boxes of 128 x 128 bytes.
 moe_status_t dense_maps(const MatmulFp8Args& a, uint32_t a_rows, CUtensorMap* tmA,
                         CUtensorMap* tmB) {
   const uint64_t K = a.K, N = a.N;
@@ -477,6 +752,18 @@ moe_status_t dense_maps(const MatmulFp8Args& a, uint32_t a_rows, CUtensorMap* tm
   const uint64_t db[2] = {a.transposed ? K : N, a.transposed ? N : K}, sb[1] = {db[0]};
   return encode_tensor_map(tmB, a.w, 2, db, sb, bb, CU_TENSOR_MAP_DATA_TYPE_UINT8,
                            CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Tensor map of the output, boxes of 32 rows x 128 bytes.
+moe_status_t dense_out_map(const MatmulFp8Args& a, CUtensorMap* tmO) {
+  const uint64_t eb = a.out_f32 ? 4 : 2;
+  const uint64_t d[2] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.M)};
+  const uint64_t st[1] = {static_cast<uint64_t>(a.N) * eb};
+  const uint32_t box[2] = {static_cast<uint32_t>(128 / eb), 32};
+  return encode_tensor_map(
+      tmO, a.out, 2, d, st, box,
+      a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <bool TR>
@@ -500,14 +787,62 @@ moe_status_t launch_pair(const MatmulFp8Args& a, const DenseParams& P, cudaStrea
   if (regs < kDpRegsLaunch)
     return set_error(MOE_ERR_CUDA, "matmul_fp8 was compiled to %d registers, %d needed", regs,
                      kDpRegsLaunch);
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmO;
   if (moe_status_t st = dense_maps(a, 128, &tmA, &tmB)) return st;
+  if (moe_status_t st = dense_out_map(a, &tmO)) return st;
   const int64_t tiles = ceil_div<int64_t>(a.M, 256) * ceil_div(a.N, 256);
   const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, a.num_sms / 2));
   prof_before("matmul_fp8", s);
-  launch_kernel(dense_fp8_pair_kernel<TR>, grid, kDpThreads, kDpSmem, s, tmA, tmB, P);
+  launch_kernel(dense_fp8_pair_kernel<TR>, grid, kDpThreads, kDpSmem, s, tmA, tmB, tmO, P);
   prof_after("matmul_fp8", s);
   return check_launch("matmul_fp8");
+}
+
+template <int T, bool TR>
+moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
+  using G = DsGeo<T>;
+  static PerDevice attr;
+  if (attr.get([](int*) {
+        return cudaFuncSetAttribute(dense_fp8_split_kernel<T, TR>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(G::SMEM));
+      }) != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "attributes of matmul_fp8: %s",
+                     cudaGetErrorString(cudaGetLastError()));
+  CUtensorMap tmA, tmB;
+  if (moe_status_t st = dense_maps(a, T, &tmA, &tmB)) return st;
+  const int64_t mt = ceil_div<int64_t>(a.M, T);
+  const int nt = ceil_div(a.N, 128), KB = ceil_div(a.K, 128);
+  // as many parts of K as fill the SMs once, up to a portable cluster
+  const int S = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({8, KB, a.num_sms / (nt * mt)})));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(nt * S), static_cast<unsigned>(mt));
+  cfg.blockDim = dim3(kDsThreads);
+  cfg.dynamicSmemBytes = G::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(S);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  prof_before("matmul_fp8", s);
+  cudaLaunchKernelEx(&cfg, dense_fp8_split_kernel<T, TR>, tmA, tmB, P, S);
+  prof_after("matmul_fp8", s);
+  return check_launch("matmul_fp8");
+}
+
+template <bool TR>
+moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
+  if (a.M <= 16) return launch_split<16, TR>(a, P, s);
+  if (a.M <= 32) return launch_split<32, TR>(a, P, s);
+  if (a.M <= 64) return launch_split<64, TR>(a, P, s);
+  if (a.M <= 128) return launch_split<128, TR>(a, P, s);
+  return launch_pair<TR>(a, P, s);
 }
 
 }  // namespace
@@ -524,15 +859,8 @@ moe_status_t launch_quant_groups_fp8(const QuantGroupsArgs& a, cudaStream_t s) {
 }
 
 moe_status_t launch_matmul_fp8(const MatmulFp8Args& a, cudaStream_t s) {
-  const DenseParams P{a.a, a.a_scale, a.w, a.w_scale, a.bias, a.out, a.M, a.K, a.N, a.transposed,
-                      a.out_f32, a.error_word};
-  if (a.M > 128) return a.transposed ? launch_pair<true>(a, P, s) : launch_pair<false>(a, P, s);
-  const dim3 grid(static_cast<unsigned>(ceil_div<int64_t>(a.M, 64)),
-                  static_cast<unsigned>(ceil_div(a.N, 64)));
-  prof_before("matmul_fp8", s);
-  launch_kernel(dense_fp8_simt_kernel, grid, 256, 0, s, P);
-  prof_after("matmul_fp8", s);
-  return check_launch("matmul_fp8");
+  const DenseParams P{a.a_scale, a.w_scale, a.bias, a.out, a.M, a.K, a.N, a.out_f32, a.error_word};
+  return a.transposed ? launch_matmul<true>(a, P, s) : launch_matmul<false>(a, P, s);
 }
 
 }  // namespace gbmoe

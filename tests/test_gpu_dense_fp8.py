@@ -121,6 +121,8 @@ SHAPES = [
     (31, 1024, 256), (33, 128, 2064), (64, 2048, 1024), (65, 528, 384), (100, 896, 640),
     (128, 1024, 528), (129, 272, 144), (200, 1536, 304), (255, 384, 512), (257, 640, 272),
     (300, 2048, 1536), (513, 512, 784), (1000, 144, 2048), (1025, 1280, 912),
+    (3, 4352, 10256),        # more K blocks per part than scales are held at a time
+    (2601, 400, 2064), (4100, 656, 1808),   # several tiles per CTA pair
 ]
 
 
