@@ -120,38 +120,46 @@ def moe_route(router_logits: torch.Tensor, top_k: int, routing_method: str = "so
     return topk_weights, topk_ids
 
 
-def _tensor(t, name: str, dtypes, shape, device, optional: bool = False):
-    """Checks an argument of the functions that take them as they come:
-    type, shape, contiguity, and the device of the call."""
-    if t is None and optional:
+def _tensor(t, name: str, dtypes, shape, device: int):
+    """Checks an argument of the functions that take them as they come: type,
+    shape, contiguity, and the device of the call.  (One expression where all
+    is well: these calls are a few microseconds long.)"""
+    if (type(t) is torch.Tensor and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+            and t.get_device() == device):
         return
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a tensor of {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected "
+                         f"{'the CPU' if device < 0 else f'cuda:{device}'}")
 
 
-def _call(fn, where: str, device: torch.device, stream, outs, *args):
-    """Calls an entry point on `stream` (default: the current one) with
-    `device` current; tensors allocated for the call are recorded on a stream
-    of the caller's."""
-    if device.type != "cuda":
-        raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
-    if device.index != (_current_device or torch.cuda.current_device)():
+def _call(name: str, device: int, stream, new, *args):
+    """Calls the entry point `name` on `stream` (default: the current one)
+    with `device` current; tensors allocated for the call are recorded on a
+    stream of the caller's."""
+    if device < 0:
+        raise ValueError(f"{name}: tensors must be on a CUDA device")
+    if device != (_current_device or torch.cuda.current_device)():
         with torch.cuda.device(device):
-            return _call(fn, where, device, stream, outs, *args)
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
-        for t in outs:
+            return _call(name, device, stream, new, *args)
+    if stream is None:
+        handle = (_raw_current_stream(device) if _raw_current_stream is not None
+                  else torch.cuda.current_stream().cuda_stream)
+    else:
+        if stream.device.index != device:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on "
+                             f"cuda:{device}")
+        for t in new:
             t.record_stream(stream)
-    st = fn(*args, _stream(stream))
+        handle = stream.cuda_stream
+    st = getattr(_lib.load(), name)(*args, handle)
     if st != MOE_OK:
-        _check(st, where)
+        _check(st, name)
 
 
 _LOGITS = (torch.float32, torch.bfloat16)
@@ -165,13 +173,13 @@ def _matrix(t, name: str):
     return t.shape
 
 
-def _out(t, name: str, dtype, shape, device, new: list):
+def _out(t, name: str, dtype, shape, device: int, new: list):
     """The caller's output tensor after its checks, or a new one (noted in
     `new`)."""
     if t is not None:
         _tensor(t, name, (dtype,), shape, device)
         return t
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device if device >= 0 else "cpu")
     new.append(t)
     return t
 
@@ -180,13 +188,13 @@ def _route_biased(router_logits, score_bias, top_k, routing_method, renormalize,
                   group_count, group_select_mode, routed_scaling_factor, topk_weights, topk_ids,
                   stream):
     M, E = _matrix(router_logits, "router_logits")
-    dev = router_logits.device
+    dev = router_logits.get_device()
     _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
     _tensor(score_bias, "score_bias", _F32, (E,), dev)
     new = []
     topk_weights = _out(topk_weights, "topk_weights", torch.float32, (M, top_k), dev, new)
     topk_ids = _out(topk_ids, "topk_ids", torch.int32, (M, top_k), dev, new)
-    _call(lib().moe_route_biased, "moe_route_biased", dev, stream, new, router_logits.data_ptr(),
+    _call("moe_route_biased", dev, stream, new, router_logits.data_ptr(),
           int(router_logits.dtype == torch.bfloat16), score_bias.data_ptr(), M, E, top_k,
           ROUTING[routing_method], int(bool(renormalize)), k_group, group_count,
           group_select_mode, float(routed_scaling_factor), topk_weights.data_ptr(),
@@ -205,14 +213,15 @@ def moe_route_backward(grad_weights: torch.Tensor, router_logits: torch.Tensor,
     id is outside [0, E) (such items take no part)."""
     M, E = _matrix(router_logits, "router_logits")
     k = _matrix(topk_ids, "topk_ids")[1]
-    dev = router_logits.device
+    dev = router_logits.get_device()
     _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
     _tensor(topk_ids, "topk_ids", _I32, (M, k), dev)
     _tensor(grad_weights, "grad_weights", _F32, (M, k), dev)
-    _tensor(error_word, "error_word", _I32, (1,), dev, optional=True)
+    if error_word is not None:
+        _tensor(error_word, "error_word", _I32, (1,), dev)
     new = []
     grad_logits = _out(grad_logits, "grad_logits", router_logits.dtype, (M, E), dev, new)
-    _call(lib().moe_route_backward, "moe_route_backward", dev, stream, new,
+    _call("moe_route_backward", dev, stream, new,
           grad_weights.data_ptr(), router_logits.data_ptr(),
           int(router_logits.dtype == torch.bfloat16), topk_ids.data_ptr(), M, E, k,
           ROUTING[routing_method], int(bool(renormalize)), float(routed_scaling_factor),
@@ -362,7 +371,7 @@ def moe_quant_groups_fp8(x: torch.Tensor, swiglu: bool = False,
     [M, ceil(K/128)]).  swiglu: x is [M, 2K], and SiLU(x[:, :K]) * x[:, K:]
     is what is quantised."""
     M, cols = _matrix(x, "x")
-    dev = x.device
+    dev = x.get_device()
     _tensor(x, "x", _BF16, (M, cols), dev)
     if swiglu and cols % 2:
         raise ValueError("swiglu needs an even number of columns")
@@ -373,7 +382,7 @@ def moe_quant_groups_fp8(x: torch.Tensor, swiglu: bool = False,
     else:
         _tensor(q8, "q8", _FP8, (M, K), dev)
     scale = _out(scale, "scale", torch.float32, (M, -(-K // FP8_BLOCK)), dev, new)
-    _call(lib().moe_quant_groups_fp8, "moe_quant_groups_fp8", dev, stream, new, x.data_ptr(), M, K,
+    _call("moe_quant_groups_fp8", dev, stream, new, x.data_ptr(), M, K,
           int(bool(swiglu)), q8.data_ptr(), scale.data_ptr())
     return q8, scale
 
@@ -391,21 +400,23 @@ def moe_matmul_fp8(a_q: torch.Tensor, a_scale: torch.Tensor, w_q: torch.Tensor,
     M, K = _matrix(a_q, "a_q")
     rows, cols = _matrix(w_q, "w_q")
     N = rows if transposed else cols
-    dev = a_q.device
+    dev = a_q.get_device()
     KB, NB = -(-K // FP8_BLOCK), -(-N // FP8_BLOCK)
     _tensor(a_q, "a_q", _FP8, (M, K), dev)
     _tensor(a_scale, "a_scale", _F32, (M, KB), dev)
     _tensor(w_q, "w_q", _FP8, (N, K) if transposed else (K, N), dev)
     _tensor(w_scale, "w_scale", _F32, (NB, KB) if transposed else (KB, NB), dev)
-    _tensor(bias, "bias", _BF16, (N,), dev, optional=True)
-    _tensor(error_word, "error_word", _I32, (1,), dev, optional=True)
+    if bias is not None:
+        _tensor(bias, "bias", _BF16, (N,), dev)
+    if error_word is not None:
+        _tensor(error_word, "error_word", _I32, (1,), dev)
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _LOGITS:
         raise ValueError("the output is torch.bfloat16 or torch.float32")
     new = []
     out = _out(out, "out", out_dtype, (M, N), dev, new)
-    _call(lib().moe_matmul_fp8, "moe_matmul_fp8", dev, stream, new, a_q.data_ptr(),
+    _call("moe_matmul_fp8", dev, stream, new, a_q.data_ptr(),
           a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), int(bool(transposed)),
           None if bias is None else bias.data_ptr(), M, K, N, int(out_dtype == torch.float32),
           out.data_ptr(), None if error_word is None else error_word.data_ptr())
