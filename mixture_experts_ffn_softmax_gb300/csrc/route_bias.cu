@@ -6,7 +6,7 @@
 // c is compared as in 64-bit arithmetic: two fp32 values of c closer than
 // their rounding say nothing about the order of the exact ones, and the ids
 // are integers, right or wrong.
-#include <cfloat>
+#include <algorithm>
 
 #include "common.cuh"
 
@@ -162,9 +162,11 @@ __device__ __forceinline__ void rb_weights(const T* row, const RbParams& P, int 
   }
 }
 
+// Every token by the 64-bit choice: more than 30 experts per token, or more
+// groups than a warp has lanes.
 template <typename T>
 __global__ void __launch_bounds__(kRbWarps * 32)
-    route_biased_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
+    route_biased_exact_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
                         float* __restrict__ out_w, int32_t* __restrict__ out_ids) {
   pdl_begin();
   extern __shared__ double rb_smem[];
@@ -184,15 +186,446 @@ __global__ void __launch_bounds__(kRbWarps * 32)
   rb_weights(row, P, id0, id1, mx, sum, out_w + t * P.top_k, out_ids + t * P.top_k);
 }
 
-// Gradient with respect to the logits of sum_j gw_j w_j, one warp per token.
+// Order-preserving map of a float (not NaN) to an unsigned key, and back.
+__device__ __forceinline__ uint32_t rb_key(float f) {
+  const uint32_t b = f == 0.0f ? 0u : __float_as_uint(f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float rb_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+template <int LPT, typename F>
+__device__ __forceinline__ F rb_seg_max(F v) {
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float rb_seg_sum(float v) {
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// N consecutive logits as floats; vec: N elements at p are there and aligned.
+template <int N>
+__device__ __forceinline__ void rb_load(const float* p, float (&l)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+      l[i] = v.x;
+      l[i + 1] = v.y;
+      l[i + 2] = v.z;
+      l[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(p + i));
+      l[i] = v.x;
+      l[i + 1] = v.y;
+    }
+  }
+}
+__device__ __forceinline__ void rb_pair(uint32_t u, float& a, float& b) {
+  a = __uint_as_float(u << 16);
+  b = __uint_as_float(u & 0xffff0000u);
+}
+template <int N>
+__device__ __forceinline__ void rb_load(const bf16* p, float (&l)[N]) {
+  if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + i));
+      rb_pair(v.x, l[i], l[i + 1]);
+      rb_pair(v.y, l[i + 2], l[i + 3]);
+      rb_pair(v.z, l[i + 4], l[i + 5]);
+      rb_pair(v.w, l[i + 6], l[i + 7]);
+    }
+  } else if constexpr (N == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    rb_pair(v.x, l[0], l[1]);
+    rb_pair(v.y, l[2], l[3]);
+  } else {
+    rb_pair(__ldg(reinterpret_cast<const uint32_t*>(p)), l[0], l[1]);
+  }
+}
+
+// The choice in fp32 where fp32 decides it, else as rb_choose64 does.
+//
+// LPT lanes per token, EPL consecutive experts per lane.  A candidate is one
+// 32-bit key: c in order-preserving form with its low bits replaced by the
+// expert (complemented: the lower id wins), so that a maximum over the lanes
+// is a chosen expert; each lane offers its largest key below the last one it
+// gave.  top_k + 2 rounds leave a candidate per lane.  Their exact fp32 c (the
+// keys' low bits back) puts them in order, and the choice stands if no two
+// neighbours down to the (top_k + 1)-th are closer than the error of c, nor
+// the top_k-th and what was not a candidate; equal logits with equal biases
+// are ties for certain.  Otherwise (0.3 % of the tokens of 256 normally
+// distributed sigmoid scores), or where a score is NaN, the warp takes the
+// token by rb_choose64.
+//
+// Bound: issue slots.  8192 tokens x 256 experts, 8 of 4 of 8 groups, from
+// 281 us (every token by rb_choose64) to 35 us a call; 16384 x 128 bf16, 8
+// chosen, 298 to 23 us.
+template <int EPL, int LPT, typename T>
+__global__ void __launch_bounds__(kRbWarps * 32)
+    route_biased_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
+                        int vec, float* __restrict__ out_w, int32_t* __restrict__ out_ids) {
+  pdl_begin();
+  extern __shared__ double rb_smem[];
+  constexpr int TPW = 32 / LPT;
+  constexpr uint32_t MASK = LPT * EPL - 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sl = lane % LPT, seg0 = lane - sl;
+  const int E = P.E, G = P.group_count, k = P.top_k;
+  const bool softmax = P.method == MOE_ROUTE_SOFTMAX;
+  const int e0 = sl * EPL;
+  double* sm = rb_smem + warp * (E + G);
+  float b[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) b[i] = e0 + i < E ? __ldg(bias + e0 + i) : 0.f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) * TPW;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * TPW; t0 < P.M;
+       t0 += step) {
+    const bool live = t0 + seg0 / LPT < P.M;
+    const int64_t t = live ? t0 + seg0 / LPT : P.M - 1;
+    const T* row = logits + t * E;
+    float c[EPL];
+    if (vec && e0 < E) {
+      rb_load<EPL>(row + e0, c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = e0 + i < E ? rb_f32(row[e0 + i]) : -INFINITY;
+    }
+    // ---- c = p + b; P1: the largest p, cf: p = exp(l - mx) cf ----
+    float mx = 0.f, sum = 1.f, cf = 1.f;
+    if (softmax) {
+      mx = c[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, c[i]);
+      mx = rb_seg_max<LPT>(mx);
+      sum = 0.f;
+    }
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float l = c[i];
+      float p;
+      if (softmax) {
+        p = expf(l - mx);
+        if (e0 + i < E) sum += p;
+      } else {
+        p = __fdividef(1.0f, 1.0f + expf(-l)) + b[i];
+        if (l == -INFINITY) p = -INFINITY;
+      }
+      c[i] = p;
+    }
+    if (softmax) {
+      sum = rb_seg_sum<LPT>(sum);
+      cf = 1.0f / sum;
+      // masked experts: exp is 0 for them (and for logits 100 below the
+      // largest, which are looked up again)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const bool masked = c[i] == 0.f && e0 + i < E && rb_f32(row[e0 + i]) == -INFINITY;
+        c[i] = masked ? -INFINITY : fmaf(c[i], cf, b[i]);
+      }
+    }
+    const float p1 = softmax ? cf : 1.0f;
+    // error of a difference of two c: p within 4.5 steps of 2^-22 (expf 2 ulp,
+    // 1 + e, __fdividef 2 ulp), for softmax 8 + EPL + 10 of 2^-24 (its sum);
+    // the addition of the bias
+    const float kerr = softmax ? 2.0f * (18 + EPL) * 5.9604645e-8f : 1.1e-6f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) bad |= c[i] != c[i] && e0 + i < E;
+    // ---- groups: kept ones as a mask of the segment ----
+    uint32_t kept = 0xffffffffu;
+    const int gs = E / G;
+    if (P.k_group < G) {
+      float gk = -INFINITY;  // lane g: group g's score
+      const int lpg = gs / EPL;
+      if (gs == lpg * EPL && (lpg & (lpg - 1)) == 0) {
+        // a group is lpg whole lanes
+        float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          b2 = fmaxf(b2, fminf(b1, c[i]));
+          b1 = fmaxf(b1, c[i]);
+        }
+        for (int o = 1; o < lpg; o <<= 1) {
+          const float o1 = __shfl_xor_sync(0xffffffffu, b1, o);
+          const float o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+          b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+          b1 = fmaxf(b1, o1);
+        }
+        const float v = P.group_select_mode == 0 ? b1 : b1 + b2;
+        gk = __shfl_sync(0xffffffffu, v, seg0 + min(sl * lpg, LPT - 1));
+      } else {
+        float* row_c = reinterpret_cast<float*>(sm) + (seg0 / LPT) * E;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (e0 + i < E) row_c[e0 + i] = c[i];
+        __syncwarp();
+        if (sl < G) {
+          float b1 = -INFINITY, b2 = -INFINITY;
+          for (int j = 0; j < gs; ++j) {
+            const float v = row_c[sl * gs + j];
+            b2 = fmaxf(b2, fminf(b1, v));
+            b1 = fmaxf(b1, v);
+          }
+          gk = P.group_select_mode == 0 ? b1 : b1 + b2;
+        }
+        __syncwarp();
+      }
+      if (sl >= G) gk = -INFINITY;
+      // rank among the groups, and the groups too close to tell apart
+      const float gerr = 3.0f * (kerr * p1 + 1.2e-7f * fabsf(gk));
+      int rank = 0;
+      uint32_t near = 0;
+      for (int h = 0; h < G; ++h) {
+        const float o = __shfl_sync(0xffffffffu, gk, seg0 + h);
+        rank += (o > gk || (o == gk && h < sl)) ? 1 : 0;
+        if (h != sl && !(fabsf(o - gk) > gerr)) near |= 1u << h;
+      }
+      const uint32_t all = __ballot_sync(0xffffffffu, sl < G && rank < P.k_group);
+      kept = LPT == 32 ? all : (all >> seg0) & ((1u << (LPT & 31)) - 1u);
+      const bool mine = (kept >> sl) & 1u;
+      bad |= sl < G && (mine ? near & ~kept : near & kept) != 0u;
+    }
+    // ---- keys ----
+    uint32_t key[EPL];
+    {
+      int g = P.k_group < G ? e0 / gs : 0, r = P.k_group < G ? e0 - g * gs : 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (P.k_group < G && r == gs) {
+          r = 0;
+          ++g;
+        }
+        ++r;
+        const bool in = e0 + i < E && (P.k_group == G || ((kept >> g) & 1u));
+        key[i] = in ? (rb_key(c[i]) & ~MASK) | (MASK - (e0 + i)) : 0u;
+      }
+    }
+    // ---- top_k + 2 rounds ----
+    uint32_t best = key[0], mine = 0, last = 0;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+    for (int r = 0; r < k + 2; ++r) {
+      last = rb_seg_max<LPT>(best);
+      if (sl == r) mine = last;
+      // the largest key below best: the differences wrap, so that the nearest
+      // one below is the largest (0, nothing left, comes out as 0)
+      uint32_t d = key[0] - best;
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) d = max(d, key[i] - best);
+      const uint32_t next = best + d;
+      if (best == last) best = next < best ? next : 0u;
+    }
+    // ---- the candidates' own c, in order ----
+    int e = mine ? static_cast<int>(MASK - (mine & MASK)) : 0x7fffffff;
+    float l = mine ? rb_f32(row[e]) : -INFINITY, be = mine ? __ldg(bias + e) : 0.f;
+    float ce = -INFINITY;
+    if (l != -INFINITY)
+      ce = softmax ? fmaf(expf(l - mx), cf, be) : __fdividef(1.0f, 1.0f + expf(-l)) + be;
+    float cn = __shfl_down_sync(0xffffffffu, ce, 1, LPT);
+    // (keys with the same high bits may come out in the wrong order)
+    if (__any_sync(0xffffffffu, sl < k + 1 && cn > ce)) {
+#pragma unroll
+      for (int pass = 0; pass < 3; ++pass) {
+        const int other = pass == 1 ? ((sl + 1) ^ 1) - 1 : sl ^ 1;
+        const int from = seg0 + min(max(other, 0), LPT - 1);
+        const float co = __shfl_sync(0xffffffffu, ce, from), lo = __shfl_sync(0xffffffffu, l, from),
+                    bo = __shfl_sync(0xffffffffu, be, from);
+        const int eo = __shfl_sync(0xffffffffu, e, from);
+        const bool front = other > sl;  // this lane keeps the better of the two
+        const bool better = co > ce || (co == ce && eo < e);
+        const bool worse = co < ce || (co == ce && eo > e);
+        if (other >= 0 && other < LPT && (front ? better : worse)) {
+          ce = co;
+          l = lo;
+          be = bo;
+          e = eo;
+        }
+      }
+      cn = __shfl_down_sync(0xffffffffu, ce, 1, LPT);
+    }
+    const float ln = __shfl_down_sync(0xffffffffu, l, 1, LPT);
+    const float bn = __shfl_down_sync(0xffffffffu, be, 1, LPT);
+    const int en = __shfl_down_sync(0xffffffffu, e, 1, LPT);
+    const float err = kerr * p1 + 1.2e-7f * fabsf(ce);
+    const bool tie = l == ln && be == bn && e < en;
+    if (sl < k && !(ce - cn > err) && !tie) bad = true;
+    if (sl == k - 1 && last != 0u && !(ce - rb_value(last | MASK) > err)) bad = true;
+    const uint32_t bads = __ballot_sync(0xffffffffu, bad && live);
+    // ---- weights (as rb_weights) ----
+    const bool chosen = sl < k;
+    const bool renorm = !softmax || P.renormalize;
+    const float top = renorm ? rb_seg_max<LPT>(chosen ? l : -INFINITY) : mx;
+    float p = (!softmax && top >= -60.f) ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
+    if (!chosen) p = 0.f;
+    const float total = renorm ? rb_seg_sum<LPT>(p) : sum;
+    const uint32_t seg_bad = LPT == 32 ? bads : (bads >> seg0) & ((1u << (LPT & 31)) - 1u);
+    if (chosen && live && seg_bad == 0u) {
+      out_w[t * k + sl] = p / total * P.scale;
+      out_ids[t * k + sl] = e;
+    }
+    // ---- tokens that fp32 does not decide ----
+    if (bads != 0u) {
+#pragma unroll
+      for (int s = 0; s < TPW; ++s) {
+        const uint32_t part = LPT == 32 ? bads : (bads >> (s * LPT)) & ((1u << (LPT & 31)) - 1u);
+        if (part == 0u) continue;
+        const int64_t tb = t0 + s;
+        const T* rb = logits + tb * E;
+        int id0 = 0, id1 = 0;
+        __syncwarp();
+        rb_choose64(rb, bias, P, sm, id0, id1);
+        rb_weights(rb, P, id0, id1, __shfl_sync(0xffffffffu, mx, s * LPT),
+                   __shfl_sync(0xffffffffu, sum, s * LPT), out_w + tb * k, out_ids + tb * k);
+        __syncwarp();
+      }
+    }
+  }
+}
+
+// Gradient with respect to the logits of sum_j gw_j w_j.
 // With v_j = w_j / scale and u_j the chosen log scores,
 //   renormalised:  v = softmax(u),  du_j = scale v_j (gw_j - sum_i v_i gw_i)
 //     softmax: dl = du at the chosen logits (the row's own sum cancels)
 //     sigmoid: dl = du sigma(-l)
 //   softmax as it is: v_j = p_j,  dl_e = scale (sum_j [id_j = e] gw_j p_e - p_e sum_i gw_i p_i)
-template <typename T>
+//
+// Registers hold a token's row: LPT lanes per token (two tokens per warp up to
+// 256 experts and 16 items, else one), EPL consecutive experts per lane.  The
+// row goes out in 16-byte stores with what every entry has (0, or -p_e times
+// the dot product), then the lanes of the items store their experts' entries
+// over it.
+template <int N>
+__device__ __forceinline__ void rg_store(float* p, const float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) *reinterpret_cast<float2*>(p + i) = make_float2(v[i], v[i + 1]);
+  }
+}
+__device__ __forceinline__ uint32_t rg_pack(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+template <int N>
+__device__ __forceinline__ void rg_store(bf16* p, const float (&v)[N]) {
+  if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      *reinterpret_cast<uint4*>(p + i) =
+          make_uint4(rg_pack(v[i], v[i + 1]), rg_pack(v[i + 2], v[i + 3]),
+                     rg_pack(v[i + 4], v[i + 5]), rg_pack(v[i + 6], v[i + 7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      *reinterpret_cast<uint32_t*>(p + i) = rg_pack(v[i], v[i + 1]);
+  }
+}
+
+template <int EPL, int LPT, typename T>
 __global__ void __launch_bounds__(kRbWarps * 32)
     route_backward_kernel(const float* __restrict__ gw, const T* __restrict__ logits,
+                          const int32_t* __restrict__ ids, RbParams P, int vec,
+                          T* __restrict__ out, int32_t* error_word) {
+  pdl_begin();
+  const int lane = threadIdx.x & 31, sl = lane % LPT;
+  const int64_t warp0 = static_cast<int64_t>(blockIdx.x) * kRbWarps + (threadIdx.x >> 5);
+  const int64_t token = warp0 * (32 / LPT) + lane / LPT;
+  const bool live = token < P.M;
+  const int64_t t = live ? token : P.M - 1;
+  const int E = P.E, k = P.top_k, e0 = sl * EPL;
+  const T* row = logits + t * E;
+  // the lane's item
+  int id = sl < k ? ids[t * k + sl] : -1;
+  if (sl < k && (id < 0 || id >= E)) {
+    if (live) record_error(error_word, MOE_ERR_BAD_EXPERT_ID);
+    id = -1;
+  }
+  const float l = id >= 0 ? rb_f32(row[id]) : -INFINITY;
+  const float g = id >= 0 ? gw[t * k + sl] : 0.f;
+  float v[EPL];
+  float d;            // the item's own part of its expert's entry
+  float base = 0.f;   // what the entry has without it
+  if (P.method == MOE_ROUTE_SOFTMAX && !P.renormalize) {
+    if (vec && e0 < E) {
+      rb_load<EPL>(row + e0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = e0 + i < E ? rb_f32(row[e0 + i]) : -INFINITY;
+    }
+    float mx = v[0], s = 0.f;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, v[i]);
+    mx = rb_seg_max<LPT>(mx);
+    const bool none = mx == -INFINITY;  // nothing but masked experts (or NaN, which stays)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      v[i] = none && v[i] == -INFINITY ? 0.f : expf(v[i] - mx);
+      s += v[i];
+    }
+    s = rb_seg_sum<LPT>(s);
+    const float inv = s == 0.f ? 0.f : 1.0f / s;
+    const float p = l == -INFINITY ? 0.f : expf(l - mx) * inv;
+    d = P.scale * p * g;
+    const float dot = rb_seg_sum<LPT>(d);
+    base = -p * dot;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = -(v[i] * inv) * dot;
+  } else {
+    const bool sigmoid = P.method == MOE_ROUTE_SIGMOID;
+    const float u = sigmoid ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
+    const float mx = rb_seg_max<LPT>(u);
+    const float e = (id < 0 || mx == -INFINITY) && !(l != l) ? 0.f : expf(u - mx);
+    const float s = rb_seg_sum<LPT>(e);
+    const float w = e * (s == 0.f ? 0.f : 1.0f / s);
+    const float dot = rb_seg_sum<LPT>(w * g);
+    d = P.scale * w * (g - dot);
+    if (sigmoid) d *= 1.0f / (1.0f + expf(l));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = 0.f;
+  }
+  // an expert named twice: its first item's lane adds the others' parts, in order
+  const unsigned same =
+      __match_any_sync(0xffffffffu, id >= 0 ? id | (lane / LPT) << 16 : -1 - lane);
+  if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+    float all = 0.f;
+    for (int j = 0; j < 32; ++j) {
+      const float o = __shfl_sync(0xffffffffu, d, j);
+      if ((same >> j) & 1u) all += o;
+    }
+    d = all;
+  }
+  T* dst = out + t * E;
+  if (live) {
+    if (vec) {
+      if (e0 < E) rg_store<EPL>(dst + e0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (e0 + i < E) rb_store(dst + e0 + i, v[i]);
+    }
+  }
+  __syncwarp();
+  if (live && id >= 0 && lane == __ffs(same) - 1) rb_store(dst + id, base + d);
+}
+
+// More than 32 items per token: one warp per token, the row in shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kRbWarps * 32)
+    route_backward_wide_kernel(const float* __restrict__ gw, const T* __restrict__ logits,
                           const int32_t* __restrict__ ids, RbParams P, T* __restrict__ out,
                           int32_t* error_word) {
   pdl_begin();
@@ -265,28 +698,62 @@ __global__ void __launch_bounds__(kRbWarps * 32)
   for (int e = lane; e < E; e += 32) rb_store(out + t * E + e, acc[e]);
 }
 
-}  // namespace
+// Blocks and shared memory of a launch over the tokens: warps per block so
+// that 48 KB hold their 64-bit values.
+int rb_warps(const RouteArgs& a) { return a.E + a.group_count <= 1536 ? kRbWarps : kRbWarps / 2; }
 
-moe_status_t launch_route_biased(const RouteArgs& a, const float* bias, cudaStream_t s) {
-  // 48 KB of shared memory hold the four warps' values up to 1536 of them each
-  const int warps = a.E + a.group_count <= 1536 ? kRbWarps : kRbWarps / 2;
-  const int64_t blocks = ceil_div<int64_t>(a.M, warps);
-  const RbParams P{a.M, a.E, a.top_k, a.method, a.renormalize, a.k_group, a.group_count,
-                   a.group_select_mode, a.scale};
+template <int EPL, int LPT, typename T>
+void launch_fast(const RouteArgs& a, const float* bias, const RbParams& P, cudaStream_t s) {
+  const int warps = rb_warps(a);
   const size_t smem = static_cast<size_t>(warps) * (a.E + a.group_count) * sizeof(double);
-  prof_before("route_biased", s);
-  if (a.logits_bf16)
-    launch_kernel(route_biased_kernel<bf16>, static_cast<unsigned>(blocks), warps * 32, smem, s,
-                  static_cast<const bf16*>(a.logits), bias, P, a.weights, a.ids);
-  else
-    launch_kernel(route_biased_kernel<float>, static_cast<unsigned>(blocks), warps * 32, smem, s,
-                  static_cast<const float*>(a.logits), bias, P, a.weights, a.ids);
-  prof_after("route_biased", s);
-  return check_launch("route_biased");
+  const int64_t blocks = ceil_div<int64_t>(a.M, warps * (32 / LPT));
+  // whole lanes of experts, and 16-byte (for few experts narrower) aligned loads of them
+  const int bytes = EPL * static_cast<int>(sizeof(T)) < 16 ? EPL * static_cast<int>(sizeof(T)) : 16;
+  const int vec = a.E % EPL == 0 && (a.E * sizeof(T)) % bytes == 0 &&
+                  reinterpret_cast<uintptr_t>(a.logits) % bytes == 0;
+  launch_kernel(route_biased_kernel<EPL, LPT, T>,
+                static_cast<unsigned>(std::min<int64_t>(blocks, 152 * 16)), warps * 32, smem, s,
+                static_cast<const T*>(a.logits), bias, P, vec, a.weights, a.ids);
 }
 
-moe_status_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
-  const int64_t blocks = ceil_div<int64_t>(a.M, kRbWarps);
+template <typename T>
+void launch_biased(const RouteArgs& a, const float* bias, cudaStream_t s) {
+  const RbParams P{a.M, a.E, a.top_k, a.method, a.renormalize, a.k_group, a.group_count,
+                   a.group_select_mode, a.scale};
+  const bool grouped = a.k_group < a.group_count;
+  // a candidate per lane (two beyond top_k), a group per lane
+  if (a.E <= 256 && a.top_k <= 14 && (!grouped || a.group_count <= 16)) {
+    if (a.E <= 32) return launch_fast<2, 16, T>(a, bias, P, s);
+    if (a.E <= 64) return launch_fast<4, 16, T>(a, bias, P, s);
+    if (a.E <= 128) return launch_fast<8, 16, T>(a, bias, P, s);
+    return launch_fast<16, 16, T>(a, bias, P, s);
+  }
+  if (a.top_k <= 30 && (!grouped || a.group_count <= 32)) {
+    if (a.E <= 128) return launch_fast<4, 32, T>(a, bias, P, s);
+    if (a.E <= 256) return launch_fast<8, 32, T>(a, bias, P, s);
+    if (a.E <= 512) return launch_fast<16, 32, T>(a, bias, P, s);
+    return launch_fast<32, 32, T>(a, bias, P, s);
+  }
+  const int warps = rb_warps(a);
+  launch_kernel(route_biased_exact_kernel<T>, static_cast<unsigned>(ceil_div<int64_t>(a.M, warps)),
+                warps * 32, static_cast<size_t>(warps) * (a.E + a.group_count) * sizeof(double), s,
+                static_cast<const T*>(a.logits), bias, P, a.weights, a.ids);
+}
+
+template <int EPL, int LPT, typename T>
+void launch_rg(const RouteBackwardArgs& a, const RbParams& P, cudaStream_t s) {
+  const int bytes = EPL * static_cast<int>(sizeof(T)) < 16 ? EPL * static_cast<int>(sizeof(T)) : 16;
+  const int vec = a.E % EPL == 0 && (a.E * sizeof(T)) % bytes == 0 &&
+                  reinterpret_cast<uintptr_t>(a.logits) % bytes == 0 &&
+                  reinterpret_cast<uintptr_t>(a.grad_logits) % bytes == 0;
+  launch_kernel(route_backward_kernel<EPL, LPT, T>,
+                static_cast<unsigned>(ceil_div<int64_t>(a.M, kRbWarps * (32 / LPT))), kRbWarps * 32,
+                0, s, a.grad_weights, static_cast<const T*>(a.logits), a.ids, P, vec,
+                static_cast<T*>(a.grad_logits), a.error_word);
+}
+
+template <typename T>
+void launch_backward(const RouteBackwardArgs& a, cudaStream_t s) {
   RbParams P{};
   P.M = a.M;
   P.E = a.E;
@@ -294,16 +761,41 @@ moe_status_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
   P.method = a.method;
   P.renormalize = a.renormalize;
   P.scale = a.scale;
-  const size_t smem = static_cast<size_t>(kRbWarps) * a.E * sizeof(float);
+  if (a.top_k <= 16 && a.E <= 256) {
+    if (a.E <= 32) return launch_rg<2, 16, T>(a, P, s);
+    if (a.E <= 128) return launch_rg<8, 16, T>(a, P, s);
+    return launch_rg<16, 16, T>(a, P, s);
+  }
+  if (a.top_k <= 32) {
+    if (a.E <= 256) return launch_rg<8, 32, T>(a, P, s);
+    if (a.E <= 512) return launch_rg<16, 32, T>(a, P, s);
+    return launch_rg<32, 32, T>(a, P, s);
+  }
+  launch_kernel(route_backward_wide_kernel<T>,
+                static_cast<unsigned>(ceil_div<int64_t>(a.M, kRbWarps)), kRbWarps * 32,
+                static_cast<size_t>(kRbWarps) * a.E * sizeof(float), s, a.grad_weights,
+                static_cast<const T*>(a.logits), a.ids, P, static_cast<T*>(a.grad_logits),
+                a.error_word);
+}
+
+}  // namespace
+
+moe_status_t launch_route_biased(const RouteArgs& a, const float* bias, cudaStream_t s) {
+  prof_before("route_biased", s);
+  if (a.logits_bf16)
+    launch_biased<bf16>(a, bias, s);
+  else
+    launch_biased<float>(a, bias, s);
+  prof_after("route_biased", s);
+  return check_launch("route_biased");
+}
+
+moe_status_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
   prof_before("route_backward", s);
   if (a.logits_bf16)
-    launch_kernel(route_backward_kernel<bf16>, static_cast<unsigned>(blocks), kRbWarps * 32, smem, s,
-                  a.grad_weights, static_cast<const bf16*>(a.logits), a.ids, P,
-                  static_cast<bf16*>(a.grad_logits), a.error_word);
+    launch_backward<bf16>(a, s);
   else
-    launch_kernel(route_backward_kernel<float>, static_cast<unsigned>(blocks), kRbWarps * 32, smem,
-                  s, a.grad_weights, static_cast<const float*>(a.logits), a.ids, P,
-                  static_cast<float*>(a.grad_logits), a.error_word);
+    launch_backward<float>(a, s);
   prof_after("route_backward", s);
   return check_launch("route_backward");
 }
