@@ -101,6 +101,9 @@ def test_quant_groups_swiglu_saturated_gates():
     assert torch.isfinite(s).all() and torch.isfinite(q.float()).all()
     v = q.float()[0, :8] * s[0, 0]
     assert (v[:6] == 0).all() and abs(v[6].item() / 1e30 - 1) < 0.01
+    x[0, 3], x[0, 130] = float("inf"), 2.0                    # an infinite gate, a finite up
+    q, s = pkg.moe_quant_groups_fp8(x, swiglu=True)
+    assert torch.isinf(s[0, 0]) and torch.isnan(q.float()[0, 3]) and q.float()[0, 2] == 0
 
 
 def test_quant_groups_views_and_rows_behind():
