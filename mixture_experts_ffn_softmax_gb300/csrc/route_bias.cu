@@ -38,103 +38,137 @@ struct RbParams {
   float scale;
 };
 
-// Best (value, index) over the warp, ties to the lower index.
-__device__ __forceinline__ void rb_warp_best(double& v, int& i) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
-    const int i2 = __shfl_xor_sync(0xffffffffu, i, o);
-    if (v2 > v || (v2 == v && i2 < i)) {
-      v = v2;
-      i = i2;
-    }
-  }
+// Order-preserving map of a double to an unsigned key, and back; NaN goes with
+// -inf, and 0 is below every key.  (Comparisons of doubles run at this GPU's
+// FP64 rate: the choice below took 30 us per token with them.)
+__device__ __forceinline__ uint64_t rb_key64(double v) {
+  if (!(v == v)) v = -INFINITY;
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+  return (b >> 63) ? ~b : (b | (uint64_t(1) << 63));
+}
+__device__ __forceinline__ double rb_value64(uint64_t k) {
+  return __longlong_as_double(
+      static_cast<long long>((k >> 63) ? k & ~(uint64_t(1) << 63) : ~k));
 }
 
-// One token's choice in 64 bits, by one warp.  c: E + group_count doubles of
+// A score in 64 bits: sigmoid, or exp(l - m).  (One warp-wide FP64 operation
+// takes 64 cycles here, a sigmoid about 2000: the paths below call this for as
+// few experts as they can.)
+__device__ __noinline__ double rb_score64(float l, bool softmax, float m) {
+  const double e = exp(softmax ? static_cast<double>(l) - m : -static_cast<double>(l));
+  return softmax ? e : 1.0 / (1.0 + e);
+}
+
+// Largest key over the warp; i: the lowest index among the lanes that have it.
+__device__ __forceinline__ uint64_t rb_warp_best(uint64_t v, int& i) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = __reduce_max_sync(
+      0xffffffffu, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  const uint64_t best = static_cast<uint64_t>(hi) << 32 | lo;
+  i = static_cast<int>(
+      __reduce_min_sync(0xffffffffu, v == best ? static_cast<uint32_t>(i) : 0x7fffffffu));
+  return best;
+}
+
+// The largest of keys c[first], c[first + 32], ... below n, and its index
+// (the lowest of equals).
+__device__ __forceinline__ uint64_t rb_scan(const uint64_t* c, int first, int n, int& i) {
+  uint64_t v = 0;
+  i = 0x7fffffff;
+#pragma unroll 4
+  for (int e = first; e < n; e += 32)
+    if (c[e] > v) {
+      v = c[e];
+      i = e;
+    }
+  return v;
+}
+
+// One token's choice in 64 bits, by one warp.  c: E + group_count keys in
 // shared memory.  Lane j receives chosen experts j and j + 32.  A candidate
-// that is out (its group not kept, or chosen) is marked by NaN; a masked
-// expert (logit -inf) or a NaN score has c = -inf and comes last.
+// that is out (its group not kept, or chosen) has key 0; a masked expert
+// (logit -inf) or a NaN score has that of -inf and comes last.
 template <typename T>
-__device__ void rb_choose64(const T* row, const float* bias, const RbParams& P, double* c, int& id0,
-                            int& id1) {
+__device__ __noinline__ int2 rb_choose64(const T* row, const float* bias, const RbParams& P,
+                                         uint64_t* c) {
   const int lane = threadIdx.x & 31;
   const int E = P.E;
-  double m = 0.0, inv = 1.0;
-  if (P.method == MOE_ROUTE_SOFTMAX) {
-    float mf = -INFINITY;
-    for (int e = lane; e < E; e += 32) mf = fmaxf(mf, rb_f32(row[e]));
-    m = rb_max(mf);
+  const bool softmax = P.method == MOE_ROUTE_SOFTMAX;
+  float m = 0.f;
+  double inv = 1.0;
+  if (softmax) {
+    m = -INFINITY;
+    for (int e = lane; e < E; e += 32) m = fmaxf(m, rb_f32(row[e]));
+    m = rb_max(m);
     double s = 0.0;
-    for (int e = lane; e < E; e += 32) s += exp(static_cast<double>(rb_f32(row[e])) - m);
+    for (int e = lane; e < E; e += 32) s += rb_score64(rb_f32(row[e]), true, m);
     inv = 1.0 / rb_sum(s);
   }
+#pragma unroll 1
   for (int e = lane; e < E; e += 32) {
-    const double l = rb_f32(row[e]);
-    const double p = P.method == MOE_ROUTE_SOFTMAX ? exp(l - m) * inv : 1.0 / (1.0 + exp(-l));
-    const double v = p + static_cast<double>(bias[e]);
-    c[e] = (l == -INFINITY || !(v == v)) ? -INFINITY : v;
+    const float l = rb_f32(row[e]);
+    c[e] = rb_key64(l == -INFINITY ? -INFINITY
+                                   : fma(rb_score64(l, softmax, m), inv,
+                                         static_cast<double>(bias[e])) + 0.0);
   }
   __syncwarp();
   if (P.group_count > 1) {
     const int G = P.group_count, gs = E / G;
-    double* gk = c + E;
+    uint64_t* gk = c + E;
     for (int g = lane; g < G; g += 32) {
-      double b1 = -INFINITY, b2 = -INFINITY;
+      uint64_t b1 = 0, b2 = 0;
+#pragma unroll 4
       for (int j = 0; j < gs; ++j) {
-        const double v = c[g * gs + j];
-        if (v > b1) {
-          b2 = b1;
-          b1 = v;
-        } else if (v > b2) {
-          b2 = v;
-        }
+        const uint64_t v = c[g * gs + j];
+        b2 = max(b2, min(b1, v));
+        b1 = max(b1, v);
       }
-      gk[g] = P.group_select_mode == 0 ? b1 : b1 + b2;
+      gk[g] = P.group_select_mode == 0 ? b1 : rb_key64(rb_value64(b1) + rb_value64(b2));
     }
     __syncwarp();
-    // the k_group best groups leave gk (NaN); what is left there is dropped
+    // the k_group best groups leave gk (0); what is left there is dropped
     for (int r = 0; r < P.k_group; ++r) {
-      double v = -INFINITY;
-      int i = 0x7fffffff;
-      for (int g = lane; g < G; g += 32)
-        if (gk[g] > v || (gk[g] == v && g < i)) {
-          v = gk[g];
-          i = g;
-        }
-      rb_warp_best(v, i);
-      if (lane == 0) gk[i] = NAN;
+      int i;
+      rb_warp_best(rb_scan(gk, lane, G, i), i);
+      if (lane == 0) gk[i] = 0;
       __syncwarp();
     }
     for (int e = lane; e < E; e += 32)
-      if (gk[e / gs] == gk[e / gs]) c[e] = NAN;
+      if (gk[e / gs] != 0) c[e] = 0;
     __syncwarp();
   }
+  int2 id = make_int2(0, 0);
+  int mine;
+  uint64_t v = rb_scan(c, lane, E, mine);
   for (int j = 0; j < P.top_k; ++j) {
-    double v = -INFINITY;
-    int i = 0x7fffffff;
-    for (int e = lane; e < E; e += 32)
-      if (c[e] > v || (c[e] == v && e < i)) {
-        v = c[e];
-        i = e;
-      }
+    int i = mine;
     rb_warp_best(v, i);
-    if (lane == 0) c[i] = NAN;
-    if (lane == (j & 31)) (j < 32 ? id0 : id1) = i;
-    __syncwarp();
+    if (lane == (j & 31)) (j < 32 ? id.x : id.y) = i;
+    if (i == mine) {  // this lane's: the next best of its experts
+      c[i] = 0;
+      v = rb_scan(c, lane, E, mine);
+    }
   }
+  return id;
 }
 
 // Weights of the chosen experts (lane j: chosen j and j + 32), in fp32.
 // Ratios of the chosen scores come from the logits' differences where the
 // scores themselves would underflow; a masked expert's weight is 0, and a
 // token with nothing but masked experts has weights of 0.
-// softmax: mx the row's largest logit and sum that of exp(l - mx) over it
-// (NaN where the row holds a NaN or +inf).
 template <typename T>
-__device__ __forceinline__ void rb_weights(const T* row, const RbParams& P, int id0, int id1,
-                                           float mx, float sum, float* out_w, int32_t* out_ids) {
+__device__ __noinline__ void rb_weights(const T* row, const RbParams& P, int id0, int id1,
+                                        float* out_w, int32_t* out_ids) {
   const int lane = threadIdx.x & 31;
+  // softmax: the row's largest logit and the sum of exp(l - mx) over it (NaN
+  // where the row holds a NaN or +inf)
+  float mx = -INFINITY, sum = 0.f;
+  if (P.method == MOE_ROUTE_SOFTMAX) {
+    for (int e = lane; e < P.E; e += 32) mx = fmaxf(mx, rb_f32(row[e]));
+    mx = rb_max(mx);
+    for (int e = lane; e < P.E; e += 32) sum += expf(rb_f32(row[e]) - mx);
+    sum = rb_sum(sum);
+  }
   const bool h0 = lane < P.top_k, h1 = lane + 32 < P.top_k;
   const float l0 = h0 ? rb_f32(row[id0]) : -INFINITY, l1 = h1 ? rb_f32(row[id1]) : -INFINITY;
   const bool masked = __all_sync(0xffffffffu, l0 == -INFINITY && l1 == -INFINITY);
@@ -169,30 +203,67 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     route_biased_exact_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
                         float* __restrict__ out_w, int32_t* __restrict__ out_ids) {
   pdl_begin();
-  extern __shared__ double rb_smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  extern __shared__ uint64_t rb_smem[];
+  const int warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
   if (t >= P.M) return;
   const T* row = logits + t * P.E;
-  int id0 = 0, id1 = 0;
-  rb_choose64(row, bias, P, rb_smem + warp * (P.E + P.group_count), id0, id1);
-  float mx = -INFINITY, sum = 0.f;
-  if (P.method == MOE_ROUTE_SOFTMAX) {
-    for (int e = lane; e < P.E; e += 32) mx = fmaxf(mx, rb_f32(row[e]));
-    mx = rb_max(mx);
-    for (int e = lane; e < P.E; e += 32) sum += expf(rb_f32(row[e]) - mx);
-    sum = rb_sum(sum);
-  }
-  rb_weights(row, P, id0, id1, mx, sum, out_w + t * P.top_k, out_ids + t * P.top_k);
+  const int2 id = rb_choose64(row, bias, P, rb_smem + warp * (P.E + P.group_count));
+  rb_weights(row, P, id.x, id.y, out_w + t * P.top_k, out_ids + t * P.top_k);
 }
 
-// Order-preserving map of a float (not NaN) to an unsigned key, and back.
+// Order-preserving map of a float (neither NaN nor -0) to an unsigned key, and back.
 __device__ __forceinline__ uint32_t rb_key(float f) {
-  const uint32_t b = f == 0.0f ? 0u : __float_as_uint(f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t b = __float_as_uint(f);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float rb_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// 2^x (within 2^-22 of it) and 1 / x (within 2^-23), relative.
+__device__ __forceinline__ float rb_ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rb_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// The N largest keys of a lane in descending order, from EPL of them.
+__device__ __forceinline__ void rb_order(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+__device__ __forceinline__ void rb_sort4(uint32_t (&t)[4]) {
+  rb_order(t[0], t[1]);
+  rb_order(t[2], t[3]);
+  rb_order(t[0], t[2]);
+  rb_order(t[1], t[3]);
+  rb_order(t[1], t[2]);
+}
+template <int EPL>
+__device__ __forceinline__ void rb_top4(const uint32_t (&key)[EPL], uint32_t (&t)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = i < EPL ? key[i] : 0u;
+  rb_sort4(t);
+#pragma unroll
+  for (int q = 4; q < EPL; q += 4) {
+    uint32_t u[4] = {key[q], key[q + 1], key[q + 2], key[q + 3]};
+    rb_sort4(u);
+    // the larger half of two sorted quads, a bitonic sequence again
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = max(t[i], u[3 - i]);
+    rb_order(t[0], t[2]);
+    rb_order(t[1], t[3]);
+    rb_order(t[0], t[1]);
+    rb_order(t[2], t[3]);
+  }
 }
 
 template <int LPT, typename F>
@@ -253,40 +324,46 @@ __device__ __forceinline__ void rb_load(const bf16* p, float (&l)[N]) {
   }
 }
 
-// The choice in fp32 where fp32 decides it, else as rb_choose64 does.
+// The choice in fp32 where fp32 decides it.
 //
 // LPT lanes per token, EPL consecutive experts per lane.  A candidate is one
 // 32-bit key: c in order-preserving form with its low bits replaced by the
 // expert (complemented: the lower id wins), so that a maximum over the lanes
-// is a chosen expert; each lane offers its largest key below the last one it
-// gave.  top_k + 2 rounds leave a candidate per lane.  Their exact fp32 c (the
-// keys' low bits back) puts them in order, and the choice stands if no two
-// neighbours down to the (top_k + 1)-th are closer than the error of c, nor
-// the top_k-th and what was not a candidate; equal logits with equal biases
-// are ties for certain.  Otherwise (0.3 % of the tokens of 256 normally
-// distributed sigmoid scores), or where a score is NaN, the warp takes the
-// token by rb_choose64.
+// is a chosen expert; each lane offers its four largest in turn, and past those
+// its largest below the last one it gave.  top_k + 2 rounds leave a candidate
+// per lane.  Their exact fp32 c (the keys' low bits back) puts them in order,
+// and the choice stands if no two neighbours down to the (top_k + 1)-th are
+// closer than the error of c, nor the top_k-th and what was not a candidate;
+// equal logits with equal biases are ties for certain.  If only candidates
+// are too close (a token in a thousand of normally distributed scores), the
+// lanes rank them in 64 bits, and sigmoid groups that are too close likewise;
+// where that does not settle it, or a score is NaN, the warp takes the token by
+// rb_choose64.
+//
+// WHOLE: lanes hold EPL experts or none, of one group (a power of two of lanes
+// to a group).
 //
 // Bound: issue slots.  8192 tokens x 256 experts, 8 of 4 of 8 groups, from
-// 281 us (every token by rb_choose64) to 35 us a call; 16384 x 128 bf16, 8
-// chosen, 298 to 23 us.
-template <int EPL, int LPT, typename T>
+// 281 us (every token by rb_choose64) to 11.5 us; 16384 x 128 bf16, 8 chosen,
+// 298 to 11 us.
+template <int EPL, int LPT, bool WHOLE, typename T>
 __global__ void __launch_bounds__(kRbWarps * 32)
     route_biased_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
                         int vec, float* __restrict__ out_w, int32_t* __restrict__ out_ids) {
   pdl_begin();
-  extern __shared__ double rb_smem[];
+  extern __shared__ uint64_t rb_smem[];
   constexpr int TPW = 32 / LPT;
   constexpr uint32_t MASK = LPT * EPL - 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sl = lane % LPT, seg0 = lane - sl;
-  const int E = P.E, G = P.group_count, k = P.top_k;
-  const bool softmax = P.method == MOE_ROUTE_SOFTMAX;
-  const int e0 = sl * EPL;
-  double* sm = rb_smem + warp * (E + G);
+  const int E = P.E, G = P.group_count, k = P.top_k, gs = E / G;
+  const bool softmax = P.method == MOE_ROUTE_SOFTMAX, grouped = P.k_group < G;
+  const int e0 = sl * EPL, g0 = e0 / gs;
+  auto exists = [&](int i) { return WHOLE ? e0 < E : e0 + i < E; };
+  uint64_t* sm = rb_smem + warp * (E + G);
   float b[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) b[i] = e0 + i < E ? __ldg(bias + e0 + i) : 0.f;
+  for (int i = 0; i < EPL; ++i) b[i] = exists(i) ? __ldg(bias + e0 + i) : 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) * TPW;
   for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * TPW; t0 < P.M;
        t0 += step) {
@@ -298,60 +375,54 @@ __global__ void __launch_bounds__(kRbWarps * 32)
       rb_load<EPL>(row + e0, c);
     } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) c[i] = e0 + i < E ? rb_f32(row[e0 + i]) : -INFINITY;
+      for (int i = 0; i < EPL; ++i) c[i] = exists(i) ? rb_f32(row[e0 + i]) : -INFINITY;
     }
-    // ---- c = p + b; P1: the largest p, cf: p = exp(l - mx) cf ----
-    float mx = 0.f, sum = 1.f, cf = 1.f;
+    // ---- c = p + b (p = exp(l - mx) cf for softmax) ----
+    float lo = c[0], mx = c[0], mx2 = 0.f, sum = 0.f, cf = 1.f;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) lo = fminf(lo, c[i]);
     if (softmax) {
-      mx = c[0];
 #pragma unroll
       for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, c[i]);
       mx = rb_seg_max<LPT>(mx);
-      sum = 0.f;
-    }
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const float l = c[i];
-      float p;
-      if (softmax) {
-        p = expf(l - mx);
-        if (e0 + i < E) sum += p;
-      } else {
-        p = __fdividef(1.0f, 1.0f + expf(-l)) + b[i];
-        if (l == -INFINITY) p = -INFINITY;
-      }
-      c[i] = p;
-    }
-    if (softmax) {
-      sum = rb_seg_sum<LPT>(sum);
-      cf = 1.0f / sum;
-      // masked experts: exp is 0 for them (and for logits 100 below the
-      // largest, which are looked up again)
+      mx2 = mx * kLog2e;  // (its rounding scales every exp alike)
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const bool masked = c[i] == 0.f && e0 + i < E && rb_f32(row[e0 + i]) == -INFINITY;
-        c[i] = masked ? -INFINITY : fmaf(c[i], cf, b[i]);
+        c[i] = rb_ex2(fmaf(c[i], kLog2e, -mx2));
+        sum += c[i];
       }
+      sum = rb_seg_sum<LPT>(sum);
+      cf = 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = fmaf(c[i], cf, b[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = rb_rcp(1.0f + rb_ex2(-kLog2e * c[i])) + b[i];
+    }
+    if (lo == -INFINITY) {  // masked experts of this lane, or none at all here
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (!exists(i) || rb_f32(row[e0 + i]) == -INFINITY) c[i] = -INFINITY;
     }
     const float p1 = softmax ? cf : 1.0f;
-    // error of a difference of two c: p within 4.5 steps of 2^-22 (expf 2 ulp,
-    // 1 + e, __fdividef 2 ulp), for softmax 8 + EPL + 10 of 2^-24 (its sum);
-    // the addition of the bias
-    const float kerr = softmax ? 2.0f * (18 + EPL) * 5.9604645e-8f : 1.1e-6f;
+    // error of a difference of two c, over p1.  Sigmoid: the exponential's
+    // 2^-22 + |l| 2^-23.5 times p (1 - p) (at most 2^-23.5), the sum's 2^-24, the
+    // reciprocal's 2^-23, twice.  Softmax, in 2^-24: each exp 4 + 1, the sum's
+    // EPL + 5 additions and terms, its reciprocal and product 3, twice.  The
+    // rounding of the bias' addition is in the comparisons.
+    const float kerr = softmax ? 2.0f * (18 + EPL) * 5.9604645e-8f : 6e-7f;
+    bool hard = false;  // needs rb_choose64
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) bad |= c[i] != c[i] && e0 + i < E;
+    for (int i = 0; i < EPL; ++i) hard |= c[i] != c[i];
     // ---- groups: kept ones as a mask of the segment ----
     uint32_t kept = 0xffffffffu;
-    const int gs = E / G;
-    if (P.k_group < G) {
+    if (grouped) {
       float gk = -INFINITY;  // lane g: group g's score
-      const int lpg = gs / EPL;
-      if (gs == lpg * EPL && (lpg & (lpg - 1)) == 0) {
-        // a group is lpg whole lanes
-        float b1 = -INFINITY, b2 = -INFINITY;
+      const int lpg = gs / EPL;  // WHOLE: lanes of a group
+      if constexpr (WHOLE) {
+        float b1 = c[0], b2 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
+        for (int i = 1; i < EPL; ++i) {
           b2 = fmaxf(b2, fminf(b1, c[i]));
           b1 = fmaxf(b1, c[i]);
         }
@@ -368,10 +439,11 @@ __global__ void __launch_bounds__(kRbWarps * 32)
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (e0 + i < E) row_c[e0 + i] = c[i];
+          if (exists(i)) row_c[e0 + i] = c[i];
         __syncwarp();
         if (sl < G) {
           float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 4
           for (int j = 0; j < gs; ++j) {
             const float v = row_c[sl * gs + j];
             b2 = fmaxf(b2, fminf(b1, v));
@@ -389,57 +461,129 @@ __global__ void __launch_bounds__(kRbWarps * 32)
       for (int h = 0; h < G; ++h) {
         const float o = __shfl_sync(0xffffffffu, gk, seg0 + h);
         rank += (o > gk || (o == gk && h < sl)) ? 1 : 0;
-        if (h != sl && !(fabsf(o - gk) > gerr)) near |= 1u << h;
+        if (!(fabsf(o - gk) > gerr)) near |= 1u << h;
       }
       const uint32_t all = __ballot_sync(0xffffffffu, sl < G && rank < P.k_group);
       kept = LPT == 32 ? all : (all >> seg0) & ((1u << (LPT & 31)) - 1u);
-      const bool mine = (kept >> sl) & 1u;
-      bad |= sl < G && (mine ? near & ~kept : near & kept) != 0u;
+      // (a group's own bit is never on the other side)
+      const bool unsure = sl < G && (((kept >> sl) & 1u) ? near & ~kept : near & kept) != 0u;
+      if (!WHOLE || softmax) {
+        hard |= unsure;
+      } else if (const uint32_t which = __ballot_sync(0xffffffffu, unsure && live)) {
+        // group scores in 64 bits from each lane's two best experts, where its
+        // third is no rival of them
+        float v1 = -INFINITY, v2 = -INFINITY, v3 = -INFINITY;
+        int i1 = 0, i2 = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (c[i] > v1) {
+            v3 = v2;
+            v2 = v1;
+            i2 = i1;
+            v1 = c[i];
+            i1 = i;
+          } else if (c[i] > v2) {
+            v3 = v2;
+            v2 = c[i];
+            i2 = i;
+          } else {
+            v3 = fmaxf(v3, c[i]);
+          }
+        }
+        const bool seg_unsure =
+            (LPT == 32 ? which : (which >> seg0) & ((1u << (LPT & 31)) - 1u)) != 0u;
+        if (seg_unsure && e0 < E)
+          hard |= !((P.group_select_mode == 0 ? v1 : v2) - v3 > kerr * p1 + 1.2e-7f * fabsf(v1));
+        uint64_t q1 = 0, q2 = 0;
+        if (e0 < E) {
+          const float l1 = rb_f32(row[e0 + i1]), l2 = rb_f32(row[e0 + i2]);
+          q1 = rb_key64(l1 == -INFINITY ? -INFINITY : rb_score64(l1, false, 0.f) + __ldg(bias + e0 + i1) + 0.0);
+          q2 = rb_key64(l2 == -INFINITY ? -INFINITY : rb_score64(l2, false, 0.f) + __ldg(bias + e0 + i2) + 0.0);
+        }
+        uint64_t top = max(q1, q2), sec = min(q1, q2);
+        for (int o = 1; o < lpg; o <<= 1) {
+          const uint64_t o1 = __shfl_xor_sync(0xffffffffu, top, o);
+          const uint64_t o2 = __shfl_xor_sync(0xffffffffu, sec, o);
+          sec = max(min(top, o1), max(sec, o2));
+          top = max(top, o1);
+        }
+        if (P.group_select_mode == 1) top = rb_key64(rb_value64(top) + rb_value64(sec));
+        uint64_t g64 = __shfl_sync(0xffffffffu, top, seg0 + min(sl * lpg, LPT - 1));
+        if (sl >= G) g64 = 0;
+        rank = 0;
+#pragma unroll 1
+        for (int h = 0; h < G; ++h) {
+          const uint64_t o = __shfl_sync(0xffffffffu, g64, seg0 + h);
+          rank += (o > g64 || (o == g64 && h < sl)) ? 1 : 0;
+        }
+        const uint32_t all64 = __ballot_sync(0xffffffffu, sl < G && rank < P.k_group);
+        if (seg_unsure) kept = LPT == 32 ? all64 : (all64 >> seg0) & ((1u << (LPT & 31)) - 1u);
+      }
     }
-    // ---- keys ----
+    // ---- keys, the lane's four largest ----
     uint32_t key[EPL];
-    {
-      int g = P.k_group < G ? e0 / gs : 0, r = P.k_group < G ? e0 - g * gs : 0;
+    uint32_t top4[4];
+    if constexpr (WHOLE) {
+      // (e0 is a multiple of EPL: MASK - e0 - i is (MASK - e0) ^ i)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] = ((rb_key(c[i]) & ~MASK) | (MASK - e0)) ^ i;
+      rb_top4<EPL>(key, top4);
+      if (e0 >= E || !((kept >> (grouped ? g0 : 0)) & 1u)) top4[0] = top4[1] = top4[2] = top4[3] = 0u;
+    } else {
+      int g = g0, r = e0 - g0 * gs;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        if (P.k_group < G && r == gs) {
+        if (r == gs) {
           r = 0;
           ++g;
         }
         ++r;
-        const bool in = e0 + i < E && (P.k_group == G || ((kept >> g) & 1u));
-        key[i] = in ? (rb_key(c[i]) & ~MASK) | (MASK - (e0 + i)) : 0u;
+        const bool in = exists(i) && (!grouped || ((kept >> g) & 1u));
+        key[i] = in ? ((rb_key(c[i]) & ~MASK) | (MASK - e0)) ^ i : 0u;
       }
+      rb_top4<EPL>(key, top4);
     }
     // ---- top_k + 2 rounds ----
-    uint32_t best = key[0], mine = 0, last = 0;
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+    uint32_t mine = 0, last = 0;
+    int left = 4;  // of the lane's four
     for (int r = 0; r < k + 2; ++r) {
-      last = rb_seg_max<LPT>(best);
+      last = rb_seg_max<LPT>(top4[0]);
       if (sl == r) mine = last;
-      // the largest key below best: the differences wrap, so that the nearest
-      // one below is the largest (0, nothing left, comes out as 0)
-      uint32_t d = key[0] - best;
+      if (top4[0] == last) {
+        top4[0] = top4[1];
+        top4[1] = top4[2];
+        top4[2] = top4[3];
+        top4[3] = 0u;
+        --left;
+      }
+      if (EPL > 4 && r >= 3 && __any_sync(0xffffffffu, left == 0)) {
+        // a lane gave all four: its largest key below the last one.  (The
+        // differences wrap, so that the nearest one below is the largest;
+        // nothing left comes out as 0.)
+        if (left == 0) {
+          uint32_t d = key[0] - last;
 #pragma unroll
-      for (int i = 1; i < EPL; ++i) d = max(d, key[i] - best);
-      const uint32_t next = best + d;
-      if (best == last) best = next < best ? next : 0u;
+          for (int i = 1; i < EPL; ++i) d = max(d, key[i] - last);
+          top4[0] = last + d < last ? last + d : 0u;
+          left = 1;
+        }
+      }
     }
     // ---- the candidates' own c, in order ----
     int e = mine ? static_cast<int>(MASK - (mine & MASK)) : 0x7fffffff;
     float l = mine ? rb_f32(row[e]) : -INFINITY, be = mine ? __ldg(bias + e) : 0.f;
     float ce = -INFINITY;
     if (l != -INFINITY)
-      ce = softmax ? fmaf(expf(l - mx), cf, be) : __fdividef(1.0f, 1.0f + expf(-l)) + be;
+      ce = softmax ? fmaf(rb_ex2(fmaf(l, kLog2e, -mx2)), cf, be)
+                   : rb_rcp(1.0f + rb_ex2(-kLog2e * l)) + be;
     float cn = __shfl_down_sync(0xffffffffu, ce, 1, LPT);
     // (keys with the same high bits may come out in the wrong order)
     if (__any_sync(0xffffffffu, sl < k + 1 && cn > ce)) {
-#pragma unroll
+#pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {
         const int other = pass == 1 ? ((sl + 1) ^ 1) - 1 : sl ^ 1;
         const int from = seg0 + min(max(other, 0), LPT - 1);
-        const float co = __shfl_sync(0xffffffffu, ce, from), lo = __shfl_sync(0xffffffffu, l, from),
+        const float co = __shfl_sync(0xffffffffu, ce, from), lo2 = __shfl_sync(0xffffffffu, l, from),
                     bo = __shfl_sync(0xffffffffu, be, from);
         const int eo = __shfl_sync(0xffffffffu, e, from);
         const bool front = other > sl;  // this lane keeps the better of the two
@@ -447,7 +591,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
         const bool worse = co < ce || (co == ce && eo > e);
         if (other >= 0 && other < LPT && (front ? better : worse)) {
           ce = co;
-          l = lo;
+          l = lo2;
           be = bo;
           e = eo;
         }
@@ -459,34 +603,67 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     const int en = __shfl_down_sync(0xffffffffu, e, 1, LPT);
     const float err = kerr * p1 + 1.2e-7f * fabsf(ce);
     const bool tie = l == ln && be == bn && e < en;
-    if (sl < k && !(ce - cn > err) && !tie) bad = true;
-    if (sl == k - 1 && last != 0u && !(ce - rb_value(last | MASK) > err)) bad = true;
-    const uint32_t bads = __ballot_sync(0xffffffffu, bad && live);
+    const bool close = sl < k && !(ce - cn > err) && !tie;
+    // what is no candidate has to be below the top_k-th for certain
+    if (sl == k - 1 && last != 0u && !(ce - rb_value(last | MASK) > err)) hard = true;
+    int rank = sl;  // of the lane's candidate
+    bool open = false;
+    const uint32_t closes = __ballot_sync(0xffffffffu, close && live);
+    if (closes != 0u) {
+      // in 64 bits among the candidates.  Softmax: the sum stays in fp32, each
+      // term within 2 ulp and their additions compensated, 2^-21 in all; what
+      // that leaves open takes the 64-bit sum of rb_choose64.
+      double inv = 1.0;
+      if (softmax) {
+        float s = 0.f, comp = 0.f;
+#pragma unroll 1
+        for (int i = sl; i < E; i += LPT) {
+          const float x = expf(rb_f32(row[i]) - mx), y = s + x;
+          comp += s >= x ? (s - y) + x : (x - y) + s;
+          s = y;
+        }
+        inv = 1.0 / (static_cast<double>(rb_seg_sum<LPT>(s)) + rb_seg_sum<LPT>(comp));
+      }
+      const double p64 = rb_score64(l, softmax, mx) * inv;
+      const double c64 = l == -INFINITY ? -INFINITY : p64 + be + 0.0;
+      const uint64_t mykey = mine ? rb_key64(c64) : 0;
+      rank = 0;
+#pragma unroll 1
+      for (int j = 0; j < k + 2; ++j) {
+        const uint64_t o = __shfl_sync(0xffffffffu, mykey, seg0 + j);
+        const int oe = __shfl_sync(0xffffffffu, e, seg0 + j);
+        rank += (o > mykey || (o == mykey && oe < e)) ? 1 : 0;
+      }
+      if (mine == 0u) rank = LPT;
+      if (softmax) {
+        // the nearest of the candidates' neighbours (they are neighbours in fp32)
+        const float dp = static_cast<float>(p64) - __shfl_down_sync(0xffffffffu, static_cast<float>(p64), 1, LPT);
+        const float dc = static_cast<float>(c64 - __shfl_down_sync(0xffffffffu, c64, 1, LPT));
+        if (close && !(fabsf(dc) > 6e-7f * fabsf(dp))) open = true;
+      }
+    }
+    const uint32_t hards = __ballot_sync(0xffffffffu, (hard || open) && live);
     // ---- weights (as rb_weights) ----
-    const bool chosen = sl < k;
+    const bool chosen = rank < k;
     const bool renorm = !softmax || P.renormalize;
     const float top = renorm ? rb_seg_max<LPT>(chosen ? l : -INFINITY) : mx;
     float p = (!softmax && top >= -60.f) ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
     if (!chosen) p = 0.f;
     const float total = renorm ? rb_seg_sum<LPT>(p) : sum;
-    const uint32_t seg_bad = LPT == 32 ? bads : (bads >> seg0) & ((1u << (LPT & 31)) - 1u);
-    if (chosen && live && seg_bad == 0u) {
-      out_w[t * k + sl] = p / total * P.scale;
-      out_ids[t * k + sl] = e;
+    const uint32_t seg_hard = LPT == 32 ? hards : (hards >> seg0) & ((1u << (LPT & 31)) - 1u);
+    if (chosen && live && seg_hard == 0u) {
+      out_w[t * k + rank] = p / total * P.scale;
+      out_ids[t * k + rank] = e;
     }
-    // ---- tokens that fp32 does not decide ----
-    if (bads != 0u) {
-#pragma unroll
+    if (hards != 0u) {
+#pragma unroll 1
       for (int s = 0; s < TPW; ++s) {
-        const uint32_t part = LPT == 32 ? bads : (bads >> (s * LPT)) & ((1u << (LPT & 31)) - 1u);
+        const uint32_t part = LPT == 32 ? hards : (hards >> (s * LPT)) & ((1u << (LPT & 31)) - 1u);
         if (part == 0u) continue;
         const int64_t tb = t0 + s;
-        const T* rb = logits + tb * E;
-        int id0 = 0, id1 = 0;
         __syncwarp();
-        rb_choose64(rb, bias, P, sm, id0, id1);
-        rb_weights(rb, P, id0, id1, __shfl_sync(0xffffffffu, mx, s * LPT),
-                   __shfl_sync(0xffffffffu, sum, s * LPT), out_w + tb * k, out_ids + tb * k);
+        const int2 id = rb_choose64(logits + tb * E, bias, P, sm);
+        rb_weights(logits + tb * E, P, id.x, id.y, out_w + tb * k, out_ids + tb * k);
         __syncwarp();
       }
     }
@@ -705,13 +882,18 @@ int rb_warps(const RouteArgs& a) { return a.E + a.group_count <= 1536 ? kRbWarps
 template <int EPL, int LPT, typename T>
 void launch_fast(const RouteArgs& a, const float* bias, const RbParams& P, cudaStream_t s) {
   const int warps = rb_warps(a);
-  const size_t smem = static_cast<size_t>(warps) * (a.E + a.group_count) * sizeof(double);
+  const size_t smem = static_cast<size_t>(warps) * (a.E + a.group_count) * sizeof(uint64_t);
   const int64_t blocks = ceil_div<int64_t>(a.M, warps * (32 / LPT));
-  // whole lanes of experts, and 16-byte (for few experts narrower) aligned loads of them
+  // 16-byte (for few experts narrower) aligned loads of a lane's experts
   const int bytes = EPL * static_cast<int>(sizeof(T)) < 16 ? EPL * static_cast<int>(sizeof(T)) : 16;
   const int vec = a.E % EPL == 0 && (a.E * sizeof(T)) % bytes == 0 &&
                   reinterpret_cast<uintptr_t>(a.logits) % bytes == 0;
-  launch_kernel(route_biased_kernel<EPL, LPT, T>,
+  const int gs = a.E / a.group_count, lpg = gs / EPL;
+  const bool whole =
+      a.E % EPL == 0 && (a.k_group == a.group_count ||
+                         (gs == lpg * EPL && (lpg & (lpg - 1)) == 0));
+  launch_kernel(whole ? route_biased_kernel<EPL, LPT, true, T>
+                      : route_biased_kernel<EPL, LPT, false, T>,
                 static_cast<unsigned>(std::min<int64_t>(blocks, 152 * 16)), warps * 32, smem, s,
                 static_cast<const T*>(a.logits), bias, P, vec, a.weights, a.ids);
 }
@@ -736,7 +918,7 @@ void launch_biased(const RouteArgs& a, const float* bias, cudaStream_t s) {
   }
   const int warps = rb_warps(a);
   launch_kernel(route_biased_exact_kernel<T>, static_cast<unsigned>(ceil_div<int64_t>(a.M, warps)),
-                warps * 32, static_cast<size_t>(warps) * (a.E + a.group_count) * sizeof(double), s,
+                warps * 32, static_cast<size_t>(warps) * (a.E + a.group_count) * sizeof(uint64_t), s,
                 static_cast<const T*>(a.logits), bias, P, a.weights, a.ids);
 }
 
