@@ -160,7 +160,7 @@ __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, int32
 
 // Waits for the warp's TMEM loads, the registers tied to the wait so that
 // nothing reads them before it.
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
@@ -168,6 +168,18 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 // Arrives on an mbarrier of a CTA of the cluster without ordering this
 // thread's other memory operations: what the accumulator's next writer has
 // to follow are TMEM loads, which the tcgen05 fences order.  The releasing
@@ -225,6 +237,15 @@ struct DpCtl {
   int32_t abort;
 };
 static_assert(kDpSmem + sizeof(DpCtl) <= 232448, "shared memory budget");
+
+// The two halves of a cluster barrier; this arrival orders nothing (a releasing
+// one waits for the thread's loads in flight).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 struct TileMN {
   int m, n;
@@ -473,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
         const uint64_t sc = pair_of(f, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          tmem_wait16(v[i & 1]);
+          tmem_wait(v[i & 1]);
           if (i < 7) {
             ptx::tmem_ld_16cols(ta + 16 * (i + 1), v[(i + 1) & 1]);
           } else {  // the accumulator is in registers
@@ -544,28 +565,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
 // ---- few rows: the weight's columns as the MMA's rows, K split over a cluster ----
 // The weight's bytes bound these products, so that every SM has to stream
 // them: a CTA takes 128 weight columns (the MMA's M) and one of S parts of K
-// for T rows of A (the MMA's N), the S CTAs of a cluster add their sums through
-// distributed shared memory in a fixed order.  TMEM lane = weight column, TMEM
-// column = row of A, so a thread's sums are one output column for T rows and
-// the output is written along its rows.
+// for T rows of A (the MMA's N).  TMEM lane = weight column, TMEM column = row of
+// A, so a thread's sums are one output column for T rows.  The S CTAs of a
+// cluster each own every S-th group of four rows: they store their sums into
+// the owners' shared memory (reading the others' instead was a chain of remote
+// loads, 8 of 17 us at 77 x 2048 x 7168), and the owner adds the S parts in order.
 constexpr int kDsThreads = 64 + 128;   // TMA warp, MMA warp, 4 promotion warps
 constexpr int kDsScaleBlocks = 16;     // K blocks whose scales are held at a time
 template <int T>
 struct DsGeo {
   static constexpr int STAGE = 16384 + T * 128;
-  static constexpr int STAGES = T <= 32 ? 9 : T == 64 ? 7 : 5;
+  static constexpr int STAGES = T <= 32 ? 8 : T == 64 ? 7 : 4;
   static constexpr int ACCS = T == 128 ? 4 : 8;  // TMEM accumulators of T columns
   static constexpr int COLS = ACCS * T;
-  static constexpr int PART = 132;               // padded row of the partial sums, floats
-  static constexpr size_t SMEM = 1024 + STAGES * STAGE;
-  static_assert(T * PART * 4 <= STAGES * STAGE, "partial sums in the ring's memory");
+  // sums of S parts for the T / 4 row groups (up to 7 more slots than groups: the
+  // groups of an owner are rounded up)
+  static constexpr int PARTS = (T / 4 + 8) * 128 * 16;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE + PARTS;
 };
 template <int T>
 struct DsCtl {
   uint64_t full[DsGeo<T>::STAGES], empty[DsGeo<T>::STAGES];
   uint64_t tmem_full[DsGeo<T>::ACCS], tmem_empty[DsGeo<T>::ACCS];
   uint64_t scale_free, scale_ready;
-  alignas(16) float scale[kDsScaleBlocks][T];  // row scale times the block's weight scale
+  // row scale times the block's weight scale (padded: stored a column at a time)
+  alignas(16) float scale[kDsScaleBlocks][T + 4];
   uint32_t tmem_base;
   int32_t abort;
 };
@@ -575,10 +599,10 @@ static_assert(DsGeo<16>::SMEM + sizeof(DsCtl<16>) <= 232448 &&
                   DsGeo<128>::SMEM + sizeof(DsCtl<128>) <= 232448,
               "shared memory budget");
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
+               "f"(c), "f"(d)
+               : "memory");
 }
 
 template <int T, bool TR>
@@ -593,6 +617,35 @@ __global__ void __launch_bounds__(kDsThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(ptx::cluster_ctarank());  // the part of K
   uint8_t* tiles = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  float4* parts = reinterpret_cast<float4*>(tiles + G::STAGES * G::STAGE);
+  const int groups = ceil_div(T / 4, S);  // row groups of an owner; parts [S][groups][128]
+  const int KB = ceil_div(P.K, 128), NB = ceil_div(P.N, 128);
+  const int nb = static_cast<int>(blockIdx.x) / S;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * T;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / S);
+  // Scales of the next kDsScaleBlocks blocks, from block kb on: thread p of the
+  // promotion warps takes block p % 16 of rows p / 16, p / 16 + 8, ... (a warp's
+  // load is two rows' 64 bytes); the first ones are loaded ahead of everything
+  // else (they were 2000 cycles of latency between the first MMA and its
+  // promotion).  Rows past M count as 0.
+  static_assert(kDsScaleBlocks == 16, "one block per thread");
+  const int p = static_cast<int>(threadIdx.x) - 64;
+  const int sb = p & 15, sr = p >> 4;
+  auto load_scale = [&](int kb, int j) {  // (the block's for j < 0)
+    const int64_t m = m0 + sr + 8 * j;
+    if (sb >= kb1 - kb || m >= P.M) return 0.f;
+    if (j < 0)
+      return __ldg(P.w_scale + (TR ? static_cast<int64_t>(nb) * KB + kb + sb
+                                   : static_cast<int64_t>(kb + sb) * NB + nb));
+    return __ldg(P.a_scale + m * KB + kb + sb);
+  };
+  float ra[T / 8], rw = 0.f;
+  if (warp >= 2) {
+    rw = load_scale(kb0, -1);
+#pragma unroll
+    for (int j = 0; j < T / 8; ++j) ra[j] = load_scale(kb0, j);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::STAGES; ++i) {
       ptx::mbar_init(&ctl.full[i], 1);
@@ -615,16 +668,11 @@ __global__ void __launch_bounds__(kDsThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
+  cluster_arrive_relaxed();  // (waited for ahead of the stores to the others' memory)
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
 
-  const int KB = ceil_div(P.K, 128), NB = ceil_div(P.N, 128);
-  const int nb = static_cast<int>(blockIdx.x) / S;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * T;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / S);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / S);
   bool ok = true;
-
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
@@ -674,7 +722,6 @@ __global__ void __launch_bounds__(kDsThreads, 1)
     }
   } else {
     const int q = warp & 3;
-    const int p = threadIdx.x - 64;      // 0 .. 127, for the scales
     const int col = q * 32 + lane;       // weight column of the tile
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint64_t sum[T / 2];
@@ -698,15 +745,13 @@ __global__ void __launch_bounds__(kDsThreads, 1)
           ok = false;
           break;
         }
+        if (chunk == 0) {
+#pragma unroll
+          for (int j = 0; j < T / 8; ++j) ctl.scale[sb][sr + 8 * j] = ra[j] * rw;
+        } else {
+          const float w = load_scale(kb, -1);
 #pragma unroll 4
-        for (int i = p; i < kDsScaleBlocks * T; i += 128) {
-          const int b = i % kDsScaleBlocks, r = i / kDsScaleBlocks;
-          float s = 0.f;
-          if (kb + b < kb1 && m0 + r < P.M)
-            s = __ldg(P.a_scale + (m0 + r) * KB + kb + b) *
-                __ldg(P.w_scale + (TR ? static_cast<int64_t>(nb) * KB + kb + b
-                                      : static_cast<int64_t>(kb + b) * NB + nb));
-          ctl.scale[b][r] = s;
+          for (int j = 0; j < T / 8; ++j) ctl.scale[sb][sr + 8 * j] = load_scale(kb, j) * w;
         }
         if (!meet(&ctl.scale_ready, chunk & 1)) {
           ok = false;
@@ -720,18 +765,20 @@ __global__ void __launch_bounds__(kDsThreads, 1)
       }
       ptx::tc_fence_after();
       const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(ctl.scale[slot]);
+      constexpr int W = T < 32 ? T : 32;  // columns per TMEM load
 #pragma unroll
-      for (int c = 0; c < T; c += 16) {
-        uint32_t v[16];
-        ptx::tmem_ld_16cols(lane_addr + acc * T + c, v);
-        tmem_wait16(v);
-        if (c + 16 == T) {  // the accumulator is in registers
+      for (int c = 0; c < T; c += W) {
+        uint32_t v[W];
+        if constexpr (W == 32) ptx::tmem_ld_32cols(lane_addr + acc * T + c, v);
+        else ptx::tmem_ld_16cols(lane_addr + acc * T + c, v);
+        tmem_wait(v);
+        if (c + W == T) {  // the accumulator is in registers
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&ctl.tmem_empty[acc]);
         }
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
+        for (int j = 0; j < W; j += 4) {
           const ulonglong2 s4 = sc[(c + j) / 4];
           fma_pair(sum[(c + j) / 2], v[j], v[j + 1], s4.x);
           fma_pair(sum[(c + j) / 2 + 1], v[j + 2], v[j + 3], s4.y);
@@ -742,39 +789,71 @@ __global__ void __launch_bounds__(kDsThreads, 1)
         turn ^= 1u;
       }
     }
-    // every stage of the ring has been read (the last block's MMA is done):
-    // its memory takes the partial sums, [row of A][column]
-    float* part = reinterpret_cast<float*>(tiles);
+    __syncwarp();
+    cluster_wait();
     if (ok) {
+      uint32_t slot = ptx::smem_u32(parts + rank * groups * 128 + col);
+      int owner = 0;
 #pragma unroll
-      for (int j = 0; j < T; j += 2) {
-        const float2 v = unpair(sum[j / 2]);
-        part[j * G::PART + col] = v.x;
-        part[(j + 1) * G::PART + col] = v.y;
+      for (int g = 0; g < T / 4; ++g) {
+        const float2 a = unpair(sum[2 * g]), b = unpair(sum[2 * g + 1]);
+        st_cluster_f32x4(ptx::mapa_shared(slot, owner), a.x, a.y, b.x, b.y);
+        if (++owner == S) {
+          owner = 0;
+          slot += 128 * 16;
+        }
       }
     }
   }
   __syncwarp();
+  if (warp < 2) cluster_wait();
   ptx::cluster_sync();
   if (warp >= 2) {
-    // rows rank, rank + S, ... of the tile: the parts in order, bias, output
-    const int col = threadIdx.x - 64;
+    const int col = (warp & 3) * 32 + lane;
     const int n = nb * 128 + col;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(T), P.M - m0));
     const float b = P.bias != nullptr && n < P.N ? __bfloat162float(P.bias[n]) : 0.f;
-    const uint32_t mine = ptx::smem_u32(tiles) + col * 4;
-    if (n < P.N) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(T), P.M - m0));
+    auto put = [&](auto* out) {
+      using O = std::remove_pointer_t<decltype(out)>;
+      const int64_t ld = P.N;
+      out += (m0 + 4 * rank) * ld + n;
+      const float4* mine = parts + col;
+      auto add = [&](int i) {
+        float4 v = make_float4(b, b, b, b);
 #pragma unroll 4
-      for (int r = rank; r < rows; r += S) {
-        float v = b;
-        for (int s = 0; s < S; ++s)
-          v += ld_cluster_f32(ptx::mapa_shared(mine + r * (G::PART * 4), s));
-        const int64_t o = (m0 + r) * P.N + n;
-        if (P.out_f32)
-          static_cast<float*>(P.out)[o] = v;
-        else
-          static_cast<bf16*>(P.out)[o] = __float2bfloat16(v);
+        for (int s = 0; s < S; ++s) {
+          const float4 o = mine[(s * groups + i) * 128];
+          v.x += o.x;
+          v.y += o.y;
+          v.z += o.z;
+          v.w += o.w;
+        }
+        return v;
+      };
+      // whole groups of this owner, then the one the rows end in
+      const int whole = rows / 4 > rank ? (rows / 4 - rank - 1) / S + 1 : 0;
+#pragma unroll 4
+      for (int i = 0; i < whole; ++i) {
+        const float4 v = add(i);
+        O* d = out + i * (4 * S) * ld;
+        d[0] = static_cast<O>(v.x);
+        d[ld] = static_cast<O>(v.y);
+        d[2 * ld] = static_cast<O>(v.z);
+        d[3 * ld] = static_cast<O>(v.w);
       }
+      if (rows % 4 != 0 && rows / 4 % S == rank) {
+        const float4 v = add(rows / 4 / S);
+        O* d = out + rows / 4 / S * (4 * S) * ld;
+        d[0] = static_cast<O>(v.x);
+        if (rows % 4 > 1) d[ld] = static_cast<O>(v.y);
+        if (rows % 4 > 2) d[2 * ld] = static_cast<O>(v.z);
+      }
+    };
+    if (n < P.N) {
+      if (P.out_f32)
+        put(static_cast<float*>(P.out));
+      else
+        put(static_cast<bf16*>(P.out));
     }
   }
   if (*reinterpret_cast<volatile int32_t*>(&ctl.abort)) {
@@ -782,8 +861,7 @@ __global__ void __launch_bounds__(kDsThreads, 1)
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
-  __syncwarp();
-  ptx::cluster_sync();  // (no CTA leaves while another reads its sums)
+  __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, G::COLS);
@@ -849,30 +927,12 @@ moe_status_t launch_pair(const MatmulFp8Args& a, const DenseParams& P, cudaStrea
   return check_launch("matmul_fp8");
 }
 
+// A launch of the split kernel with clusters of S (cfg.attrs: room for two).
 template <int T, bool TR>
-moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
-  using G = DsGeo<T>;
-  static PerDevice attr;
-  if (attr.get([](int*) {
-        return cudaFuncSetAttribute(dense_fp8_split_kernel<T, TR>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(G::SMEM));
-      }) != cudaSuccess)
-    return set_error(MOE_ERR_CUDA, "attributes of matmul_fp8: %s",
-                     cudaGetErrorString(cudaGetLastError()));
-  CUtensorMap tmA, tmB;
-  if (moe_status_t st = dense_maps(a, T, &tmA, &tmB)) return st;
-  const int64_t mt = ceil_div<int64_t>(a.M, T);
-  const int nt = ceil_div(a.N, 128), KB = ceil_div(a.K, 128);
-  // as many parts of K as fill the SMs once, up to a portable cluster
-  const int S = static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>({8, KB, a.num_sms / (nt * mt)})));
-  cudaLaunchConfig_t cfg = {};
+void split_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, int S, int nt, int64_t mt) {
   cfg.gridDim = dim3(static_cast<unsigned>(nt * S), static_cast<unsigned>(mt));
   cfg.blockDim = dim3(kDsThreads);
-  cfg.dynamicSmemBytes = G::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
+  cfg.dynamicSmemBytes = DsGeo<T>::SMEM;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
   at[1].id = cudaLaunchAttributeClusterDimension;
@@ -881,18 +941,90 @@ moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, cudaStre
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
+}
+
+// Parts of K for the split kernel: the most whose clusters are all resident at
+// once (one cluster too many makes a second wave: 17 clusters of 8 took 20.7 us
+// for 128 x 4096 x 2064, 17 of 7 11.7).
+template <int T, bool TR>
+int split_parts(int nt, int64_t mt, int KB, int num_sms) {
+  constexpr int MAX_S = 8;  // a portable cluster
+  static PerDevice attr, resident[MAX_S + 1];
+  attr.get([](int*) {
+    return cudaFuncSetAttribute(dense_fp8_split_kernel<T, TR>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(DsGeo<T>::SMEM));
+  });
+  int S = 1;
+  for (int c = 2; c <= std::min(MAX_S, KB); ++c) {
+    if (c * nt * mt > num_sms) break;
+    int clusters = 0;
+    if (resident[c].get(
+            [&](int* v) {
+              cudaLaunchConfig_t cfg = {};
+              cudaLaunchAttribute at[2];
+              split_config<T, TR>(cfg, at, c, 1, 1);
+              return cudaOccupancyMaxActiveClusters(v, dense_fp8_split_kernel<T, TR>, &cfg);
+            },
+            &clusters) != cudaSuccess) {
+      cudaGetLastError();
+      break;
+    }
+    if (nt * mt <= clusters) S = c;
+  }
+  return S;
+}
+
+template <int T, bool TR>
+moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, int S, cudaStream_t s) {
+  CUtensorMap tmA, tmB;
+  if (moe_status_t st = dense_maps(a, T, &tmA, &tmB)) return st;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  split_config<T, TR>(cfg, at, S, ceil_div(a.N, 128), ceil_div<int64_t>(a.M, T));
+  cfg.stream = s;
   prof_before("matmul_fp8", s);
   cudaLaunchKernelEx(&cfg, dense_fp8_split_kernel<T, TR>, tmA, tmB, P, S);
   prof_after("matmul_fp8", s);
   return check_launch("matmul_fp8");
 }
 
+// The kernel for a call: the least of the times estimated from a fixed part
+// and one per K block of a CTA, as measured on GB300 (us; K x N of 7168 x 4096,
+// 2048 x 7168, 4096 x 2064 and 1024 x 1024, 1 to 2048 rows):
+//   split, 16 rows a tile: 3.5 + 0.35    32 rows: 3.7 + 0.36
+//          64 rows: 4.2 + 0.39           128 rows: 5.7 + 0.52
+//   pairs: 4.8 + 0.45
+// e.g. 256 x 7168 x 4096: 25.7 (64), 20.8 (128), 29.0 (pairs); 256 x 2048 x 7168:
+// 19.9, 13.7, 12.1; 512 x 1024 x 1024: 5.9, 7.3, 8.6; 768 x 4096 x 2064: 31.5, 21.5,
+// 19.1.
 template <bool TR>
 moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
-  if (a.M <= 16) return launch_split<16, TR>(a, P, s);
-  if (a.M <= 32) return launch_split<32, TR>(a, P, s);
-  if (a.M <= 64) return launch_split<64, TR>(a, P, s);
-  if (a.M <= 128) return launch_split<128, TR>(a, P, s);
+  const int nt = ceil_div(a.N, 128), KB = ceil_div(a.K, 128);
+  const int64_t pairs = ceil_div<int64_t>(a.M, 256) * ceil_div(a.N, 256);
+  float best = 4.8f + 0.45f * KB * static_cast<float>(ceil_div<int64_t>(pairs, a.num_sms / 2));
+  int T = 256, S = 1;
+  auto consider = [&](auto rows, float fixed, float per_block) {
+    constexpr int R = decltype(rows)::value;
+    const int64_t mt = ceil_div<int64_t>(a.M, R);
+    if (mt > 64) return;  // the pairs' case, and a bound of the grid's y
+    const int parts = split_parts<R, TR>(nt, mt, KB, a.num_sms);
+    const int64_t waves = ceil_div<int64_t>(nt * mt * parts, a.num_sms);
+    const float t = fixed + per_block * ceil_div(KB, parts) * static_cast<float>(waves);
+    if (t < best) {
+      best = t;
+      T = R;
+      S = parts;
+    }
+  };
+  consider(std::integral_constant<int, 128>{}, 5.7f, 0.52f);
+  consider(std::integral_constant<int, 64>{}, 4.2f, 0.39f);
+  consider(std::integral_constant<int, 32>{}, 3.7f, 0.36f);
+  consider(std::integral_constant<int, 16>{}, 3.5f, 0.35f);
+  if (T == 16) return launch_split<16, TR>(a, P, S, s);
+  if (T == 32) return launch_split<32, TR>(a, P, S, s);
+  if (T == 64) return launch_split<64, TR>(a, P, S, s);
+  if (T == 128) return launch_split<128, TR>(a, P, S, s);
   return launch_pair<TR>(a, P, s);
 }
 
