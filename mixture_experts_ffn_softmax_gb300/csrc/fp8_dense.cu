@@ -20,31 +20,70 @@ namespace {
 // ---- quantisation ----
 constexpr int kQgWarps = 8;
 
+// Pairs of fp32 in one register pair, and operations on both at once (each
+// rounded as the plain one): half the issue slots, which bound these kernels.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// div_fixed (fp8q.cuh) of a pair: x / s from r = 1 / s, ns = -s.
+__device__ __forceinline__ uint64_t div_fixed2(uint64_t x, uint64_t ns, uint64_t r) {
+  const uint64_t q = mul2(x, r);
+  return fma2(fma2(q, ns, x), r, q);
+}
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
 __device__ __forceinline__ void unpack8(const uint4 u, float (&f)[8]) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = __bfloat1622float2(h[i]);
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 
 // SiLU(g) * u of eight columns.  The quotient g / (1 + e^-g) by the reciprocal
-// (within 2 ulp) and one correction (div_fixed: the remainder is exact, one
+// (within an ulp) and one correction (div_fixed: the remainder is exact, one
 // rounding); for gates outside the range in which that holds, by the division.
 __device__ __forceinline__ void swiglu8(float (&g)[8], const float (&u)[8]) {
-  float lo = g[0], hi = g[0];
+  float top = 0.f;
 #pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    lo = fminf(lo, g[j]);
-    hi = fmaxf(hi, g[j]);
-  }
-  if (lo > -80.f && hi < 1e38f) {
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(g[j]));
+  if (top < 80.f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float den = 1.0f + expf(-g[j]);
-      g[j] = div_fixed(g[j], den, __fdividef(1.0f, den)) * u[j];
+    for (int j = 0; j < 8; j += 2) {
+      float den[2], r[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        den[i] = 1.0f + expf(-g[j + i]);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(den[i]));
+      }
+      const float2 z = unpair(mul2(div_fixed2(pair_of(g[j], g[j + 1]), pair_of(-den[0], -den[1]),
+                                              pair_of(r[0], r[1])),
+                                   pair_of(u[j], u[j + 1])));
+      g[j] = z.x;
+      g[j + 1] = z.y;
     }
   } else {
 #pragma unroll
@@ -52,25 +91,30 @@ __device__ __forceinline__ void swiglu8(float (&g)[8], const float (&u)[8]) {
   }
 }
 
-// E4M3 codes of eight values, each fp32(z / s) rounded to nearest even.
-__device__ __forceinline__ uint2 e4m3_codes8(const float (&z)[8], float s) {
-  // (the correction is exact while the remainder does not underflow)
-  const bool fast = s >= 1e-30f && s <= 1e30f;
-  const float r = fast ? __frcp_rn(s) : 0.f;
+// E4M3 codes of eight values, each fp32(z / s) rounded to nearest even; r = 1 / s
+// where fast (no remainder of the correction underflows).
+__device__ __forceinline__ uint2 e4m3_codes8(const float (&z)[8], float s, float r, bool fast) {
   uint32_t c[4];
+  if (fast) {
+    const uint64_t ns = pair_of(-s, -s), r2 = pair_of(r, r);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 q = fast ? make_float2(div_fixed(z[2 * j], s, r), div_fixed(z[2 * j + 1], s, r))
-                          : make_float2(__fdiv_rn(z[2 * j], s), __fdiv_rn(z[2 * j + 1], s));
-    c[j] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    for (int j = 0; j < 4; ++j)
+      c[j] = __nv_cvt_float2_to_fp8x2(unpair(div_fixed2(pair_of(z[2 * j], z[2 * j + 1]), ns, r2)),
+                                      __NV_SATFINITE, __NV_E4M3);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = __nv_cvt_float2_to_fp8x2(
+          make_float2(__fdiv_rn(z[2 * j], s), __fdiv_rn(z[2 * j + 1], s)), __NV_SATFINITE,
+          __NV_E4M3);
   }
-  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 // A half-warp per (row, group of 128 columns), 8 columns per lane.  A warp
 // takes U passes of 256 columns of a row with all their loads in flight.
-// Bound: HBM (3 bytes per element of x, 5 per element of z for SiLU(gate) *
-// up).  8192 x 7168: 40 us; 8191 x 2048 of gate and up: 26 us.
+// Bound: issue slots and HBM (3 bytes per element of x, 5 per element of z for
+// SiLU(gate) * up).  8192 x 7168: QUANT_T1 us; 8191 x 2048 of gate and up: QUANT_T2 us.
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kQgWarps * 32)
     quant_groups_kernel(const bf16* __restrict__ x, int64_t M, int K, uint8_t* __restrict__ q8,
@@ -88,37 +132,50 @@ __global__ void __launch_bounds__(kQgWarps * 32)
   const int64_t step_row = warps / segs;
   const int step_seg = static_cast<int>(warps - step_row * segs);
   while (row < M) {
-    const bf16* src = x + row * K * (SWIGLU ? 2 : 1);
     const int col0 = seg * (256 * U) + lane * 8;
+    const bf16* src = x + row * K * (SWIGLU ? 2 : 1) + col0;
     uint4 a[U], b[SWIGLU ? U : 1];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int col = col0 + 256 * i;
-      a[i] = col < K ? __ldg(reinterpret_cast<const uint4*>(src + col)) : make_uint4(0, 0, 0, 0);
+      const bool in = col0 + 256 * i < K;
+      a[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + 256 * i)) : make_uint4(0, 0, 0, 0);
       if constexpr (SWIGLU)
-        b[i] = col < K ? __ldg(reinterpret_cast<const uint4*>(src + K + col))
-                       : make_uint4(0, 0, 0, 0);
+        b[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + K + 256 * i))
+                  : make_uint4(0, 0, 0, 0);
     }
+    uint8_t* dst = q8 + row * K + col0;
+    float* sc = scale + row * G + col0 / 128;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int col = col0 + 256 * i;
       float z[8];
       unpack8(a[i], z);
+      float m = 0.f;  // max |z|, or NaN
       if constexpr (SWIGLU) {
         float u[8];
         unpack8(b[i], u);
         swiglu8(z, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max_nan(m, z[j]);
+      } else {
+        // as bf16 pairs: the bits without the sign order as the values, NaN on top
+        uint32_t t = __vmaxu2(a[i].x & 0x7fff7fffu, a[i].y & 0x7fff7fffu);
+        t = __vmaxu2(t, a[i].z & 0x7fff7fffu);
+        t = __vmaxu2(t, a[i].w & 0x7fff7fffu);
+        m = __uint_as_float(max(t << 16, t & 0xffff0000u));
       }
-      // max |z| as an unsigned maximum of the bits: NaN is above every number
-      uint32_t mb = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mb = max(mb, __float_as_uint(z[j]) & 0x7fffffffu);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-      const float s = mb == 0u ? 1.0f : __fdiv_rn(__uint_as_float(mb), 448.0f);
-      if (col < K) {
-        *reinterpret_cast<uint2*>(q8 + row * K + col) = e4m3_codes8(z, s);
-        if ((lane & 15) == 0) scale[row * G + col / 128] = s;
+      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const bool fast = m >= 1e-27f && m <= 1e30f;
+      float s, r = 0.f;
+      if (fast) {
+        s = div_fixed(m, 448.0f, 1.0f / 448.0f);
+        r = __frcp_rn(s);
+      } else {
+        s = m == 0.f ? 1.0f : __fdiv_rn(m, 448.0f);
+      }
+      if (col0 + 256 * i < K) {
+        *reinterpret_cast<uint2*>(dst + 256 * i) = e4m3_codes8(z, s, r, fast);
+        if ((lane & 15) == 0) sc[2 * i] = s;
       }
     }
     row += step_row;
@@ -190,19 +247,8 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
                : "memory");
 }
 
-// Pairs of fp32 sums as one 64-bit register pair (fma.rn.f32x2: each rounded
-// as fmaf); kept packed, so that no pair is taken apart and put together again
-// in every block.
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
+// c += (a0, a1) * b on a pair of sums kept packed, so that no pair is taken apart
+// and put together again in every block.
 __device__ __forceinline__ void fma_pair(uint64_t& c, uint32_t a0, uint32_t a1, uint64_t b) {
   asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\tfma.rn.f32x2 %0, a, %3, %0;\n\t}"
       : "+l"(c)
