@@ -1120,9 +1120,10 @@ moe_status_t moe_quant_groups_fp8(const void* x, int64_t M, int32_t K, int32_t s
   if (!x || !q8 || !scale) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(x) || !aligned16(q8) || !aligned_to(scale, 4))
     return set_error(MOE_ERR_INVALID_ARG, "x and q8 must be 16-byte aligned");
-  if (moe_status_t st = check_device(nullptr)) return st;
+  int sms = 0;
+  if (moe_status_t st = check_device(&sms)) return st;
   const QuantGroupsArgs a{static_cast<const bf16*>(x), M, K, swiglu, static_cast<uint8_t*>(q8),
-                          scale};
+                          scale, sms};
   return launch_quant_groups_fp8(a, stream);
 }
 

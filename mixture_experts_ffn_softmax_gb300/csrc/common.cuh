@@ -143,6 +143,7 @@ struct QuantGroupsArgs {
   int32_t K, swiglu;
   uint8_t* q8;    // [M, K]
   float* scale;   // [M, ceil(K/128)]
+  int32_t num_sms;
 };
 moe_status_t launch_quant_groups_fp8(const QuantGroupsArgs& a, cudaStream_t s);
 // out [M, N] = block-scaled a [M, K] times w, w [K, N] with scales

@@ -18,7 +18,7 @@ namespace gbmoe {
 namespace {
 
 // ---- quantisation ----
-constexpr int kQgWarps = 8;
+constexpr int kQgWarps = 8, kQgBlocks = 3;  // warps of a block, blocks of an SM
 
 // Pairs of fp32 in one register pair, and operations on both at once (each
 // rounded as the plain one): half the issue slots, which bound these kernels.
@@ -112,11 +112,13 @@ __device__ __forceinline__ uint2 e4m3_codes8(const float (&z)[8], float s, float
 }
 
 // A half-warp per (row, group of 128 columns), 8 columns per lane.  A warp
-// takes U passes of 256 columns of a row with all their loads in flight.
-// Bound: issue slots and HBM (3 bytes per element of x, 5 per element of z for
-// SiLU(gate) * up).  8192 x 7168: QUANT_T1 us; 8191 x 2048 of gate and up: QUANT_T2 us.
+// takes U passes of 256 columns of a row at a time, the next ones' loads in
+// flight while it works on them (resident blocks only, three per SM: 8192 x 7168 in
+// 30.0 us, 31.0 without the loads ahead, 32.8 in blocks of one row segment after
+// another).  Bound: HBM (3 bytes per element of x, 5.9 TB/s of 6.8 measured), and
+// for SiLU(gate) * up, 5 per element of z, issue slots (8191 x 2048: 19.0 us).
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kQgWarps * 32)
+__global__ void __launch_bounds__(kQgWarps * 32, kQgBlocks)
     quant_groups_kernel(const bf16* __restrict__ x, int64_t M, int K, uint8_t* __restrict__ q8,
                         float* __restrict__ scale) {
   pdl_begin();
@@ -131,36 +133,53 @@ __global__ void __launch_bounds__(kQgWarps * 32)
   int seg = static_cast<int>(first - row * segs);
   const int64_t step_row = warps / segs;
   const int step_seg = static_cast<int>(warps - step_row * segs);
-  while (row < M) {
+  uint4 a[U], b[SWIGLU ? U : 1];
+  auto load = [&]() {  // of (row, seg); zeros past K and M
     const int col0 = seg * (256 * U) + lane * 8;
     const bf16* src = x + row * K * (SWIGLU ? 2 : 1) + col0;
-    uint4 a[U], b[SWIGLU ? U : 1];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const bool in = col0 + 256 * i < K;
+      const bool in = row < M && col0 + 256 * i < K;
       a[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + 256 * i)) : make_uint4(0, 0, 0, 0);
       if constexpr (SWIGLU)
         b[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + K + 256 * i))
                   : make_uint4(0, 0, 0, 0);
     }
+  };
+  load();
+  while (row < M) {
+    const int col0 = seg * (256 * U) + lane * 8;
+    uint4 ca[U], cb[SWIGLU ? U : 1];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      ca[i] = a[i];
+      if constexpr (SWIGLU) cb[i] = b[i];
+    }
     uint8_t* dst = q8 + row * K + col0;
     float* sc = scale + row * G + col0 / 128;
+    row += step_row;
+    seg += step_seg;
+    if (seg >= segs) {
+      seg -= segs;
+      ++row;
+    }
+    load();  // the next unit's, while this one is worked on
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       float z[8];
-      unpack8(a[i], z);
+      unpack8(ca[i], z);
       float m = 0.f;  // max |z|, or NaN
       if constexpr (SWIGLU) {
         float u[8];
-        unpack8(b[i], u);
+        unpack8(cb[i], u);
         swiglu8(z, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = max_nan(m, z[j]);
       } else {
         // as bf16 pairs: the bits without the sign order as the values, NaN on top
-        uint32_t t = __vmaxu2(a[i].x & 0x7fff7fffu, a[i].y & 0x7fff7fffu);
-        t = __vmaxu2(t, a[i].z & 0x7fff7fffu);
-        t = __vmaxu2(t, a[i].w & 0x7fff7fffu);
+        uint32_t t = __vmaxu2(ca[i].x & 0x7fff7fffu, ca[i].y & 0x7fff7fffu);
+        t = __vmaxu2(t, ca[i].z & 0x7fff7fffu);
+        t = __vmaxu2(t, ca[i].w & 0x7fff7fffu);
         m = __uint_as_float(max(t << 16, t & 0xffff0000u));
       }
 #pragma unroll
@@ -177,12 +196,6 @@ __global__ void __launch_bounds__(kQgWarps * 32)
         *reinterpret_cast<uint2*>(dst + 256 * i) = e4m3_codes8(z, s, r, fast);
         if ((lane & 15) == 0) sc[2 * i] = s;
       }
-    }
-    row += step_row;
-    seg += step_seg;
-    if (seg >= segs) {
-      seg -= segs;
-      ++row;
     }
   }
 }
@@ -1079,7 +1092,7 @@ moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStr
 moe_status_t launch_quant_groups_fp8(const QuantGroupsArgs& a, cudaStream_t s) {
   const int64_t units = a.M * ceil_div(a.K, a.swiglu ? 512 : 1024);
   const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>(ceil_div<int64_t>(units, kQgWarps), 152 * 32));
+      static_cast<unsigned>(std::min<int64_t>(ceil_div<int64_t>(units, kQgWarps), a.num_sms * kQgBlocks));
   prof_before("quant_groups_fp8", s);
   launch_kernel(a.swiglu ? quant_groups_kernel<true> : quant_groups_kernel<false>, grid,
                 kQgWarps * 32, 0, s, a.x, a.M, a.K, a.q8, a.scale);
