@@ -647,9 +647,11 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     const bool chosen = rank < k;
     const bool renorm = !softmax || P.renormalize;
     const float top = renorm ? rb_seg_max<LPT>(chosen ? l : -INFINITY) : mx;
+    const bool none = top == -INFINITY;  // nothing chosen that is not masked
     float p = (!softmax && top >= -60.f) ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
-    if (!chosen) p = 0.f;
-    const float total = renorm ? rb_seg_sum<LPT>(p) : sum;
+    if (!chosen || none) p = 0.f;
+    float total = renorm ? rb_seg_sum<LPT>(p) : sum;
+    if (none) total = 1.0f;
     const uint32_t seg_hard = LPT == 32 ? hards : (hards >> seg0) & ((1u << (LPT & 31)) - 1u);
     if (chosen && live && seg_hard == 0u) {
       out_w[t * k + rank] = p / total * P.scale;

@@ -133,6 +133,22 @@ def test_route_biased_masked_experts(E, kg, G, mode, method, renorm):
     check_biased(torch.tensor(logits, device="cuda"), bias, args(k, method, renorm, kg, G, mode))
 
 
+@pytest.mark.parametrize("E,k,G,kg", [(1, 1, 1, 1), (8, 8, 1, 1), (14, 14, 1, 1), (30, 30, 1, 1),
+                                      (64, 14, 8, 2), (32, 8, 4, 1), (64, 64, 1, 1)])
+@pytest.mark.parametrize("method,renorm", [("sigmoid", True), ("softmax", True), ("softmax", False)])
+def test_route_biased_masked_rows_that_choose_every_expert(E, k, G, kg, method, renorm):
+    """Every expert (of the kept groups) is chosen, so that nothing is left to
+    compare the last one with: none, some or all of them masked."""
+    rng = np.random.default_rng(E + k)
+    logits = rng.normal(size=(12, E)).astype(np.float32)
+    for t in range(12):
+        logits[t, rng.permutation(E)[:[0, E // 2, E - 1, E][t % 4]]] = -np.inf
+    for bias in (np.zeros(E), rng.normal(size=E)):
+        bias = torch.tensor(bias, dtype=torch.float32, device="cuda")
+        check_biased(torch.tensor(logits, device="cuda"), bias,
+                     args(k, method, renorm, kg, G, 0))
+
+
 @pytest.mark.parametrize("method", ["sigmoid", "softmax"])
 def test_route_biased_non_finite_scores(method):
     """Whatever the logits hold, ids are valid and distinct; other tokens keep
