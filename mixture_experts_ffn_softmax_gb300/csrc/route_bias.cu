@@ -597,6 +597,8 @@ __global__ void __launch_bounds__(kRbWarps * 32)
         }
       }
       cn = __shfl_down_sync(0xffffffffu, ce, 1, LPT);
+      // (what three passes leave out of order could hide near ties of others)
+      if (sl < k + 1 && cn > ce) hard = true;
     }
     const float ln = __shfl_down_sync(0xffffffffu, l, 1, LPT);
     const float bn = __shfl_down_sync(0xffffffffu, be, 1, LPT);

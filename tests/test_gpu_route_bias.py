@@ -149,6 +149,22 @@ def test_route_biased_masked_rows_that_choose_every_expert(E, k, G, kg, method, 
                      args(k, method, renorm, kg, G, 0))
 
 
+@pytest.mark.parametrize("E,k,G,kg", [(256, 8, 1, 1), (256, 8, 8, 4), (128, 5, 1, 1), (512, 8, 1, 1),
+                                      (1024, 3, 1, 1)])
+@pytest.mark.parametrize("method", ["sigmoid", "softmax"])
+def test_route_biased_scores_in_falling_order_a_few_roundings_apart(E, k, G, kg, method):
+    """Scores that rise with the expert's number (against the order of ties) in
+    steps from a tenth of an fp32 rounding to thousands of them."""
+    M = 96
+    step = 2.0 ** np.linspace(-27, -13, M)[:, None]
+    rng = np.random.default_rng(E + k)
+    jitter = 1 + 0.5 * rng.random((M, E))
+    logits = (step * np.cumsum(jitter, 1)).astype(np.float32)
+    bias = torch.zeros(E, device="cuda")
+    for l in (logits, logits[:, ::-1].copy(), logits[:, rng.permutation(E)].copy()):
+        check_biased(torch.tensor(l, device="cuda"), bias, args(k, method, True, kg, G, 0))
+
+
 @pytest.mark.parametrize("method", ["sigmoid", "softmax"])
 def test_route_biased_non_finite_scores(method):
     """Whatever the logits hold, ids are valid and distinct; other tokens keep
