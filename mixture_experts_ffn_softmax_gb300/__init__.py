@@ -138,15 +138,14 @@ def _tensor(t, name: str, dtypes, shape, device: int):
                          f"{'the CPU' if device < 0 else f'cuda:{device}'}")
 
 
-def _call(name: str, device: int, stream, new, *args):
+def _call(name: str, device: int, stream, *args):
     """Calls the entry point `name` on `stream` (default: the current one)
-    with `device` current; tensors allocated for the call are recorded on a
-    stream of the caller's."""
+    with `device` current."""
     if device < 0:
         raise ValueError(f"{name}: tensors must be on a CUDA device")
     if device != (_current_device or torch.cuda.current_device)():
         with torch.cuda.device(device):
-            return _call(name, device, stream, new, *args)
+            return _call(name, device, stream, *args)
     if stream is None:
         handle = (_raw_current_stream(device) if _raw_current_stream is not None
                   else torch.cuda.current_stream().cuda_stream)
@@ -154,8 +153,6 @@ def _call(name: str, device: int, stream, new, *args):
         if stream.device.index != device:
             raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on "
                              f"cuda:{device}")
-        for t in new:
-            t.record_stream(stream)
         handle = stream.cuda_stream
     st = getattr(_lib.load(), name)(*args, handle)
     if st != MOE_OK:
@@ -173,14 +170,20 @@ def _matrix(t, name: str):
     return t.shape
 
 
-def _out(t, name: str, dtype, shape, device: int, new: list):
-    """The caller's output tensor after its checks, or a new one (noted in
-    `new`)."""
+def _out(t, name: str, dtype, shape, device: int, stream):
+    """The caller's output tensor after its checks, or a new one.  For a
+    stream of the caller's it is of that stream's memory (the current stream
+    may still be at work on blocks that it has given back), and is kept for
+    the current one's uses too."""
     if t is not None:
         _tensor(t, name, (dtype,), shape, device)
         return t
-    t = torch.empty(shape, dtype=dtype, device=device if device >= 0 else "cpu")
-    new.append(t)
+    if stream is None or device < 0:
+        return torch.empty(shape, dtype=dtype, device=device if device >= 0 else "cpu")
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
     return t
 
 
@@ -191,10 +194,9 @@ def _route_biased(router_logits, score_bias, top_k, routing_method, renormalize,
     dev = router_logits.get_device()
     _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
     _tensor(score_bias, "score_bias", _F32, (E,), dev)
-    new = []
-    topk_weights = _out(topk_weights, "topk_weights", torch.float32, (M, top_k), dev, new)
-    topk_ids = _out(topk_ids, "topk_ids", torch.int32, (M, top_k), dev, new)
-    _call("moe_route_biased", dev, stream, new, router_logits.data_ptr(),
+    topk_weights = _out(topk_weights, "topk_weights", torch.float32, (M, top_k), dev, stream)
+    topk_ids = _out(topk_ids, "topk_ids", torch.int32, (M, top_k), dev, stream)
+    _call("moe_route_biased", dev, stream, router_logits.data_ptr(),
           int(router_logits.dtype == torch.bfloat16), score_bias.data_ptr(), M, E, top_k,
           ROUTING[routing_method], int(bool(renormalize)), k_group, group_count,
           group_select_mode, float(routed_scaling_factor), topk_weights.data_ptr(),
@@ -219,9 +221,8 @@ def moe_route_backward(grad_weights: torch.Tensor, router_logits: torch.Tensor,
     _tensor(grad_weights, "grad_weights", _F32, (M, k), dev)
     if error_word is not None:
         _tensor(error_word, "error_word", _I32, (1,), dev)
-    new = []
-    grad_logits = _out(grad_logits, "grad_logits", router_logits.dtype, (M, E), dev, new)
-    _call("moe_route_backward", dev, stream, new,
+    grad_logits = _out(grad_logits, "grad_logits", router_logits.dtype, (M, E), dev, stream)
+    _call("moe_route_backward", dev, stream,
           grad_weights.data_ptr(), router_logits.data_ptr(),
           int(router_logits.dtype == torch.bfloat16), topk_ids.data_ptr(), M, E, k,
           ROUTING[routing_method], int(bool(renormalize)), float(routed_scaling_factor),
@@ -376,13 +377,12 @@ def moe_quant_groups_fp8(x: torch.Tensor, swiglu: bool = False,
     if swiglu and cols % 2:
         raise ValueError("swiglu needs an even number of columns")
     K = cols // 2 if swiglu else cols
-    new = []
     if q8 is None or q8.dtype != torch.uint8:
-        q8 = _out(q8, "q8", torch.float8_e4m3fn, (M, K), dev, new)
+        q8 = _out(q8, "q8", torch.float8_e4m3fn, (M, K), dev, stream)
     else:
         _tensor(q8, "q8", _FP8, (M, K), dev)
-    scale = _out(scale, "scale", torch.float32, (M, -(-K // FP8_BLOCK)), dev, new)
-    _call("moe_quant_groups_fp8", dev, stream, new, x.data_ptr(), M, K,
+    scale = _out(scale, "scale", torch.float32, (M, -(-K // FP8_BLOCK)), dev, stream)
+    _call("moe_quant_groups_fp8", dev, stream, x.data_ptr(), M, K,
           int(bool(swiglu)), q8.data_ptr(), scale.data_ptr())
     return q8, scale
 
@@ -414,9 +414,8 @@ def moe_matmul_fp8(a_q: torch.Tensor, a_scale: torch.Tensor, w_q: torch.Tensor,
         out_dtype = out.dtype
     if out_dtype not in _LOGITS:
         raise ValueError("the output is torch.bfloat16 or torch.float32")
-    new = []
-    out = _out(out, "out", out_dtype, (M, N), dev, new)
-    _call("moe_matmul_fp8", dev, stream, new, a_q.data_ptr(),
+    out = _out(out, "out", out_dtype, (M, N), dev, stream)
+    _call("moe_matmul_fp8", dev, stream, a_q.data_ptr(),
           a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), int(bool(transposed)),
           None if bias is None else bias.data_ptr(), M, K, N, int(out_dtype == torch.float32),
           out.data_ptr(), None if error_word is None else error_word.data_ptr())

@@ -427,3 +427,21 @@ def test_layer_with_score_bias():
                                    spec.routed_scaling_factor)
     ref = oracle.forward(wl.to_f64(d["hidden"]), rw, rids, wl.to_f64(d["w13"]), wl.to_f64(d["w2"]))
     check_out(y.double().cpu().numpy(), ref, "layer with score bias")
+
+
+def test_results_on_a_stream_of_the_callers_come_from_its_memory():
+    """A block that the current stream has just given back may still be in use
+    by it: a result on another stream must not be put there."""
+    logits = torch.randn(512, 256, device="cuda")
+    bias = torch.zeros(256, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [torch.empty(512, 8, device="cuda") for _ in range(4)] + [
+        torch.empty(512, 256, device="cuda") for _ in range(2)]
+    at = {t.data_ptr() for t in old}
+    del old
+    w, ids = pkg.moe_route(logits, 8, score_bias=bias, stream=s)
+    gl = pkg.moe_route_backward(w, logits, ids, stream=s)
+    s.synchronize()
+    assert not at & {w.data_ptr(), ids.data_ptr(), gl.data_ptr()}
+    assert torch.equal(ids, pkg.moe_route(logits, 8, score_bias=bias)[1])
