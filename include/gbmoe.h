@@ -455,7 +455,7 @@ GBMOE_API moe_status_t moe_quant_rows_fp8(const void* x, int64_t M, int32_t H, v
  *  x      device bf16 [M, K], or [M, 2K] for swiglu
  *  q8     device E4M3 bytes [M, K], written
  *  scale  device fp32 [M, ceil(K / 128)], written
- * x and q8 16-byte aligned.  Limits: K a multiple of 16 up to 2^24, M < 2^31.
+ * q8 and scale must not overlap x; x and q8 16-byte aligned.  Limits: K a multiple of 16 up to 2^24, M < 2^31.
  */
 GBMOE_API moe_status_t moe_quant_groups_fp8(const void* x, int64_t M, int32_t K, int32_t swiglu,
                                             void* q8, float* scale, moe_stream_t stream);
@@ -473,7 +473,7 @@ GBMOE_API moe_status_t moe_quant_groups_fp8(const void* x, int64_t M, int32_t K,
  *  error_word device int32 or NULL: set to MOE_ERR_TIMEOUT if a pipeline
  *            wait ran out of time (the output is then incomplete)
  * a, w, bias and out 16-byte aligned.  Limits: K a multiple of 16 up to 2^24,
- * N a multiple of 16 up to 2^22, M < 2^31.
+ * N a multiple of 16 up to 2^22, M < 2^31, M * N <= 2^44.
  */
 GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const void* w,
                                       const float* w_scale, int32_t w_transposed,

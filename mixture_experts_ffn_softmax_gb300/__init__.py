@@ -167,6 +167,8 @@ _FP8 = (torch.float8_e4m3fn, torch.uint8)
 def _matrix(t, name: str):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-dimensional tensor")
+    if max(t.shape) >= 1 << 31:  # (the C entry points take 32-bit sizes)
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: sizes are below 2^31")
     return t.shape
 
 
@@ -377,7 +379,7 @@ def moe_quant_groups_fp8(x: torch.Tensor, swiglu: bool = False,
     if swiglu and cols % 2:
         raise ValueError("swiglu needs an even number of columns")
     K = cols // 2 if swiglu else cols
-    if q8 is None or q8.dtype != torch.uint8:
+    if getattr(q8, "dtype", None) != torch.uint8:
         q8 = _out(q8, "q8", torch.float8_e4m3fn, (M, K), dev, stream)
     else:
         _tensor(q8, "q8", _FP8, (M, K), dev)
@@ -411,7 +413,7 @@ def moe_matmul_fp8(a_q: torch.Tensor, a_scale: torch.Tensor, w_q: torch.Tensor,
     if error_word is not None:
         _tensor(error_word, "error_word", _I32, (1,), dev)
     if out is not None:
-        out_dtype = out.dtype
+        out_dtype = getattr(out, "dtype", None)
     if out_dtype not in _LOGITS:
         raise ValueError("the output is torch.bfloat16 or torch.float32")
     out = _out(out, "out", out_dtype, (M, N), dev, stream)

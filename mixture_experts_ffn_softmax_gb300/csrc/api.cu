@@ -1140,6 +1140,8 @@ moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const void* w,
   if (w_transposed != 0 && w_transposed != 1)
     return set_error(MOE_ERR_INVALID_ARG, "w_transposed=%d", w_transposed);
   if (out_f32 != 0 && out_f32 != 1) return set_error(MOE_ERR_INVALID_ARG, "out_f32=%d", out_f32);
+  if (M > (int64_t(1) << 44) / N)  // (tiles of the output are counted in 32 bits)
+    return set_error(MOE_ERR_INVALID_ARG, "M=%lld times N=%d above 2^44", (long long)M, N);
   if (M == 0) return MOE_OK;
   if (!a || !a_scale || !w || !w_scale || !out) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(a) || !aligned16(w) || !aligned16(out) || (bias && !aligned16(bias)) ||

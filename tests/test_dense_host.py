@@ -231,3 +231,36 @@ def test_binding_refuses_wrong_tensors():
         pkg.moe_matmul_fp8(q, sa, w, sw, out=torch.zeros(4, 32))
     with pytest.raises(ValueError, match="CUDA"):
         pkg.moe_matmul_fp8(q, sa, w, sw)
+
+
+def test_matmul_fp8_refuses_more_tiles_than_it_counts():
+    def mm(M, N):
+        p = _p(4096)
+        return pkg.lib().moe_matmul_fp8(p, p, p, p, 0, None, M, 64, N, 0, p, None, None)
+    assert mm((1 << 31) - 1, 1 << 22) == INVALID
+    assert mm((1 << 22) + 1, 1 << 22) == INVALID
+    if not torch.cuda.is_available():
+        assert mm(1 << 22, 1 << 22) == NO_DEVICE
+
+
+def test_binding_refuses_sizes_that_32_bits_would_cut():
+    def big(rows, cols, dtype):
+        return torch.zeros(1, 1, dtype=dtype).expand(rows, cols)
+    n = (1 << 32) + 16
+    u8 = torch.uint8
+    with pytest.raises(ValueError, match="below 2"):
+        pkg.moe_matmul_fp8(big(1, n, u8), torch.ones(1, 1), big(n, 16, u8), torch.ones(1, 1))
+    with pytest.raises(ValueError, match="below 2"):
+        pkg.moe_matmul_fp8(big(1, 16, u8), torch.ones(1, 1), big(16, n, u8), torch.ones(1, 1))
+    with pytest.raises(ValueError, match="below 2"):
+        pkg.moe_quant_groups_fp8(big(1, n, torch.bfloat16))
+    with pytest.raises(ValueError, match="below 2"):
+        pkg.moe_route(big(1, n, torch.float32), 2, score_bias=torch.zeros(8))
+    with pytest.raises(ValueError, match="below 2"):
+        pkg.moe_route_backward(torch.ones(1, 2), big(1, n, torch.float32),
+                               torch.zeros(1, 2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        pkg.moe_matmul_fp8(torch.zeros(1, 16, dtype=u8), torch.ones(1, 1),
+                           torch.zeros(16, 16, dtype=u8), torch.ones(1, 1), out=[0.0])
+    with pytest.raises(ValueError):
+        pkg.moe_quant_groups_fp8(torch.zeros(1, 16, dtype=torch.bfloat16), q8=[0])
