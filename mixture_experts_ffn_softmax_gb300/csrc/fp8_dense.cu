@@ -748,6 +748,12 @@ __global__ void __launch_bounds__(kDsThreads, 1)
           phase ^= 1u;
         }
       }
+      // the last stages' commits, which no load waits for, have to arrive
+      // before the barriers' memory goes
+      for (int i = max(0, kb1 - kb0 - G::STAGES); i < kb1 - kb0; ++i)
+        if (!dense_wait(&ctl.empty[i % G::STAGES], static_cast<uint32_t>(i / G::STAGES) & 1u,
+                        &ctl.abort, P.error_word))
+          break;
     }
   } else if (warp == 1) {
     if (lane == 0) {

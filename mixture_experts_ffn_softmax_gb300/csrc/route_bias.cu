@@ -896,6 +896,7 @@ void launch_fast(const RouteArgs& a, const float* bias, const RbParams& P, cudaS
   const bool whole =
       a.E % EPL == 0 && (a.k_group == a.group_count ||
                          (gs == lpg * EPL && (lpg & (lpg - 1)) == 0));
+  // at most the 16 blocks of four warps that an SM holds, on 152 of them
   launch_kernel(whole ? route_biased_kernel<EPL, LPT, true, T>
                       : route_biased_kernel<EPL, LPT, false, T>,
                 static_cast<unsigned>(std::min<int64_t>(blocks, 152 * 16)), warps * 32, smem, s,

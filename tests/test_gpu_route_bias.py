@@ -1,5 +1,8 @@
 """GPU parity of the routing with a bias (ids equal to the 64-bit oracle's,
 weights within fp32 rounding) and of the routing gradient."""
+import pathlib
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -445,3 +448,33 @@ def test_results_on_a_stream_of_the_callers_come_from_its_memory():
     s.synchronize()
     assert not at & {w.data_ptr(), ids.data_ptr(), gl.data_ptr()}
     assert torch.equal(ids, pkg.moe_route(logits, 8, score_bias=bias)[1])
+
+
+FIRST_IN_CAPTURE = """
+import torch
+import mixture_experts_ffn_softmax_gb300 as pkg
+E4M3 = torch.float8_e4m3fn
+l, b = torch.randn(70, 256, device="cuda"), torch.randn(256, device="cuda") * 0.1
+x = torch.randn(600, 512, device="cuda").to(torch.bfloat16)
+w13, w2 = torch.ones(512, 768, device="cuda").to(E4M3), torch.ones(384, 512, device="cuda").to(E4M3)
+s13, s2 = torch.ones(4, 6, device="cuda") / 64, torch.ones(3, 4, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    w, ids = pkg.moe_route(l, 8, "sigmoid", True, 4, 8, 1, 2.5, score_bias=b)
+    gl = pkg.moe_route_backward(w, l, ids, "sigmoid", True, 2.5)
+    y = pkg.moe_shared_expert_fp8(x, w13, w2, s13, s2)
+    y1 = pkg.moe_shared_expert_fp8(x[:9], w13, w2, s13, s2)
+g.replay()
+torch.cuda.synchronize()
+w_, ids_ = pkg.moe_route(l, 8, "sigmoid", True, 4, 8, 1, 2.5, score_bias=b)
+assert torch.equal(ids, ids_) and torch.equal(w, w_)
+assert torch.equal(gl, pkg.moe_route_backward(w, l, ids, "sigmoid", True, 2.5))
+assert torch.equal(y, pkg.moe_shared_expert_fp8(x, w13, w2, s13, s2))
+assert torch.equal(y1, pkg.moe_shared_expert_fp8(x[:9], w13, w2, s13, s2))
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    root = pathlib.Path(__file__).resolve().parents[1]
+    subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, check=True, timeout=300)
