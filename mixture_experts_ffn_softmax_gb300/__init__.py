@@ -167,9 +167,10 @@ _FP8 = (torch.float8_e4m3fn, torch.uint8)
 def _matrix(t, name: str):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-dimensional tensor")
-    if max(t.shape) >= 1 << 31:  # (the C entry points take 32-bit sizes)
-        raise ValueError(f"{name} has shape {tuple(t.shape)}: sizes are below 2^31")
-    return t.shape
+    rows, cols = shape = t.shape
+    if rows >= 1 << 31 or cols >= 1 << 31:  # (the C entry points take 32-bit sizes)
+        raise ValueError(f"{name} has shape {tuple(shape)}: sizes are below 2^31")
+    return shape
 
 
 def _out(t, name: str, dtype, shape, device: int, stream):

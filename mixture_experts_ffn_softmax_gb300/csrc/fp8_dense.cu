@@ -1010,33 +1010,33 @@ void split_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, int S, int n
 
 // Parts of K for the split kernel: the most whose clusters are all resident at
 // once (one cluster too many makes a second wave: 17 clusters of 8 took 20.7 us
-// for 128 x 4096 x 2064, 17 of 7 11.7).
+// for 128 x 4096 x 2064, 17 of 7 11.7).  What fits is asked once per host thread
+// and device (dev: the current one).
 template <int T, bool TR>
-int split_parts(int nt, int64_t mt, int KB, int num_sms) {
+int split_parts(int dev, int64_t clusters, int KB) {
   constexpr int MAX_S = 8;  // a portable cluster
-  static PerDevice attr, resident[MAX_S + 1];
-  attr.get([](int*) {
-    return cudaFuncSetAttribute(dense_fp8_split_kernel<T, TR>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(DsGeo<T>::SMEM));
-  });
-  int S = 1;
-  for (int c = 2; c <= std::min(MAX_S, KB); ++c) {
-    if (c * nt * mt > num_sms) break;
-    int clusters = 0;
-    if (resident[c].get(
-            [&](int* v) {
-              cudaLaunchConfig_t cfg = {};
-              cudaLaunchAttribute at[2];
-              split_config<T, TR>(cfg, at, c, 1, 1);
-              return cudaOccupancyMaxActiveClusters(v, dense_fp8_split_kernel<T, TR>, &cfg);
-            },
-            &clusters) != cudaSuccess) {
+  thread_local int room_dev = -1, room[MAX_S + 1];
+  if (dev != room_dev) {
+    if (cudaFuncSetAttribute(dense_fp8_split_kernel<T, TR>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(DsGeo<T>::SMEM)) != cudaSuccess) {
       cudaGetLastError();
-      break;
+      return 1;
     }
-    if (nt * mt <= clusters) S = c;
+    for (int c = 2; c <= MAX_S; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute at[2];
+      split_config<T, TR>(cfg, at, c, 1, 1);
+      if (cudaOccupancyMaxActiveClusters(&room[c], dense_fp8_split_kernel<T, TR>, &cfg) !=
+          cudaSuccess) {
+        cudaGetLastError();
+        room[c] = 0;
+      }
+    }
+    room_dev = dev;
   }
+  int S = 1;
+  for (int c = 2; c <= std::min(MAX_S, KB) && clusters <= room[c]; ++c) S = c;
   return S;
 }
 
@@ -1067,13 +1067,16 @@ template <bool TR>
 moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
   const int nt = ceil_div(a.N, 128), KB = ceil_div(a.K, 128);
   const int64_t pairs = ceil_div<int64_t>(a.M, 256) * ceil_div(a.N, 256);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "matmul_fp8: %s", cudaGetErrorString(cudaGetLastError()));
   float best = 4.8f + 0.45f * KB * static_cast<float>(ceil_div<int64_t>(pairs, a.num_sms / 2));
   int T = 256, S = 1;
   auto consider = [&](auto rows, float fixed, float per_block) {
     constexpr int R = decltype(rows)::value;
     const int64_t mt = ceil_div<int64_t>(a.M, R);
     if (mt > 64) return;  // the pairs' case, and a bound of the grid's y
-    const int parts = split_parts<R, TR>(nt, mt, KB, a.num_sms);
+    const int parts = split_parts<R, TR>(dev, nt * mt, KB);
     const int64_t waves = ceil_div<int64_t>(nt * mt * parts, a.num_sms);
     const float t = fixed + per_block * ceil_div(KB, parts) * static_cast<float>(waves);
     if (t < best) {
