@@ -8,6 +8,7 @@ PyTorch supplies device memory and the current stream.
     w, ids = moe_route(logits, top_k, "softmax", renormalize=True)
     y = moe_forward(hidden, w, ids, w13, w2)            # [M, H] bf16
     y = fused_moe(hidden, logits, w13, w2, top_k, ...)  # route + forward
+    y = moe_shared_expert_fp8(hidden, w13_q, w2_q, s13, s2)  # dense, FP8 block scales
 """
 from __future__ import annotations
 
