@@ -36,6 +36,7 @@ struct RbParams {
   int64_t M;
   int E, top_k, method, renormalize, k_group, group_count, group_select_mode;
   float scale;
+  int gs, lpg_log;  // experts of a group; log2 of the lanes that hold one (WHOLE, below)
 };
 
 // Order-preserving map of a double to an unsigned key, and back; NaN goes with
@@ -279,6 +280,16 @@ __device__ __forceinline__ float rb_seg_sum(float v) {
   return v;
 }
 
+// The largest key of a segment, by the warp's reduction (one for each half of the
+// warp: 5 instructions where exchanges take 8, and the shorter chain).
+template <int LPT>
+__device__ __forceinline__ uint32_t rb_seg_top(uint32_t v, int seg0) {
+  if constexpr (LPT == 32) return __reduce_max_sync(0xffffffffu, v);
+  const uint32_t first = __reduce_max_sync(0xffffffffu, seg0 == 0 ? v : 0u);
+  const uint32_t second = __reduce_max_sync(0xffffffffu, seg0 == 0 ? 0u : v);
+  return seg0 == 0 ? first : second;
+}
+
 // N consecutive logits as floats; vec: N elements at p are there and aligned.
 template <int N>
 __device__ __forceinline__ void rb_load(const float* p, float (&l)[N]) {
@@ -343,9 +354,9 @@ __device__ __forceinline__ void rb_load(const bf16* p, float (&l)[N]) {
 // WHOLE: lanes hold EPL experts or none, of one group (a power of two of lanes
 // to a group).
 //
-// Bound: issue slots.  8192 tokens x 256 experts, 8 of 4 of 8 groups, from
-// 281 us (every token by rb_choose64) to 11.5 us; 16384 x 128 bf16, 8 chosen,
-// 298 to 11 us.
+// Bound: issue slots and, for few tokens, the chain of one token (2.9 us of a graph
+// node with 256 experts).  8192 tokens x 256 experts, 8 of 4 of 8 groups, from 281 us
+// (every token by rb_choose64) to 11.3 us; 16384 x 128 bf16, 8 chosen, 298 to 10.6 us.
 template <int EPL, int LPT, bool WHOLE, typename T>
 __global__ void __launch_bounds__(kRbWarps * 32)
     route_biased_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
@@ -356,9 +367,9 @@ __global__ void __launch_bounds__(kRbWarps * 32)
   constexpr uint32_t MASK = LPT * EPL - 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sl = lane % LPT, seg0 = lane - sl;
-  const int E = P.E, G = P.group_count, k = P.top_k, gs = E / G;
+  const int E = P.E, G = P.group_count, k = P.top_k, gs = P.gs;
   const bool softmax = P.method == MOE_ROUTE_SOFTMAX, grouped = P.k_group < G;
-  const int e0 = sl * EPL, g0 = e0 / gs;
+  const int e0 = sl * EPL, g0 = WHOLE ? sl >> P.lpg_log : e0 / gs;
   auto exists = [&](int i) { return WHOLE ? e0 < E : e0 + i < E; };
   uint64_t* sm = rb_smem + warp * (E + G);
   float b[EPL];
@@ -418,7 +429,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     uint32_t kept = 0xffffffffu;
     if (grouped) {
       float gk = -INFINITY;  // lane g: group g's score
-      const int lpg = gs / EPL;  // WHOLE: lanes of a group
+      const int lpg = 1 << P.lpg_log;  // WHOLE: lanes of a group
       if constexpr (WHOLE) {
         float b1 = c[0], b2 = -INFINITY;
 #pragma unroll
@@ -547,7 +558,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     uint32_t mine = 0, last = 0;
     int left = 4;  // of the lane's four
     for (int r = 0; r < k + 2; ++r) {
-      last = rb_seg_max<LPT>(top4[0]);
+      last = rb_seg_top<LPT>(top4[0], seg0);
       if (sl == r) mine = last;
       if (top4[0] == last) {
         top4[0] = top4[1];
@@ -884,7 +895,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
 int rb_warps(const RouteArgs& a) { return a.E + a.group_count <= 1536 ? kRbWarps : kRbWarps / 2; }
 
 template <int EPL, int LPT, typename T>
-void launch_fast(const RouteArgs& a, const float* bias, const RbParams& P, cudaStream_t s) {
+void launch_fast(const RouteArgs& a, const float* bias, RbParams P, cudaStream_t s) {
   const int warps = rb_warps(a);
   const size_t smem = static_cast<size_t>(warps) * (a.E + a.group_count) * sizeof(uint64_t);
   const int64_t blocks = ceil_div<int64_t>(a.M, warps * (32 / LPT));
@@ -892,7 +903,8 @@ void launch_fast(const RouteArgs& a, const float* bias, const RbParams& P, cudaS
   const int bytes = EPL * static_cast<int>(sizeof(T)) < 16 ? EPL * static_cast<int>(sizeof(T)) : 16;
   const int vec = a.E % EPL == 0 && (a.E * sizeof(T)) % bytes == 0 &&
                   reinterpret_cast<uintptr_t>(a.logits) % bytes == 0;
-  const int gs = a.E / a.group_count, lpg = gs / EPL;
+  const int gs = P.gs, lpg = gs / EPL;
+  while ((2 << P.lpg_log) <= lpg) ++P.lpg_log;
   const bool whole =
       a.E % EPL == 0 && (a.k_group == a.group_count ||
                          (gs == lpg * EPL && (lpg & (lpg - 1)) == 0));
@@ -906,10 +918,14 @@ void launch_fast(const RouteArgs& a, const float* bias, const RbParams& P, cudaS
 template <typename T>
 void launch_biased(const RouteArgs& a, const float* bias, cudaStream_t s) {
   const RbParams P{a.M, a.E, a.top_k, a.method, a.renormalize, a.k_group, a.group_count,
-                   a.group_select_mode, a.scale};
+                   a.group_select_mode, a.scale, a.E / a.group_count, 0};
   const bool grouped = a.k_group < a.group_count;
-  // a candidate per lane (two beyond top_k), a group per lane
-  if (a.E <= 256 && a.top_k <= 14 && (!grouped || a.group_count <= 16)) {
+  // A candidate per lane (two beyond top_k), a group per lane.  Half a warp per token
+  // halves the instructions, a whole one shortens a token's chain and, from 65 experts
+  // on, wins up to 4096 tokens (half, whole; 256 experts: 1 token 3.3, 2.9 us; 4096: 8.4,
+  // 8.2; 16384: 15.1, 18.0; 128: 2.7, 2.2; 5.7, 5.4; 10.5, 11.0; 64: 2.2, 2.2; 4.9, 5.5).
+  const bool whole_warp = a.E > 64 && a.M <= 4096;
+  if (!whole_warp && a.E <= 256 && a.top_k <= 14 && (!grouped || a.group_count <= 16)) {
     if (a.E <= 32) return launch_fast<2, 16, T>(a, bias, P, s);
     if (a.E <= 64) return launch_fast<4, 16, T>(a, bias, P, s);
     if (a.E <= 128) return launch_fast<8, 16, T>(a, bias, P, s);

@@ -168,6 +168,30 @@ def test_route_biased_scores_in_falling_order_a_few_roundings_apart(E, k, G, kg,
         check_biased(torch.tensor(l, device="cuda"), bias, args(k, method, True, kg, G, 0))
 
 
+@pytest.mark.parametrize("E,k,G,kg,mode", [(256, 8, 8, 4, 1), (256, 14, 1, 1, 0), (128, 8, 1, 1, 0),
+                                           (160, 6, 5, 2, 1), (66, 5, 1, 1, 0), (192, 8, 16, 3, 0)])
+@pytest.mark.parametrize("method,renorm", [("sigmoid", True), ("softmax", True), ("softmax", False)])
+def test_route_biased_many_and_few_tokens(E, k, G, kg, mode, method, renorm):
+    """More tokens than a whole warp each is used for: normal rows, masked
+    ones, scores a few roundings apart; the same ids in parts of fewer tokens."""
+    M = 4097 + 72
+    rng = np.random.default_rng(E + k)
+    logits = rng.normal(size=(M, E)).astype(np.float32)
+    for t in range(64):
+        logits[t, rng.permutation(E)[:[1, E // 2, E - 3, E][t % 4]]] = -np.inf
+    step = 2.0 ** np.linspace(-27, -13, 256)[:, None]
+    logits[100:356] = (step * np.cumsum(1 + 0.5 * rng.random((256, E)), 1)).astype(np.float32)
+    logits[400:500] = np.round(logits[400:500] * 4) / 4               # ties
+    logits = torch.tensor(logits, device="cuda")
+    for spread in (0.0, 0.3):
+        bias = torch.tensor(rng.normal(size=E) * spread, dtype=torch.float32, device="cuda")
+        a = args(k, method, renorm, kg, G, mode, 2.5)
+        w, ids = check_biased(logits, bias, a)
+        pos = (a["k"], a["method"], a["renorm"], a["kg"], a["G"], a["mode"], a["scale"])
+        for part in (slice(0, 4096), slice(4096, M)):
+            assert torch.equal(pkg.moe_route(logits[part], *pos, score_bias=bias)[1], ids[part])
+
+
 @pytest.mark.parametrize("method", ["sigmoid", "softmax"])
 def test_route_biased_non_finite_scores(method):
     """Whatever the logits hold, ids are valid and distinct; other tokens keep
