@@ -650,9 +650,9 @@ constexpr int kDsScaleBlocks = 16;     // K blocks whose scales are held at a ti
 template <int T>
 struct DsGeo {
   static constexpr int STAGE = 16384 + T * 128;
-  static constexpr int STAGES = T <= 32 ? 8 : T == 64 ? 7 : 4;
-  static constexpr int ACCS = T == 128 ? 4 : 8;  // TMEM accumulators of T columns
-  static constexpr int COLS = ACCS * T;
+  static constexpr int STAGES = T <= 32 ? 8 : T == 64 ? 7 : T == 96 ? 5 : 4;
+  static constexpr int ACCS = T >= 96 ? 4 : 8;  // TMEM accumulators of T columns
+  static constexpr int COLS = T == 96 ? 512 : ACCS * T;  // (allocated: a power of two)
   // sums of S parts for the T / 4 row groups (up to 7 more slots than groups: the
   // groups of an owner are rounded up)
   static constexpr int PARTS = (T / 4 + 8) * 128 * 16;
@@ -671,6 +671,7 @@ struct DsCtl {
 static_assert(DsGeo<16>::SMEM + sizeof(DsCtl<16>) <= 232448 &&
                   DsGeo<32>::SMEM + sizeof(DsCtl<32>) <= 232448 &&
                   DsGeo<64>::SMEM + sizeof(DsCtl<64>) <= 232448 &&
+                  DsGeo<96>::SMEM + sizeof(DsCtl<96>) <= 232448 &&
                   DsGeo<128>::SMEM + sizeof(DsCtl<128>) <= 232448,
               "shared memory budget");
 
@@ -1074,9 +1075,11 @@ moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, int S, c
 // and one per K block of a CTA, as measured on GB300 (us; K x N of 7168 x 4096,
 // 2048 x 7168, 4096 x 2064 and 1024 x 1024, 1 to 2048 rows):
 //   split, 16 rows a tile: 3.5 + 0.35    32 rows: 3.7 + 0.36
-//          64 rows: 4.2 + 0.39           128 rows: 5.7 + 0.52
+//          64 rows: 4.2 + 0.39           96 rows: 5.0 + 0.43
+//         128 rows: 5.7 + 0.52
 //   pairs: 4.8 + 0.45
-// e.g. 256 x 7168 x 4096: 25.7 (64), 20.8 (128), 29.0 (pairs); 256 x 2048 x 7168:
+// e.g. 77 x 7168 x 4096: 12.3 (128), 11.1 (96); 192 x 4096 x 2064: 9.8, 8.6; 65 x 1024 x
+// 1024: 4.6 (64), 5.4 (96); 256 x 7168 x 4096: 25.7 (64), 20.8 (128), 29.0 (pairs); 256 x 2048 x 7168:
 // 19.9, 13.7, 12.1; 512 x 1024 x 1024: 5.9, 7.3, 8.6; 768 x 4096 x 2064: 31.5, 21.5,
 // 19.1.
 template <bool TR>
@@ -1102,12 +1105,14 @@ moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStr
     }
   };
   consider(std::integral_constant<int, 128>{}, 5.7f, 0.52f);
+  consider(std::integral_constant<int, 96>{}, 5.0f, 0.43f);
   consider(std::integral_constant<int, 64>{}, 4.2f, 0.39f);
   consider(std::integral_constant<int, 32>{}, 3.7f, 0.36f);
   consider(std::integral_constant<int, 16>{}, 3.5f, 0.35f);
   if (T == 16) return launch_split<16, TR>(a, P, S, s);
   if (T == 32) return launch_split<32, TR>(a, P, S, s);
   if (T == 64) return launch_split<64, TR>(a, P, S, s);
+  if (T == 96) return launch_split<96, TR>(a, P, S, s);
   if (T == 128) return launch_split<128, TR>(a, P, S, s);
   return launch_pair<TR>(a, P, s);
 }

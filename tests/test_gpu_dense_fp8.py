@@ -299,6 +299,16 @@ def test_matmul_with_pdl_off():
     assert torch.equal(out, (y + bias.double()).float())
 
 
+@pytest.mark.parametrize("M,K,N", [(65, 2048, 4112), (96, 1792, 4096), (150, 4096, 2064), (190, 2064, 4112)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_matmul_tiles_of_96_rows(M, K, N, transposed):
+    a, sa, w, sw, bias, y = exact_case(M, K, N, transposed, M + K)
+    out = pkg.moe_matmul_fp8(a, sa, w, sw, bias, transposed, torch.float32)
+    assert torch.equal(out, (y + bias.double()).float())
+    out = pkg.moe_matmul_fp8(a, sa, w, sw, transposed=transposed)
+    assert torch.equal(out, y.to(torch.bfloat16))
+
+
 # ----------------------------------------------------------- together --
 def shared_oracle(x, w13, w2, s13, s2, b13=None, b2=None):
     q, s = quantised(x)
