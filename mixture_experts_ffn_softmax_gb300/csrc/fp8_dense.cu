@@ -285,33 +285,45 @@ __device__ __forceinline__ void fma_pair(uint64_t& c, uint32_t a0, uint32_t a1, 
 }
 
 // ---- many rows: CTA pairs ----
-// Tile of 256 rows by 256 columns on a CTA pair (tcgen05 cta_group::2), each
-// CTA holding 128 rows.  A stage is 128 of K, one scale block: 128 rows of A
-// and 128 columns of the weight per CTA.  Each K block is an accumulation of
-// its own in one of two TMEM accumulators (256 columns each), scaled and added
-// into registers by eight warps (32 rows x 128 columns each) while the other
-// accumulator is filled.
+// Tile of 256 rows by NT = 256 or 128 columns on a CTA pair (tcgen05
+// cta_group::2), each CTA holding 128 rows.  A stage is 128 of K, one scale block:
+// 128 rows of A and NT / 2 columns of the weight per CTA.  Each K block is an
+// accumulation of its own in one of 512 / NT TMEM accumulators, scaled and added
+// into registers by eight warps (32 rows x NT / 2 columns each) while the others
+// are filled.  A K block of 256 columns takes 870 cycles (512 of MMA; the hand-off
+// without the sums 700, loads and MMAs alone 590), one of 128 columns 590: the narrow
+// tile is for products whose wide tiles would leave many pairs idle (512 x 7168 x 4096:
+// 29.7 us in 32 wide tiles, 21.5 in 64 narrow ones; 8192 x 7168 x 4096: 182 and 239).
 constexpr int kDpThreads = 128 + 256;  // TMA, 2 MMA, scale warp; 8 promotion warps
-// Registers: the launch holds 168 per thread; the first warpgroup returns
-// what it does not need and the promotion warps, with 128 sums each, take it.
+// Registers: the launch holds 168 per thread; for wide tiles the first warpgroup
+// returns what it does not need and the promotion warps, with 128 sums each, take it.
 constexpr int kDpRegsLaunch = 168, kDpRegsFew = 72, kDpRegsMany = 208;
 static_assert(128 * kDpRegsFew + 256 * kDpRegsMany <= kDpThreads * kDpRegsLaunch,
               "register split within the launch's registers");
-constexpr int kDpStages = 5;
-constexpr int kDpStage = 2 * 16384;    // A 128 x 128 bytes, weight 128 x 128 bytes
 constexpr int kDpStaging = 8 * 4096;   // per promotion warp 32 rows x 128 bytes of output
-constexpr int kDpScales = 4;           // scale slots (K blocks)
 constexpr int kDpGroupM = 8;           // row tiles of a raster group
-constexpr size_t kDpSmem = 1024 + kDpStages * kDpStage + kDpStaging;
+template <int NT>  // columns of a tile
+struct DpGeo {
+  static constexpr int STAGES = NT == 256 ? 5 : 7;
+  static constexpr int STAGE = 16384 + NT / 2 * 128;  // A 128 x 128 bytes, weight 128 x NT / 2
+  static constexpr int ACCS = 512 / NT;               // TMEM accumulators
+  static constexpr int SCALES = 2 * ACCS;             // scale slots (K blocks)
+  static constexpr int AHEAD = NT == 256 ? 2 : 4;     // K blocks whose scales are loaded together
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE + kDpStaging;
+};
 
+template <int NT>
 struct DpCtl {
-  uint64_t full[kDpStages], empty[kDpStages];
-  uint64_t tmem_full[2], tmem_empty[2];
-  float a_scale[kDpScales][128], w_scale[kDpScales][2];  // rows, column blocks of a K block
+  using G = DpGeo<NT>;
+  uint64_t full[G::STAGES], empty[G::STAGES];
+  uint64_t tmem_full[G::ACCS], tmem_empty[G::ACCS];
+  float a_scale[G::SCALES][128], w_scale[G::SCALES][2];  // rows, column blocks of a K block
   uint32_t tmem_base;
   int32_t abort;
 };
-static_assert(kDpSmem + sizeof(DpCtl) <= 232448, "shared memory budget");
+static_assert(DpGeo<256>::SMEM + sizeof(DpCtl<256>) <= 232448 &&
+                  DpGeo<128>::SMEM + sizeof(DpCtl<128>) <= 232448,
+              "shared memory budget");
 
 // The two halves of a cluster barrier; this arrival orders nothing (a releasing
 // one waits for the thread's loads in flight).
@@ -364,24 +376,30 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, int lane, const uint64_t
   }
 }
 
-template <bool TR>
+// As smem_desc_sw128 with the 64-byte swizzle (mode 4): MN-major rows of 64 bytes.
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (ptx::smem_desc_sw128(saddr, lbo, sbo) & ~(uint64_t(7) << 61)) | uint64_t(4) << 61;
+}
+
+template <bool TR, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
     dense_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmO, const DenseParams P) {
+  using G = DpGeo<NT>;
   pdl_begin();
   extern __shared__ uint8_t smem_raw[];
-  __shared__ DpCtl ctl;
+  __shared__ DpCtl<NT> ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   uint8_t* tiles = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* staging = tiles + kDpStages * kDpStage;
+  uint8_t* staging = tiles + G::STAGES * G::STAGE;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kDpStages; ++i) {
+    for (int i = 0; i < G::STAGES; ++i) {
       ptx::mbar_init(&ctl.full[i], 1);
       ptx::mbar_init(&ctl.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < G::ACCS; ++i) {
       ptx::mbar_init(&ctl.tmem_full[i], 2);        // the MMA's commit, the scale warp
       ptx::mbar_init(&ctl.tmem_empty[i], 2 * 8);   // the promotion warps of both CTAs
     }
@@ -401,14 +419,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
   const uint32_t tmem = ctl.tmem_base;
 
   const int KB = ceil_div(P.K, 128), NB = ceil_div(P.N, 128);
-  const int mt = static_cast<int>(ceil_div<int64_t>(P.M, 256)), nt = ceil_div(P.N, 256);
+  const int mt = static_cast<int>(ceil_div<int64_t>(P.M, 256)), nt = ceil_div(P.N, NT);
   const int total = mt * nt;
   const int unit = static_cast<int>(blockIdx.x >> 1), units = static_cast<int>(gridDim.x >> 1);
   const int64_t blocks =  // K blocks of this pair
       unit < total ? static_cast<int64_t>((total - 1 - unit) / units + 1) * KB : 0;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDpRegsFew));
+    if constexpr (NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDpRegsFew));
     if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
@@ -416,20 +434,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
       for (int t = unit; t < total && ok; t += units) {
         const TileMN tl = dense_tile(t, mt, nt);
         const int row = tl.m * 256 + static_cast<int>(rank) * 128;
-        const int col = tl.n * 256 + static_cast<int>(rank) * 128;
+        const int col = tl.n * NT + static_cast<int>(rank) * (NT / 2);
         for (int kb = 0; kb < KB; ++kb) {
           if (!dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word)) {
             ok = false;
             break;
           }
-          uint8_t* sa = tiles + stage * kDpStage;
+          uint8_t* sa = tiles + stage * G::STAGE;
           uint8_t* sb = sa + 16384;
           // both CTAs' copies complete on the even CTA's barrier
           const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&ctl.full[stage], 2 * kDpStage);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&ctl.full[stage], 2 * G::STAGE);
           ptx::tma_load_2d_pair(sa, &tmA, full0, kb * 128, row);
           ptx::tma_load_2d_pair(sb, &tmB, full0, TR ? kb * 128 : col, TR ? col : kb * 128);
-          if (++stage == kDpStages) {
+          if (++stage == G::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -440,48 +458,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
       // queued ahead of its own, the other's waits and commits go on
       // (8192 x 7168 x 4096: 194 us with one thread for both, 180 with two)
       if (lane == 0 && rank == 0) {
-        const uint32_t acc = warp - 1;
-        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, 256, false, !TR);
-        int stage = acc;  // blocks acc, acc + 2, ...
+        uint32_t acc = warp - 1;
+        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, NT, false, !TR);
+        int stage = acc;  // blocks warp - 1, warp + 1, ...
         uint32_t phase = 0, turn = 0;
         for (int64_t g = acc; g < blocks; g += 2) {
           if (!dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word) ||
               !dense_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word))
             break;
-          turn ^= 1u;
           ptx::tc_fence_after();
-          const uint32_t sa = ptx::smem_u32(tiles + stage * kDpStage), sb = sa + 16384;
+          const uint32_t sa = ptx::smem_u32(tiles + stage * G::STAGE), sb = sa + 16384;
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             const uint64_t ad = ptx::smem_desc_sw128(sa + ks * 32, 16, 1024);
             const uint64_t bd = TR ? ptx::smem_desc_sw128(sb + ks * 32, 16, 1024)
-                                   : ptx::smem_desc_sw128(sb + ks * 4096, 16384, 1024);
-            ptx::mma_e4m3_pair(tmem + acc * 256, ad, bd, idesc, ks != 0);
+                                   : NT == 256
+                                         ? ptx::smem_desc_sw128(sb + ks * 4096, 16384, 1024)
+                                         : smem_desc_sw64(sb + ks * 2048, 8192, 512);
+            ptx::mma_e4m3_pair(tmem + acc * NT, ad, bd, idesc, ks != 0);
           }
           // (the accumulator's barrier first: the other order took a K-rows
           // weight from 182 to 206 us at 8192 x 7168 x 4096)
           ptx::mma_commit_pair(&ctl.tmem_full[acc], 0x3);
           ptx::mma_commit_pair(&ctl.empty[stage], 0x3);
           stage += 2;
-          if (stage >= kDpStages) {
-            stage -= kDpStages;
+          if (stage >= G::STAGES) {
+            stage -= G::STAGES;
             phase ^= 1u;
+          }
+          acc += 2;
+          if (acc >= G::ACCS) {
+            acc -= G::ACCS;
+            turn ^= 1u;
           }
         }
       }
     } else {
-      // scales of the promotion warps' next blocks: four rows per lane, of two K
-      // blocks at a time and loaded two blocks ahead (across tiles too).  In
-      // the promotion warps, short of registers to hold them, these loads'
-      // latency came into every group of blocks.
-      float nx[4][2], nw[2];  // (w: lanes 0 and 1, one column block each)
-      auto load2 = [&](int t, int kb0) {
+      // scales of the promotion warps' next blocks: four rows per lane, of A K
+      // blocks at a time and loaded A blocks ahead (across tiles too; narrow tiles with
+      // two ahead: 25.0 us for 512 x 7168 x 4096, 21.5 with four, for which the wide
+      // tiles' kernel has no registers).  In the promotion warps, short of registers
+      // to hold them, these loads' latency came into every group of blocks.
+      constexpr int A = G::AHEAD;
+      float nx[4][A], nw[A];  // (w: lanes 0 and 1, one column block each)
+      auto load = [&](int t, int kb0) {
         const TileMN tl = dense_tile(t, mt, nt);
         const int64_t m = static_cast<int64_t>(tl.m) * 256 + rank * 128 + lane;
-        const int nb = min(tl.n * 2 + (lane & 1), NB - 1);
+        const int nb = min(NT == 256 ? tl.n * 2 + (lane & 1) : tl.n, NB - 1);
         const float* pw = P.w_scale + (TR ? static_cast<int64_t>(nb) * KB : nb);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < A; ++j) {
           const int kb = min(kb0 + j, KB - 1);
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -489,60 +515,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
           nw[j] = __ldg(pw + (TR ? kb : static_cast<int64_t>(kb) * NB));
         }
       };
-      if (unit < total) load2(unit, 0);
+      if (unit < total) load(unit, 0);
       uint32_t g = 0;  // K blocks so far
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        for (int kb = 0; kb < KB && ok; kb += 2) {
-          float c[4][2], cw[2];
+        for (int kb = 0; kb < KB && ok; kb += A) {
+          float c[4][A], cw[A];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < A; ++j) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) c[r][j] = nx[r][j];
             cw[j] = nw[j];
           }
-          if (kb + 2 < KB)
-            load2(t, kb + 2);
+          if (kb + A < KB)
+            load(t, kb + A);
           else if (t + units < total)
-            load2(t + units, 0);
+            load(t + units, 0);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < A; ++j) {
             if (kb + j >= KB) break;
-            // block g - 2 complete means that block g - 4, whose slot this is,
-            // has left the accumulators and the slot: the MMA of g - 2 waited
+            // block g - ACCS complete means that block g - 2 ACCS, whose slot this
+            // is, has left the accumulators and the slot: the MMA of g - ACCS waited
             // for its release
             bool got = true;
-            if (g >= 2)
-              got = dense_wait(&ctl.tmem_full[g & 1], (g >> 1 & 1) ^ 1u, &ctl.abort, P.error_word);
+            const int acc = g % G::ACCS;
+            if (g >= G::ACCS)
+              got = dense_wait(&ctl.tmem_full[acc], (g / G::ACCS & 1) ^ 1u, &ctl.abort,
+                               P.error_word);
             if (!__all_sync(0xffffffffu, got)) {
               ok = false;
               break;
             }
-            const int slot = g % kDpScales;
+            const int slot = g % G::SCALES;
 #pragma unroll
             for (int r = 0; r < 4; ++r) ctl.a_scale[slot][lane + 32 * r] = c[r][j];
             if (lane < 2) ctl.w_scale[slot][lane] = cw[j];
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&ctl.tmem_full[g & 1]);
+            if (lane == 0) ptx::mbar_arrive(&ctl.tmem_full[acc]);
             ++g;
           }
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDpRegsMany));
+    if constexpr (NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDpRegsMany));
     const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * (NT / 2);
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tmem_empty[0]), 0);
     uint8_t* buf = staging + (warp - 4) * 4096;
     uint32_t g = 0;  // K blocks so far
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
-      uint64_t sum[64];  // 128 columns
-      const int n0 = dense_tile(t, mt, nt).n * 256 + half * 128;
+      uint64_t sum[NT / 4];  // NT / 2 columns
+      const int n0 = dense_tile(t, mt, nt).n * NT + half * (NT / 2);
       if (P.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 8) {  // (N is a multiple of 16)
+        for (int j = 0; j < NT / 2; j += 8) {  // (N is a multiple of 16)
           float b[8] = {};
           if (n0 + j < P.N) unpack8(__ldg(reinterpret_cast<const uint4*>(P.bias + n0 + j)), b);
 #pragma unroll
@@ -550,27 +578,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) sum[j] = 0;
+        for (int j = 0; j < NT / 4; ++j) sum[j] = 0;
       }
       for (int kb = 0; kb < KB; ++kb, ++g) {
-        const uint32_t acc = g & 1;
+        const uint32_t acc = g % G::ACCS;
         const bool got =
-            dense_wait(&ctl.tmem_full[acc], g >> 1 & 1, &ctl.abort, P.error_word);
+            dense_wait(&ctl.tmem_full[acc], g / G::ACCS & 1, &ctl.abort, P.error_word);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t ta = lane_addr + acc * 256;
+        const uint32_t ta = lane_addr + acc * NT;
         uint32_t v[2][16];
         ptx::tmem_ld_16cols(ta, v[0]);
-        const int slot = g % kDpScales;
-        const float f = ctl.a_scale[slot][q * 32 + lane] * ctl.w_scale[slot][half];
+        const int slot = g % G::SCALES;
+        const float f = ctl.a_scale[slot][q * 32 + lane] * ctl.w_scale[slot][NT == 256 ? half : 0];
         const uint64_t sc = pair_of(f, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < NT / 32; ++i) {
           tmem_wait(v[i & 1]);
-          if (i < 7) {
+          if (i < NT / 32 - 1) {
             ptx::tmem_ld_16cols(ta + 16 * (i + 1), v[(i + 1) & 1]);
           } else {  // the accumulator is in registers
             ptx::tc_fence_before();
@@ -592,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
         constexpr bool F32 = decltype(f32)::value;
         constexpr int W = F32 ? 32 : 64;
 #pragma unroll
-        for (int i = 0; i < 128 / W; ++i) {
+        for (int i = 0; i < NT / 2 / W; ++i) {
           const int n = n0 + i * W;
           if (n < P.N && m < P.M) {
             if (lane == 0) ptx::bulk_wait_read0();
@@ -620,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
   // before the barriers' memory goes
   if (threadIdx.x < 2 && blocks > static_cast<int>(threadIdx.x)) {
     const int64_t g = blocks - 1 - threadIdx.x;
-    dense_wait(&ctl.empty[g % kDpStages], static_cast<uint32_t>(g / kDpStages) & 1u, &ctl.abort,
+    dense_wait(&ctl.empty[g % G::STAGES], static_cast<uint32_t>(g / G::STAGES) & 1u, &ctl.abort,
                P.error_word);
   }
   if (*reinterpret_cast<volatile int32_t*>(&ctl.abort)) {
@@ -952,17 +980,18 @@ __global__ void __launch_bounds__(kDsThreads, 1)
 
 // Tensor maps of A [M, K], in boxes of a_rows x 128 bytes, and of the weight,
 // in boxes of 128 x 128 bytes.
-moe_status_t dense_maps(const MatmulFp8Args& a, uint32_t a_rows, CUtensorMap* tmA,
+moe_status_t dense_maps(const MatmulFp8Args& a, uint32_t a_rows, uint32_t w_cols, CUtensorMap* tmA,
                         CUtensorMap* tmB) {
   const uint64_t K = a.K, N = a.N;
   const uint64_t da[2] = {K, static_cast<uint64_t>(a.M)}, sa[1] = {K};
-  const uint32_t ba[2] = {128, a_rows}, bb[2] = {128, 128};
+  const uint32_t ba[2] = {128, a_rows};
+  const uint32_t bb[2] = {a.transposed ? 128 : w_cols, a.transposed ? w_cols : 128};
   if (moe_status_t st = encode_tensor_map(tmA, a.a, 2, da, sa, ba, CU_TENSOR_MAP_DATA_TYPE_UINT8,
                                           CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
   const uint64_t db[2] = {a.transposed ? K : N, a.transposed ? N : K}, sb[1] = {db[0]};
   return encode_tensor_map(tmB, a.w, 2, db, sb, bb, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                           CU_TENSOR_MAP_SWIZZLE_128B);
+                           bb[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Tensor map of the output, boxes of 32 rows x 128 bytes.
@@ -977,34 +1006,34 @@ moe_status_t dense_out_map(const MatmulFp8Args& a, CUtensorMap* tmO) {
       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool TR>
+template <bool TR, int NT>
 moe_status_t launch_pair(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
   static PerDevice attr;
   int regs = 0;
   if (attr.get(
           [](int* v) {
             cudaFuncAttributes fa;
-            const cudaError_t e = cudaFuncGetAttributes(&fa, dense_fp8_pair_kernel<TR>);
+            const cudaError_t e = cudaFuncGetAttributes(&fa, dense_fp8_pair_kernel<TR, NT>);
             if (e != cudaSuccess) return e;
             *v = fa.numRegs;
-            return cudaFuncSetAttribute(dense_fp8_pair_kernel<TR>,
+            return cudaFuncSetAttribute(dense_fp8_pair_kernel<TR, NT>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(kDpSmem));
+                                        static_cast<int>(DpGeo<NT>::SMEM));
           },
           &regs) != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "attributes of matmul_fp8: %s",
                      cudaGetErrorString(cudaGetLastError()));
   // fewer registers at launch would leave the promotion warps waiting for more
-  if (regs < kDpRegsLaunch)
+  if (NT == 256 && regs < kDpRegsLaunch)
     return set_error(MOE_ERR_CUDA, "matmul_fp8 was compiled to %d registers, %d needed", regs,
                      kDpRegsLaunch);
   CUtensorMap tmA, tmB, tmO;
-  if (moe_status_t st = dense_maps(a, 128, &tmA, &tmB)) return st;
+  if (moe_status_t st = dense_maps(a, 128, NT / 2, &tmA, &tmB)) return st;
   if (moe_status_t st = dense_out_map(a, &tmO)) return st;
-  const int64_t tiles = ceil_div<int64_t>(a.M, 256) * ceil_div(a.N, 256);
+  const int64_t tiles = ceil_div<int64_t>(a.M, 256) * ceil_div(a.N, NT);
   const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, a.num_sms / 2));
   prof_before("matmul_fp8", s);
-  launch_kernel(dense_fp8_pair_kernel<TR>, grid, kDpThreads, kDpSmem, s, tmA, tmB, tmO, P);
+  launch_kernel(dense_fp8_pair_kernel<TR, NT>, grid, kDpThreads, DpGeo<NT>::SMEM, s, tmA, tmB, tmO, P);
   prof_after("matmul_fp8", s);
   return check_launch("matmul_fp8");
 }
@@ -1060,7 +1089,7 @@ int split_parts(int dev, int64_t clusters, int KB) {
 template <int T, bool TR>
 moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, int S, cudaStream_t s) {
   CUtensorMap tmA, tmB;
-  if (moe_status_t st = dense_maps(a, T, &tmA, &tmB)) return st;
+  if (moe_status_t st = dense_maps(a, T, 128, &tmA, &tmB)) return st;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[2];
   split_config<T, TR>(cfg, at, S, ceil_div(a.N, 128), ceil_div<int64_t>(a.M, T));
@@ -1077,20 +1106,28 @@ moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, int S, c
 //   split, 16 rows a tile: 3.5 + 0.35    32 rows: 3.7 + 0.36
 //          64 rows: 4.2 + 0.39           96 rows: 5.0 + 0.43
 //         128 rows: 5.7 + 0.52
-//   pairs: 4.8 + 0.45
+//   pairs, 256 columns a tile: 4.8 + 0.45    128 columns: 4.7 + 0.305
 // e.g. 77 x 7168 x 4096: 12.3 (128), 11.1 (96); 192 x 4096 x 2064: 9.8, 8.6; 65 x 1024 x
-// 1024: 4.6 (64), 5.4 (96); 256 x 7168 x 4096: 25.7 (64), 20.8 (128), 29.0 (pairs); 256 x 2048 x 7168:
-// 19.9, 13.7, 12.1; 512 x 1024 x 1024: 5.9, 7.3, 8.6; 768 x 4096 x 2064: 31.5, 21.5,
-// 19.1.
+// 1024: 4.6 (64), 5.4 (96); 256 x 7168 x 4096: 25.7 (64), 20.8 (128), 29.0 (wide pairs);
+// 256 x 2048 x 7168: 13.7 (128), 12.1 (wide), 9.4 (narrow pairs); 512 x 7168 x 4096: 29.7
+// (wide), 21.5; 1999 x 4096 x 2064: 21.2, 25.6; 512 x 1024 x 1024: 5.9 (64), 7.3 (128).
 template <bool TR>
 moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
   const int nt = ceil_div(a.N, 128), KB = ceil_div(a.K, 128);
-  const int64_t pairs = ceil_div<int64_t>(a.M, 256) * ceil_div(a.N, 256);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "matmul_fp8: %s", cudaGetErrorString(cudaGetLastError()));
-  float best = 4.8f + 0.45f * KB * static_cast<float>(ceil_div<int64_t>(pairs, a.num_sms / 2));
-  int T = 256, S = 1;
+  // T: rows of a split kernel's tile; 512 and 256 stand for the wide and narrow pairs
+  const int64_t mt2 = ceil_div<int64_t>(a.M, 256), nt2 = ceil_div(a.N, 256);
+  const auto pairs = [&](float fixed, float per_block, int64_t tiles) {
+    return fixed + per_block * KB * static_cast<float>(ceil_div<int64_t>(tiles, a.num_sms / 2));
+  };
+  float best = pairs(4.8f, 0.45f, mt2 * nt2);
+  int T = 512, S = 1;
+  if (const float t = pairs(4.7f, 0.305f, mt2 * nt); t < best) {
+    best = t;
+    T = 256;
+  }
   auto consider = [&](auto rows, float fixed, float per_block) {
     constexpr int R = decltype(rows)::value;
     const int64_t mt = ceil_div<int64_t>(a.M, R);
@@ -1114,7 +1151,8 @@ moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStr
   if (T == 64) return launch_split<64, TR>(a, P, S, s);
   if (T == 96) return launch_split<96, TR>(a, P, S, s);
   if (T == 128) return launch_split<128, TR>(a, P, S, s);
-  return launch_pair<TR>(a, P, s);
+  if (T == 256) return launch_pair<TR, 128>(a, P, s);
+  return launch_pair<TR, 256>(a, P, s);
 }
 
 }  // namespace

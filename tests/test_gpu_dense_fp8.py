@@ -309,6 +309,21 @@ def test_matmul_tiles_of_96_rows(M, K, N, transposed):
     assert torch.equal(out, y.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("M,K,N", [(384, 2064, 4112), (600, 1104, 2832), (257, 2048, 7168), (1500, 400, 3200)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_matmul_pairs_with_narrow_tiles(M, K, N, transposed):
+    """Few wide tiles, and (the last) several narrow ones per pair."""
+    a, sa, w, sw, bias, y = exact_case(M, K, N, transposed, M + K)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.full((M + 2, N), 7.0, device="cuda", dtype=dt)
+        pkg.moe_matmul_fp8(a, sa, w, sw, bias, transposed, out=out[1:M + 1], error_word=err)
+        assert torch.equal(out[1:M + 1], (y + bias.double()).to(dt))
+        assert (out[0] == 7).all() and (out[M + 1] == 7).all()
+    assert torch.equal(pkg.moe_matmul_fp8(a, sa, w, sw, transposed=transposed), y.to(torch.bfloat16))
+    assert err.item() == 0
+
+
 # ----------------------------------------------------------- together --
 def shared_oracle(x, w13, w2, s13, s2, b13=None, b2=None):
     q, s = quantised(x)
