@@ -123,11 +123,9 @@ def moe_route(router_logits: torch.Tensor, top_k: int, routing_method: str = "so
 
 def _tensor(t, name: str, dtypes, shape, device: int):
     """Checks an argument of the functions that take them as they come: type,
-    shape, contiguity, and the device of the call.  (One expression where all
-    is well: these calls are a few microseconds long.)"""
-    if (type(t) is torch.Tensor and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
-            and t.get_device() == device):
-        return
+    shape, contiguity, and the device of the call.  (The functions test all of
+    their inputs in one expression first and come here where it fails: a call
+    is a few microseconds long, and these checks one by one were one of them.)"""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a tensor of {' or '.join(map(str, dtypes))}")
     if t.shape != shape:
@@ -155,11 +153,15 @@ def _call(name: str, device: int, stream, *args):
             raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on "
                              f"cuda:{device}")
         handle = stream.cuda_stream
-    st = getattr(_lib.load(), name)(*args, handle)
+    fn = _entry_points.get(name)
+    if fn is None:
+        fn = _entry_points[name] = getattr(_lib.load(), name)
+    st = fn(*args, handle)
     if st != MOE_OK:
         _check(st, name)
 
 
+_entry_points = {}
 _LOGITS = (torch.float32, torch.bfloat16)
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
@@ -180,7 +182,9 @@ def _out(t, name: str, dtype, shape, device: int, stream):
     may still be at work on blocks that it has given back), and is kept for
     the current one's uses too."""
     if t is not None:
-        _tensor(t, name, (dtype,), shape, device)
+        if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous() and t.get_device() == device):
+            _tensor(t, name, (dtype,), shape, device)
         return t
     if stream is None or device < 0:
         return torch.empty(shape, dtype=dtype, device=device if device >= 0 else "cpu")
@@ -196,8 +200,15 @@ def _route_biased(router_logits, score_bias, top_k, routing_method, renormalize,
                   stream):
     M, E = _matrix(router_logits, "router_logits")
     dev = router_logits.get_device()
-    _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
-    _tensor(score_bias, "score_bias", _F32, (E,), dev)
+    try:
+        fine = (router_logits.dtype in _LOGITS and router_logits.is_contiguous()
+                and score_bias.dtype is torch.float32 and score_bias.shape == (E,)
+                and score_bias.is_contiguous() and score_bias.get_device() == dev)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
+        _tensor(score_bias, "score_bias", _F32, (E,), dev)
     topk_weights = _out(topk_weights, "topk_weights", torch.float32, (M, top_k), dev, stream)
     topk_ids = _out(topk_ids, "topk_ids", torch.int32, (M, top_k), dev, stream)
     _call("moe_route_biased", dev, stream, router_logits.data_ptr(),
@@ -220,9 +231,18 @@ def moe_route_backward(grad_weights: torch.Tensor, router_logits: torch.Tensor,
     M, E = _matrix(router_logits, "router_logits")
     k = _matrix(topk_ids, "topk_ids")[1]
     dev = router_logits.get_device()
-    _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
-    _tensor(topk_ids, "topk_ids", _I32, (M, k), dev)
-    _tensor(grad_weights, "grad_weights", _F32, (M, k), dev)
+    try:
+        fine = (router_logits.dtype in _LOGITS and router_logits.is_contiguous()
+                and topk_ids.dtype is torch.int32 and topk_ids.shape[0] == M
+                and topk_ids.is_contiguous() and topk_ids.get_device() == dev
+                and grad_weights.dtype is torch.float32 and grad_weights.shape == (M, k)
+                and grad_weights.is_contiguous() and grad_weights.get_device() == dev)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(router_logits, "router_logits", _LOGITS, (M, E), dev)
+        _tensor(topk_ids, "topk_ids", _I32, (M, k), dev)
+        _tensor(grad_weights, "grad_weights", _F32, (M, k), dev)
     if error_word is not None:
         _tensor(error_word, "error_word", _I32, (1,), dev)
     grad_logits = _out(grad_logits, "grad_logits", router_logits.dtype, (M, E), dev, stream)
@@ -377,7 +397,8 @@ def moe_quant_groups_fp8(x: torch.Tensor, swiglu: bool = False,
     is what is quantised."""
     M, cols = _matrix(x, "x")
     dev = x.get_device()
-    _tensor(x, "x", _BF16, (M, cols), dev)
+    if not (x.dtype is torch.bfloat16 and x.is_contiguous()):
+        _tensor(x, "x", _BF16, (M, cols), dev)
     if swiglu and cols % 2:
         raise ValueError("swiglu needs an even number of columns")
     K = cols // 2 if swiglu else cols
@@ -406,10 +427,22 @@ def moe_matmul_fp8(a_q: torch.Tensor, a_scale: torch.Tensor, w_q: torch.Tensor,
     N = rows if transposed else cols
     dev = a_q.get_device()
     KB, NB = -(-K // FP8_BLOCK), -(-N // FP8_BLOCK)
-    _tensor(a_q, "a_q", _FP8, (M, K), dev)
-    _tensor(a_scale, "a_scale", _F32, (M, KB), dev)
-    _tensor(w_q, "w_q", _FP8, (N, K) if transposed else (K, N), dev)
-    _tensor(w_scale, "w_scale", _F32, (NB, KB) if transposed else (KB, NB), dev)
+    try:
+        fine = (a_q.dtype in _FP8 and a_q.is_contiguous()
+                and a_scale.dtype is torch.float32 and a_scale.shape == (M, KB)
+                and a_scale.is_contiguous() and a_scale.get_device() == dev
+                and w_q.dtype in _FP8 and (cols if transposed else rows) == K
+                and w_q.is_contiguous() and w_q.get_device() == dev
+                and w_scale.dtype is torch.float32
+                and w_scale.shape == ((NB, KB) if transposed else (KB, NB))
+                and w_scale.is_contiguous() and w_scale.get_device() == dev)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(a_q, "a_q", _FP8, (M, K), dev)
+        _tensor(a_scale, "a_scale", _F32, (M, KB), dev)
+        _tensor(w_q, "w_q", _FP8, (N, K) if transposed else (K, N), dev)
+        _tensor(w_scale, "w_scale", _F32, (NB, KB) if transposed else (KB, NB), dev)
     if bias is not None:
         _tensor(bias, "bias", _BF16, (N,), dev)
     if error_word is not None:
