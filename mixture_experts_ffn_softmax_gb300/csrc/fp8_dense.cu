@@ -290,10 +290,10 @@ __device__ __forceinline__ void fma_pair(uint64_t& c, uint32_t a0, uint32_t a1, 
 // 128 rows of A and NT / 2 columns of the weight per CTA.  Each K block is an
 // accumulation of its own in one of 512 / NT TMEM accumulators, scaled and added
 // into registers by eight warps (32 rows x NT / 2 columns each) while the others
-// are filled.  A K block of 256 columns takes 870 cycles (512 of MMA; the hand-off
+// are filled.  A K block of 256 columns takes 830 cycles (512 of MMA; the hand-off
 // without the sums 700, loads and MMAs alone 590), one of 128 columns 590: the narrow
 // tile is for products whose wide tiles would leave many pairs idle (512 x 7168 x 4096:
-// 29.7 us in 32 wide tiles, 21.5 in 64 narrow ones; 8192 x 7168 x 4096: 182 and 239).
+// 28.3 us in 32 wide tiles, 21.2 in 64 narrow ones; 8192 x 7168 x 4096: 172 and 237).
 constexpr int kDpThreads = 128 + 256;  // TMA, 2 MMA, scale warp; 8 promotion warps
 // Registers: the launch holds 168 per thread; for wide tiles the first warpgroup
 // returns what it does not need and the promotion warps, with 128 sums each, take it.
@@ -580,6 +580,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
 #pragma unroll
         for (int j = 0; j < NT / 4; ++j) sum[j] = 0;
       }
+      // (two blocks of the loop's body at a time, so that a block's last sums run
+      // under the next one's wait: 172 us at 8192 x 7168 x 4096, 182 without, 180 with
+      // four)
+#pragma unroll 2
       for (int kb = 0; kb < KB; ++kb, ++g) {
         const uint32_t acc = g % G::ACCS;
         const bool got =
@@ -1106,11 +1110,11 @@ moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, int S, c
 //   split, 16 rows a tile: 3.5 + 0.35    32 rows: 3.7 + 0.36
 //          64 rows: 4.2 + 0.39           96 rows: 5.0 + 0.43
 //         128 rows: 5.7 + 0.52
-//   pairs, 256 columns a tile: 4.8 + 0.45    128 columns: 4.7 + 0.305
+//   pairs, 256 columns a tile: 4.8 + 0.43    128 columns: 4.7 + 0.295
 // e.g. 77 x 7168 x 4096: 12.3 (128), 11.1 (96); 192 x 4096 x 2064: 9.8, 8.6; 65 x 1024 x
-// 1024: 4.6 (64), 5.4 (96); 256 x 7168 x 4096: 25.7 (64), 20.8 (128), 29.0 (wide pairs);
-// 256 x 2048 x 7168: 13.7 (128), 12.1 (wide), 9.4 (narrow pairs); 512 x 7168 x 4096: 29.7
-// (wide), 21.5; 1999 x 4096 x 2064: 21.2, 25.6; 512 x 1024 x 1024: 5.9 (64), 7.3 (128).
+// 1024: 4.6 (64), 5.4 (96); 256 x 7168 x 4096: 25.7 (64), 20.8 (128), 28.3 (wide pairs);
+// 256 x 2048 x 7168: 13.7 (128), 11.6 (wide), 9.4 (narrow pairs); 512 x 7168 x 4096: 28.3
+// (wide), 21.2; 1999 x 4096 x 2064: 20.1, 25.2; 512 x 1024 x 1024: 5.9 (64), 7.3 (128).
 template <bool TR>
 moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStream_t s) {
   const int nt = ceil_div(a.N, 128), KB = ceil_div(a.K, 128);
@@ -1122,9 +1126,9 @@ moe_status_t launch_matmul(const MatmulFp8Args& a, const DenseParams& P, cudaStr
   const auto pairs = [&](float fixed, float per_block, int64_t tiles) {
     return fixed + per_block * KB * static_cast<float>(ceil_div<int64_t>(tiles, a.num_sms / 2));
   };
-  float best = pairs(4.8f, 0.45f, mt2 * nt2);
+  float best = pairs(4.8f, 0.43f, mt2 * nt2);
   int T = 512, S = 1;
-  if (const float t = pairs(4.7f, 0.305f, mt2 * nt); t < best) {
+  if (const float t = pairs(4.7f, 0.295f, mt2 * nt); t < best) {
     best = t;
     T = 256;
   }
