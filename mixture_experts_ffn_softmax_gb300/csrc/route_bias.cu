@@ -36,7 +36,8 @@ struct RbParams {
   int64_t M;
   int E, top_k, method, renormalize, k_group, group_count, group_select_mode;
   float scale;
-  int gs, lpg_log;  // experts of a group; log2 of the lanes that hold one (WHOLE, below)
+  int gs, gs_inv;   // experts of a group; ceil(2^20 / gs): e / gs = e gs_inv >> 20 for e < 1024
+  int lpg_log;      // WHOLE (below): log2 of the lanes that hold a group
 };
 
 // Order-preserving map of a double to an unsigned key, and back; NaN goes with
@@ -102,15 +103,21 @@ __device__ __noinline__ int2 rb_choose64(const T* row, const float* bias, const 
     for (int e = lane; e < E; e += 32) m = fmaxf(m, rb_f32(row[e]));
     m = rb_max(m);
     double s = 0.0;
-    for (int e = lane; e < E; e += 32) s += rb_score64(rb_f32(row[e]), true, m);
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+      const double x = rb_score64(rb_f32(row[e]), true, m);
+      c[e] = static_cast<uint64_t>(__double_as_longlong(x));  // (for the loop below)
+      s += x;
+    }
     inv = 1.0 / rb_sum(s);
   }
 #pragma unroll 1
   for (int e = lane; e < E; e += 32) {
     const float l = rb_f32(row[e]);
+    const double x = softmax ? __longlong_as_double(static_cast<long long>(c[e]))
+                             : rb_score64(l, false, m);
     c[e] = rb_key64(l == -INFINITY ? -INFINITY
-                                   : fma(rb_score64(l, softmax, m), inv,
-                                         static_cast<double>(bias[e])) + 0.0);
+                                   : fma(x, inv, static_cast<double>(bias[e])) + 0.0);
   }
   __syncwarp();
   if (P.group_count > 1) {
@@ -337,28 +344,30 @@ __device__ __forceinline__ void rb_load(const bf16* p, float (&l)[N]) {
 
 // The choice in fp32 where fp32 decides it.
 //
-// LPT lanes per token, EPL consecutive experts per lane.  A candidate is one
-// 32-bit key: c in order-preserving form with its low bits replaced by the
-// expert (complemented: the lower id wins), so that a maximum over the lanes
-// is a chosen expert; each lane offers its four largest in turn, and past those
-// its largest below the last one it gave.  top_k + 2 rounds leave a candidate
-// per lane.  Their exact fp32 c (the keys' low bits back) puts them in order,
-// and the choice stands if no two neighbours down to the (top_k + 1)-th are
-// closer than the error of c, nor the top_k-th and what was not a candidate;
-// equal logits with equal biases are ties for certain.  If only candidates
-// are too close (a token in a thousand of normally distributed scores), the
-// lanes rank them in 64 bits, and sigmoid groups that are too close likewise;
-// where that does not settle it, or a score is NaN, the warp takes the token by
-// rb_choose64.
+// LPT lanes per token, EPL experts per lane.  A candidate is one 32-bit key: c in
+// order-preserving form with its low bits replaced by the expert (complemented: the
+// lower id wins), so that a maximum over the lanes is a chosen expert; each lane
+// offers its four largest in turn, and past those its largest below the last one it
+// gave.  top_k + 2 rounds leave a candidate per lane.  Their exact fp32 c (the keys'
+// low bits back) puts them in order, and the choice stands if no two neighbours down to
+// the (top_k + 1)-th are closer than the error of c, nor the top_k-th and what was not a
+// candidate; equal logits with equal biases are ties for certain.  Candidates that are
+// too close (a token in a thousand of normally distributed scores) are ranked in 64 bits
+// by the lanes, after as many rounds as there are lanes if the rest is too near as well;
+// groups that are too close likewise, from their two best experts.  Where that does not
+// settle it, or a score is NaN, the warp takes the token by rb_choose64 (20 us for one
+// token of 512 experts, which is why the steps before it are there: 10804 x 336 softmax,
+// 13 of 4 of 8 groups, with two such tokens 80 us, now 27).
 //
-// WHOLE: lanes hold EPL experts or none, of one group (a power of two of lanes
-// to a group).
+// WHOLE: lanes hold EPL consecutive experts or none, of one group (a power of two of
+// lanes to a group).  Otherwise every LPT-th expert, so that loads of rows of any length
+// are whole lines.
 //
 // Bound: issue slots and, for few tokens, the chain of one token (2.9 us of a graph
 // node with 256 experts).  8192 tokens x 256 experts, 8 of 4 of 8 groups, from 281 us
-// (every token by rb_choose64) to 11.3 us; 16384 x 128 bf16, 8 chosen, 298 to 10.6 us.
+// (every token by rb_choose64) to 11.3 us; 16384 x 128 bf16, 8 chosen, 298 to 11.2 us.
 template <int EPL, int LPT, bool WHOLE, typename T>
-__global__ void __launch_bounds__(kRbWarps * 32)
+__global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72-80 registers)
     route_biased_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
                         int vec, float* __restrict__ out_w, int32_t* __restrict__ out_ids) {
   pdl_begin();
@@ -369,12 +378,13 @@ __global__ void __launch_bounds__(kRbWarps * 32)
   const int sl = lane % LPT, seg0 = lane - sl;
   const int E = P.E, G = P.group_count, k = P.top_k, gs = P.gs;
   const bool softmax = P.method == MOE_ROUTE_SOFTMAX, grouped = P.k_group < G;
-  const int e0 = sl * EPL, g0 = WHOLE ? sl >> P.lpg_log : e0 / gs;
-  auto exists = [&](int i) { return WHOLE ? e0 < E : e0 + i < E; };
+  const int e0 = sl * EPL;
+  auto expert = [&](int i) { return WHOLE ? e0 + i : sl + LPT * i; };
+  auto exists = [&](int i) { return WHOLE ? e0 < E : expert(i) < E; };
   uint64_t* sm = rb_smem + warp * (E + G);
   float b[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) b[i] = exists(i) ? __ldg(bias + e0 + i) : 0.f;
+  for (int i = 0; i < EPL; ++i) b[i] = exists(i) ? __ldg(bias + expert(i)) : 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) * TPW;
   for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * TPW; t0 < P.M;
        t0 += step) {
@@ -382,11 +392,11 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     const int64_t t = live ? t0 + seg0 / LPT : P.M - 1;
     const T* row = logits + t * E;
     float c[EPL];
-    if (vec && e0 < E) {
+    if (WHOLE && vec && e0 < E) {
       rb_load<EPL>(row + e0, c);
     } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) c[i] = exists(i) ? rb_f32(row[e0 + i]) : -INFINITY;
+      for (int i = 0; i < EPL; ++i) c[i] = exists(i) ? rb_f32(row[expert(i)]) : -INFINITY;
     }
     // ---- c = p + b (p = exp(l - mx) cf for softmax) ----
     float lo = c[0], mx = c[0], mx2 = 0.f, sum = 0.f, cf = 1.f;
@@ -413,7 +423,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     if (lo == -INFINITY) {  // masked experts of this lane, or none at all here
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (!exists(i) || rb_f32(row[e0 + i]) == -INFINITY) c[i] = -INFINITY;
+        if (!exists(i) || rb_f32(row[expert(i)]) == -INFINITY) c[i] = -INFINITY;
     }
     const float p1 = softmax ? cf : 1.0f;
     // error of a difference of two c, over p1.  Sigmoid: the exponential's
@@ -425,10 +435,35 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     bool hard = false;  // needs rb_choose64
 #pragma unroll
     for (int i = 0; i < EPL; ++i) hard |= c[i] != c[i];
+    // softmax: 1 / sum of exp(l - mx) for what is compared in 64 bits.  The sum stays
+    // in fp32, each term within 2 ulp and their additions compensated, 2^-21 in all:
+    // common to all scores, it moves a difference of two c by 2^-21 of that of their p.
+    auto inv64 = [&]() {
+      float s = 0.f, comp = 0.f;
+#pragma unroll 1
+      for (int i = sl; i < E; i += LPT) {
+        const float x = expf(rb_f32(row[i]) - mx), y = s + x;
+        comp += s >= x ? (s - y) + x : (x - y) + s;
+        s = y;
+      }
+      return 1.0 / (static_cast<double>(rb_seg_sum<LPT>(s)) + rb_seg_sum<LPT>(comp));
+    };
+    // such a difference dc is open where the sum's error could turn it
+    auto undecided = [&](double dc, double dp) {
+      return softmax && dp != 0.0 && !(fabsf(static_cast<float>(dc)) > 6e-7f * fabsf(static_cast<float>(dp)));
+    };
     // ---- groups: kept ones as a mask of the segment ----
     uint32_t kept = 0xffffffffu;
     if (grouped) {
       float gk = -INFINITY;  // lane g: group g's score
+      float* row_c = reinterpret_cast<float*>(sm) + (seg0 / LPT) * E;
+      auto store_c = [&]() {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (exists(i)) row_c[expert(i)] = c[i];
+        __syncwarp();
+      };
       const int lpg = 1 << P.lpg_log;  // WHOLE: lanes of a group
       if constexpr (WHOLE) {
         float b1 = c[0], b2 = -INFINITY;
@@ -446,23 +481,28 @@ __global__ void __launch_bounds__(kRbWarps * 32)
         const float v = P.group_select_mode == 0 ? b1 : b1 + b2;
         gk = __shfl_sync(0xffffffffu, v, seg0 + min(sl * lpg, LPT - 1));
       } else {
-        float* row_c = reinterpret_cast<float*>(sm) + (seg0 / LPT) * E;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (exists(i)) row_c[e0 + i] = c[i];
-        __syncwarp();
-        if (sl < G) {
-          float b1 = -INFINITY, b2 = -INFINITY;
+        // by parts of a group per lane, joined in lane g
+        const int parts = LPT / G, part = sl / G, g = sl - part * G;
+        float b1 = -INFINITY, b2 = -INFINITY;
+        store_c();
+        if (part < parts) {
 #pragma unroll 4
-          for (int j = 0; j < gs; ++j) {
-            const float v = row_c[sl * gs + j];
+          for (int j = part; j < gs; j += parts) {
+            const float v = row_c[g * gs + j];
             b2 = fmaxf(b2, fminf(b1, v));
             b1 = fmaxf(b1, v);
           }
-          gk = P.group_select_mode == 0 ? b1 : b1 + b2;
         }
-        __syncwarp();
+        for (int p = 1; p < parts; ++p) {
+          const int from = seg0 + min(sl + p * G, LPT - 1);
+          const float o1 = __shfl_sync(0xffffffffu, b1, from);
+          const float o2 = __shfl_sync(0xffffffffu, b2, from);
+          if (sl < G) {
+            b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+            b1 = fmaxf(b1, o1);
+          }
+        }
+        gk = P.group_select_mode == 0 ? b1 : b1 + b2;
       }
       if (sl >= G) gk = -INFINITY;
       // rank among the groups, and the groups too close to tell apart
@@ -478,57 +518,96 @@ __global__ void __launch_bounds__(kRbWarps * 32)
       kept = LPT == 32 ? all : (all >> seg0) & ((1u << (LPT & 31)) - 1u);
       // (a group's own bit is never on the other side)
       const bool unsure = sl < G && (((kept >> sl) & 1u) ? near & ~kept : near & kept) != 0u;
-      if (!WHOLE || softmax) {
-        hard |= unsure;
-      } else if (const uint32_t which = __ballot_sync(0xffffffffu, unsure && live)) {
-        // group scores in 64 bits from each lane's two best experts, where its
-        // third is no rival of them
+      if (const uint32_t which = __ballot_sync(0xffffffffu, unsure && live)) {
+        // group scores in 64 bits (lane g: group g's) from the two best experts of each
+        // lane or part, where its third is no rival of them
+        const bool seg_unsure =
+            (LPT == 32 ? which : (which >> seg0) & ((1u << (LPT & 31)) - 1u)) != 0u;
+        const double inv = softmax ? inv64() : 1.0;
         float v1 = -INFINITY, v2 = -INFINITY, v3 = -INFINITY;
         int i1 = 0, i2 = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          if (c[i] > v1) {
+        auto place = [&](float v, int i) {
+          if (v > v1) {
             v3 = v2;
             v2 = v1;
             i2 = i1;
-            v1 = c[i];
+            v1 = v;
             i1 = i;
-          } else if (c[i] > v2) {
+          } else if (v > v2) {
             v3 = v2;
-            v2 = c[i];
+            v2 = v;
             i2 = i;
           } else {
-            v3 = fmaxf(v3, c[i]);
+            v3 = fmaxf(v3, v);
+          }
+        };
+        if constexpr (WHOLE) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) place(c[i], e0 + i);
+        } else if (sl < G) {
+#pragma unroll 4
+          for (int i = sl * gs; i < sl * gs + gs; ++i) place(row_c[i], i);
+        }
+        const bool holds = WHOLE ? e0 < E : sl < G;
+        if (seg_unsure && holds)
+          hard |= !((P.group_select_mode == 0 ? v1 : v2) - v3 > kerr * p1 + 1.2e-7f * fabsf(v1));
+        // the best two: keys of c and p
+        uint64_t q1 = 0, q2 = 0;
+        double pa = 0.0, pb = 0.0;
+        if (holds) {
+          pa = rb_score64(rb_f32(row[i1]), softmax, mx) * inv;
+          pb = rb_score64(rb_f32(row[i2]), softmax, mx) * inv;
+          q1 = rb_key64(v1 == -INFINITY ? -INFINITY : pa + __ldg(bias + i1) + 0.0);
+          q2 = rb_key64(v2 == -INFINITY ? -INFINITY : pb + __ldg(bias + i2) + 0.0);
+        }
+        auto order = [](uint64_t& a, double& x, uint64_t& b, double& y) {
+          if (a < b) {
+            const uint64_t t = a;
+            a = b;
+            b = t;
+            const double z = x;
+            x = y;
+            y = z;
+          }
+        };
+        order(q1, pa, q2, pb);
+        if constexpr (WHOLE) {
+          for (int o = 1; o < 1 << P.lpg_log; o <<= 1) {
+            uint64_t o1 = __shfl_xor_sync(0xffffffffu, q1, o), o2 = __shfl_xor_sync(0xffffffffu, q2, o);
+            double oa = __shfl_xor_sync(0xffffffffu, pa, o), ob = __shfl_xor_sync(0xffffffffu, pb, o);
+            order(q1, pa, o1, oa);
+            order(q2, pb, o1, oa);
+            order(q2, pb, o2, ob);
           }
         }
-        const bool seg_unsure =
-            (LPT == 32 ? which : (which >> seg0) & ((1u << (LPT & 31)) - 1u)) != 0u;
-        if (seg_unsure && e0 < E)
-          hard |= !((P.group_select_mode == 0 ? v1 : v2) - v3 > kerr * p1 + 1.2e-7f * fabsf(v1));
-        uint64_t q1 = 0, q2 = 0;
-        if (e0 < E) {
-          const float l1 = rb_f32(row[e0 + i1]), l2 = rb_f32(row[e0 + i2]);
-          q1 = rb_key64(l1 == -INFINITY ? -INFINITY : rb_score64(l1, false, 0.f) + __ldg(bias + e0 + i1) + 0.0);
-          q2 = rb_key64(l2 == -INFINITY ? -INFINITY : rb_score64(l2, false, 0.f) + __ldg(bias + e0 + i2) + 0.0);
+        double c64 = rb_value64(q1), p64 = pa;
+        if (P.group_select_mode == 1) {
+          c64 += rb_value64(q2);
+          p64 += pb;
         }
-        uint64_t top = max(q1, q2), sec = min(q1, q2);
-        for (int o = 1; o < lpg; o <<= 1) {
-          const uint64_t o1 = __shfl_xor_sync(0xffffffffu, top, o);
-          const uint64_t o2 = __shfl_xor_sync(0xffffffffu, sec, o);
-          sec = max(min(top, o1), max(sec, o2));
-          top = max(top, o1);
+        if constexpr (WHOLE) {
+          const int from = seg0 + min(sl << P.lpg_log, LPT - 1);
+          c64 = __shfl_sync(0xffffffffu, c64, from);
+          p64 = __shfl_sync(0xffffffffu, p64, from);
         }
-        if (P.group_select_mode == 1) top = rb_key64(rb_value64(top) + rb_value64(sec));
-        uint64_t g64 = __shfl_sync(0xffffffffu, top, seg0 + min(sl * lpg, LPT - 1));
-        if (sl >= G) g64 = 0;
+        const uint64_t g64 = sl < G ? rb_key64(c64) : 0;
         rank = 0;
+        uint32_t other = 0;  // near groups that these scores do not tell from this one
 #pragma unroll 1
         for (int h = 0; h < G; ++h) {
           const uint64_t o = __shfl_sync(0xffffffffu, g64, seg0 + h);
           rank += (o > g64 || (o == g64 && h < sl)) ? 1 : 0;
+          if (softmax) {
+            const double op = __shfl_sync(0xffffffffu, p64, seg0 + h);
+            if (((near >> h) & 1u) && h != sl && undecided(rb_value64(o) - c64, op - p64))
+              other |= 1u << h;
+          }
         }
         const uint32_t all64 = __ballot_sync(0xffffffffu, sl < G && rank < P.k_group);
-        if (seg_unsure) kept = LPT == 32 ? all64 : (all64 >> seg0) & ((1u << (LPT & 31)) - 1u);
+        if (seg_unsure) {
+          kept = LPT == 32 ? all64 : (all64 >> seg0) & ((1u << (LPT & 31)) - 1u);
+          if (sl < G && (((kept >> sl) & 1u) ? other & ~kept : other & kept) != 0u) hard = true;
+        }
       }
     }
     // ---- keys, the lane's four largest ----
@@ -539,25 +618,20 @@ __global__ void __launch_bounds__(kRbWarps * 32)
 #pragma unroll
       for (int i = 0; i < EPL; ++i) key[i] = ((rb_key(c[i]) & ~MASK) | (MASK - e0)) ^ i;
       rb_top4<EPL>(key, top4);
-      if (e0 >= E || !((kept >> (grouped ? g0 : 0)) & 1u)) top4[0] = top4[1] = top4[2] = top4[3] = 0u;
+      if (e0 >= E || !((kept >> (grouped ? sl >> P.lpg_log : 0)) & 1u)) top4[0] = top4[1] = top4[2] = top4[3] = 0u;
     } else {
-      int g = g0, r = e0 - g0 * gs;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        if (r == gs) {
-          r = 0;
-          ++g;
-        }
-        ++r;
-        const bool in = exists(i) && (!grouped || ((kept >> g) & 1u));
-        key[i] = in ? ((rb_key(c[i]) & ~MASK) | (MASK - e0)) ^ i : 0u;
+        const bool in =
+            exists(i) && (!grouped || ((kept >> (expert(i) * P.gs_inv >> 20)) & 1u));
+        key[i] = in ? (rb_key(c[i]) & ~MASK) | (MASK - expert(i)) : 0u;
       }
       rb_top4<EPL>(key, top4);
     }
     // ---- top_k + 2 rounds ----
     uint32_t mine = 0, last = 0;
     int left = 4;  // of the lane's four
-    for (int r = 0; r < k + 2; ++r) {
+    auto round = [&](int r) {
       last = rb_seg_top<LPT>(top4[0], seg0);
       if (sl == r) mine = last;
       if (top4[0] == last) {
@@ -579,14 +653,21 @@ __global__ void __launch_bounds__(kRbWarps * 32)
           left = 1;
         }
       }
-    }
+    };
+    for (int r = 0; r < k + 2; ++r) round(r);
     // ---- the candidates' own c, in order ----
-    int e = mine ? static_cast<int>(MASK - (mine & MASK)) : 0x7fffffff;
-    float l = mine ? rb_f32(row[e]) : -INFINITY, be = mine ? __ldg(bias + e) : 0.f;
-    float ce = -INFINITY;
-    if (l != -INFINITY)
-      ce = softmax ? fmaf(rb_ex2(fmaf(l, kLog2e, -mx2)), cf, be)
-                   : rb_rcp(1.0f + rb_ex2(-kLog2e * l)) + be;
+    int e;
+    float l, be, ce;
+    auto candidate = [&]() {
+      e = mine ? static_cast<int>(MASK - (mine & MASK)) : 0x7fffffff;
+      l = mine ? rb_f32(row[e]) : -INFINITY;
+      be = mine ? __ldg(bias + e) : 0.f;
+      ce = -INFINITY;
+      if (l != -INFINITY)
+        ce = softmax ? fmaf(rb_ex2(fmaf(l, kLog2e, -mx2)), cf, be)
+                     : rb_rcp(1.0f + rb_ex2(-kLog2e * l)) + be;
+    };
+    candidate();
     float cn = __shfl_down_sync(0xffffffffu, ce, 1, LPT);
     // (keys with the same high bits may come out in the wrong order)
     if (__any_sync(0xffffffffu, sl < k + 1 && cn > ce)) {
@@ -608,52 +689,47 @@ __global__ void __launch_bounds__(kRbWarps * 32)
         }
       }
       cn = __shfl_down_sync(0xffffffffu, ce, 1, LPT);
-      // (what three passes leave out of order could hide near ties of others)
-      if (sl < k + 1 && cn > ce) hard = true;
     }
     const float ln = __shfl_down_sync(0xffffffffu, l, 1, LPT);
     const float bn = __shfl_down_sync(0xffffffffu, be, 1, LPT);
     const int en = __shfl_down_sync(0xffffffffu, e, 1, LPT);
     const float err = kerr * p1 + 1.2e-7f * fabsf(ce);
     const bool tie = l == ln && be == bn && e < en;
-    const bool close = sl < k && !(ce - cn > err) && !tie;
-    // what is no candidate has to be below the top_k-th for certain
-    if (sl == k - 1 && last != 0u && !(ce - rb_value(last | MASK) > err)) hard = true;
+    // (what three passes left out of order could hide near ties of others)
+    const bool close = (sl < k && !(ce - cn > err) && !tie) || (sl == k && cn > ce);
+    // what is no candidate has to be below the top_k first for certain
+    auto reached = [&]() { return last != 0u && !(ce - rb_value(last | MASK) > err); };
     int rank = sl;  // of the lane's candidate
     bool open = false;
-    const uint32_t closes = __ballot_sync(0xffffffffu, close && live);
-    if (closes != 0u) {
-      // in 64 bits among the candidates.  Softmax: the sum stays in fp32, each
-      // term within 2 ulp and their additions compensated, 2^-21 in all; what
-      // that leaves open takes the 64-bit sum of rb_choose64.
-      double inv = 1.0;
-      if (softmax) {
-        float s = 0.f, comp = 0.f;
-#pragma unroll 1
-        for (int i = sl; i < E; i += LPT) {
-          const float x = expf(rb_f32(row[i]) - mx), y = s + x;
-          comp += s >= x ? (s - y) + x : (x - y) + s;
-          s = y;
-        }
-        inv = 1.0 / (static_cast<double>(rb_seg_sum<LPT>(s)) + rb_seg_sum<LPT>(comp));
-      }
+    int n = k + 2;
+    const uint32_t mores = __ballot_sync(0xffffffffu, sl < k && reached() && live);
+    if (mores != 0u) {  // as many candidates as lanes
+      for (; n < LPT; ++n) round(n);
+      if (sl < k && reached()) hard = true;
+      candidate();
+    }
+    if ((__ballot_sync(0xffffffffu, close && live) | mores) != 0u) {
+      // in 64 bits among the candidates
+      const double inv = softmax ? inv64() : 1.0;
       const double p64 = rb_score64(l, softmax, mx) * inv;
       const double c64 = l == -INFINITY ? -INFINITY : p64 + be + 0.0;
       const uint64_t mykey = mine ? rb_key64(c64) : 0;
+      uint64_t next = 0;  // the largest key below this lane's, and its p
+      double pnext = 0.0;
       rank = 0;
 #pragma unroll 1
-      for (int j = 0; j < k + 2; ++j) {
+      for (int j = 0; j < n; ++j) {
         const uint64_t o = __shfl_sync(0xffffffffu, mykey, seg0 + j);
         const int oe = __shfl_sync(0xffffffffu, e, seg0 + j);
+        const double op = __shfl_sync(0xffffffffu, p64, seg0 + j);
         rank += (o > mykey || (o == mykey && oe < e)) ? 1 : 0;
+        if (o < mykey && o > next) {
+          next = o;
+          pnext = op;
+        }
       }
       if (mine == 0u) rank = LPT;
-      if (softmax) {
-        // the nearest of the candidates' neighbours (they are neighbours in fp32)
-        const float dp = static_cast<float>(p64) - __shfl_down_sync(0xffffffffu, static_cast<float>(p64), 1, LPT);
-        const float dc = static_cast<float>(c64 - __shfl_down_sync(0xffffffffu, c64, 1, LPT));
-        if (close && !(fabsf(dc) > 6e-7f * fabsf(dp))) open = true;
-      }
+      if (softmax && rank < k && next != 0) open = undecided(c64 - rb_value64(next), p64 - pnext);
     }
     const uint32_t hards = __ballot_sync(0xffffffffu, (hard || open) && live);
     // ---- weights (as rb_weights) ----
@@ -693,7 +769,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
 //   softmax as it is: v_j = p_j,  dl_e = scale (sum_j [id_j = e] gw_j p_e - p_e sum_i gw_i p_i)
 //
 // Registers hold a token's row: LPT lanes per token (two tokens per warp up to
-// 256 experts and 16 items, else one), EPL consecutive experts per lane.  The
+// 256 experts and 16 items, else one), EPL experts per lane.  The
 // row goes out in 16-byte stores with what every entry has (0, or -p_e times
 // the dot product), then the lanes of the items store their experts' entries
 // over it.
@@ -738,7 +814,11 @@ __global__ void __launch_bounds__(kRbWarps * 32)
   const int64_t token = warp0 * (32 / LPT) + lane / LPT;
   const bool live = token < P.M;
   const int64_t t = live ? token : P.M - 1;
-  const int E = P.E, k = P.top_k, e0 = sl * EPL;
+  const int E = P.E, k = P.top_k;
+  // EPL consecutive experts, or every LPT-th where rows are no multiples of them (by
+  // the sizes alone: a tensor's alignment must not change the order of its sums)
+  const bool apart = E % EPL != 0;
+  const int e0 = apart ? sl : sl * EPL, es = apart ? LPT : 1;
   const T* row = logits + t * E;
   // the lane's item
   int id = sl < k ? ids[t * k + sl] : -1;
@@ -756,7 +836,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
       rb_load<EPL>(row + e0, v);
     } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = e0 + i < E ? rb_f32(row[e0 + i]) : -INFINITY;
+      for (int i = 0; i < EPL; ++i) v[i] = e0 + i * es < E ? rb_f32(row[e0 + i * es]) : -INFINITY;
     }
     float mx = v[0], s = 0.f;
 #pragma unroll
@@ -807,7 +887,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     } else {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (e0 + i < E) rb_store(dst + e0 + i, v[i]);
+        if (e0 + i * es < E) rb_store(dst + e0 + i * es, v[i]);
     }
   }
   __syncwarp();
@@ -918,7 +998,8 @@ void launch_fast(const RouteArgs& a, const float* bias, RbParams P, cudaStream_t
 template <typename T>
 void launch_biased(const RouteArgs& a, const float* bias, cudaStream_t s) {
   const RbParams P{a.M, a.E, a.top_k, a.method, a.renormalize, a.k_group, a.group_count,
-                   a.group_select_mode, a.scale, a.E / a.group_count, 0};
+                   a.group_select_mode, a.scale,
+                   a.E / a.group_count, ceil_div(1 << 20, a.E / a.group_count), 0};
   const bool grouped = a.k_group < a.group_count;
   // A candidate per lane (two beyond top_k), a group per lane.  Half a warp per token
   // halves the instructions, a whole one shortens a token's chain and, from 65 experts

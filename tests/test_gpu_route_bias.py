@@ -192,6 +192,27 @@ def test_route_biased_many_and_few_tokens(E, k, G, kg, mode, method, renorm):
             assert torch.equal(pkg.moe_route(logits[part], *pos, score_bias=bias)[1], ids[part])
 
 
+@pytest.mark.parametrize("E,k,G,kg,mode", [(336, 13, 8, 4, 0), (336, 13, 8, 4, 1), (463, 10, 1, 1, 0), (384, 8, 8, 4, 1),
+                                           (510, 30, 17, 9, 1), (162, 14, 6, 2, 1), (162, 5, 27, 9, 0), (1000, 8, 4, 2, 1)])
+@pytest.mark.parametrize("method,renorm", [("sigmoid", True), ("softmax", False)])
+def test_route_biased_near_groups_and_candidates(E, k, G, kg, mode, method, renorm):
+    """Group sizes that are no powers of two and rows of odd lengths, with scores
+    a few roundings apart in the whole row, in one group, and between groups."""
+    rng = np.random.default_rng(E * 3 + k)
+    M = 120
+    logits = rng.normal(size=(M, E))
+    step = 2.0 ** np.linspace(-27, -14, 40)[:, None]
+    logits[:40] = step * rng.permutation(E)[None] * (1 + rng.random((40, E)) / 8)
+    best = 2.5 + step * rng.random((40, G))                 # every group's best within a step
+    for g in range(G):
+        logits[40:80, g * (E // G) + 1] = best[:, g]
+    for dt in (torch.float32, torch.bfloat16):
+        l = torch.tensor(logits, device="cuda").to(dt)
+        for spread in (0.0, 0.2):
+            bias = torch.tensor(rng.normal(size=E) * spread, dtype=torch.float32, device="cuda")
+            check_biased(l, bias, args(k, method, renorm, kg, G, mode))
+
+
 @pytest.mark.parametrize("method", ["sigmoid", "softmax"])
 def test_route_biased_non_finite_scores(method):
     """Whatever the logits hold, ids are valid and distinct; other tokens keep
