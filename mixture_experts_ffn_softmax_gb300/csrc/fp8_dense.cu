@@ -454,9 +454,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
         }
       }
     } else if (warp <= 2) {
-      // one issuing thread per accumulator: while one is held up by the MMAs
-      // queued ahead of its own, the other's waits and commits go on
-      // (8192 x 7168 x 4096: 194 us with one thread for both, 180 with two)
+      // two issuing threads, of every second block: while one is held up by the
+      // MMAs queued ahead of its own, the other's waits and commits go on
+      // (8192 x 7168 x 4096, before later steps: 194 us with one thread, 180 with two)
       if (lane == 0 && rank == 0) {
         uint32_t acc = warp - 1;
         constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, NT, false, !TR);
@@ -478,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
             ptx::mma_e4m3_pair(tmem + acc * NT, ad, bd, idesc, ks != 0);
           }
           // (the accumulator's barrier first: the other order took a K-rows
-          // weight from 182 to 206 us at 8192 x 7168 x 4096)
+          // weight from 182 to 206 us at 8192 x 7168 x 4096, before later steps)
           ptx::mma_commit_pair(&ctl.tmem_full[acc], 0x3);
           ptx::mma_commit_pair(&ctl.empty[stage], 0x3);
           stage += 2;
@@ -581,8 +581,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
         for (int j = 0; j < NT / 4; ++j) sum[j] = 0;
       }
       // (two blocks of the loop's body at a time, so that a block's last sums run
-      // under the next one's wait: 172 us at 8192 x 7168 x 4096, 182 without, 180 with
-      // four)
+      // under the next one's wait: 172-175 us at 8192 x 7168 x 4096, 182 without, 180
+      // with four)
 #pragma unroll 2
       for (int kb = 0; kb < KB; ++kb, ++g) {
         const uint32_t acc = g % G::ACCS;

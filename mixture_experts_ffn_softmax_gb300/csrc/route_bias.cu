@@ -697,8 +697,11 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     const bool tie = l == ln && be == bn && e < en;
     // (what three passes left out of order could hide near ties of others)
     const bool close = (sl < k && !(ce - cn > err) && !tie) || (sl == k && cn > ce);
-    // what is no candidate has to be below the top_k first for certain
-    auto reached = [&]() { return last != 0u && !(ce - rb_value(last | MASK) > err); };
+    // what is no candidate has to be below the top_k first for certain (below a c of
+    // -inf it is: of equal c the keys themselves put the lower id first)
+    auto reached = [&]() {
+      return last != 0u && ce != -INFINITY && !(ce - rb_value(last | MASK) > err);
+    };
     int rank = sl;  // of the lane's candidate
     bool open = false;
     int n = k + 2;

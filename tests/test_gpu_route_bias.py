@@ -213,6 +213,23 @@ def test_route_biased_near_groups_and_candidates(E, k, G, kg, mode, method, reno
             check_biased(l, bias, args(k, method, renorm, kg, G, mode))
 
 
+@pytest.mark.parametrize("E,k,G,kg,mode", [(256, 8, 8, 4, 1), (256, 8, 1, 1, 0), (100, 6, 1, 1, 0), (336, 9, 8, 2, 0)])
+@pytest.mark.parametrize("M", [50, 4200])
+def test_route_biased_fewer_experts_left_than_chosen(E, k, G, kg, mode, M):
+    """Rows with 0 to k + 2 unmasked experts, and biases of -inf and of the
+    type's largest numbers beside the masks."""
+    rng = np.random.default_rng(M + E)
+    logits = rng.normal(size=(M, E)).astype(np.float32)
+    for t in range(M):
+        logits[t, rng.permutation(E)[t % (k + 3):]] = -np.inf
+    bias = rng.normal(size=E).astype(np.float32)
+    for special in ((), (-np.inf,), (3e38, -3e38)):
+        for i, v in enumerate(special):
+            bias[i::7] = v
+        check_biased(torch.tensor(logits, device="cuda"), torch.tensor(bias, device="cuda"),
+                     args(k, "sigmoid", True, kg, G, mode))
+
+
 @pytest.mark.parametrize("method", ["sigmoid", "softmax"])
 def test_route_biased_non_finite_scores(method):
     """Whatever the logits hold, ids are valid and distinct; other tokens keep
