@@ -648,9 +648,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDpThreads, 1)
   }
   __syncwarp();
   ptx::cluster_sync();
-  // the last stages' commits, which nothing else waits for, have to arrive
-  // before the barriers' memory goes
-  if (threadIdx.x < 2 && blocks > static_cast<int>(threadIdx.x)) {
+  // the commits of the last use of every stage, which nothing else waits for, have
+  // to arrive before the barriers' memory goes: each of them (commits of one thread
+  // complete in order, but nothing says that their arrivals do)
+  if (threadIdx.x < G::STAGES && blocks > static_cast<int>(threadIdx.x)) {
     const int64_t g = blocks - 1 - threadIdx.x;
     dense_wait(&ctl.empty[g % G::STAGES], static_cast<uint32_t>(g / G::STAGES) & 1u, &ctl.abort,
                P.error_word);

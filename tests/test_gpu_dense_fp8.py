@@ -324,6 +324,22 @@ def test_matmul_pairs_with_narrow_tiles(M, K, N, transposed):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("N", [256, 512, 1040])
+@pytest.mark.parametrize("blocks", range(1, 9))
+def test_matmul_pairs_of_few_blocks_back_to_back(blocks, N):
+    """Fewer K blocks than stages, as many, and more, so that a pair ends with
+    none, some or all of its stages in use; the next call's barriers are in the
+    same shared memory at once.  (Above 8192 rows every product is of CTA pairs.)"""
+    M, K = 8200, 128 * blocks - 112 * (blocks % 2)
+    a, sa, w, sw, bias, y = exact_case(M, K, N, blocks % 2 == 0, blocks)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.full((M, N), 7.0, device="cuda") for _ in range(6)]
+    for out in outs:
+        pkg.moe_matmul_fp8(a, sa, w, sw, bias, blocks % 2 == 0, out=out, error_word=err)
+    ref = (y + bias.double()).float()
+    assert all(torch.equal(out, ref) for out in outs) and err.item() == 0
+
+
 # ----------------------------------------------------------- together --
 def shared_oracle(x, w13, w2, s13, s2, b13=None, b2=None):
     q, s = quantised(x)
