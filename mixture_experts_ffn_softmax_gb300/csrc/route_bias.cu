@@ -399,17 +399,19 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
       for (int i = 0; i < EPL; ++i) c[i] = exists(i) ? rb_f32(row[expert(i)]) : -INFINITY;
     }
     // ---- c = p + b (p = exp(l - mx) cf for softmax) ----
-    float lo = c[0], mx = c[0], mx2 = 0.f, sum = 0.f, cf = 1.f;
+    float lo = c[0], mx = c[0], sum = 0.f, cf = 1.f;
 #pragma unroll
     for (int i = 1; i < EPL; ++i) lo = fminf(lo, c[i]);
     if (softmax) {
 #pragma unroll
       for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, c[i]);
       mx = rb_seg_max<LPT>(mx);
-      mx2 = mx * kLog2e;  // (its rounding scales every exp alike)
+      // (the difference first, as in the weights' numerator: l log2 e - mx log2 e with a
+      // rounded second term scales every exp by 2^(its error), which the numerator does
+      // not see, and for large logits lowers cf below the largest p)
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        c[i] = rb_ex2(fmaf(c[i], kLog2e, -mx2));
+        c[i] = rb_ex2((c[i] - mx) * kLog2e);
         sum += c[i];
       }
       sum = rb_seg_sum<LPT>(sum);
@@ -428,9 +430,11 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     const float p1 = softmax ? cf : 1.0f;
     // error of a difference of two c, over p1.  Sigmoid: the exponential's
     // 2^-22 + |l| 2^-23.5 times p (1 - p) (at most 2^-23.5), the sum's 2^-24, the
-    // reciprocal's 2^-23, twice.  Softmax, in 2^-24: each exp 4 + 1, the sum's
-    // EPL + 5 additions and terms, its reciprocal and product 3, twice.  The
-    // rounding of the bias' addition is in the comparisons.
+    // reciprocal's 2^-23, twice.  Softmax, in 2^-24, with d = mx - l: an exponential's 4
+    // and its argument's 2.25 d (d e^-d is below 0.4), twice; once, as it is common to
+    // the row, the sum's: its terms' 4 and 2.25 times their mean d (below 4.5 for 1024
+    // experts), EPL + 5 additions, the reciprocal: EPL + 30 of the 2 EPL + 36 here.
+    // The rounding of the bias' addition is in the comparisons.
     const float kerr = softmax ? 2.0f * (18 + EPL) * 5.9604645e-8f : 6e-7f;
     bool hard = false;  // needs rb_choose64
 #pragma unroll
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
       be = mine ? __ldg(bias + e) : 0.f;
       ce = -INFINITY;
       if (l != -INFINITY)
-        ce = softmax ? fmaf(rb_ex2(fmaf(l, kLog2e, -mx2)), cf, be)
+        ce = softmax ? fmaf(rb_ex2((l - mx) * kLog2e), cf, be)
                      : rb_rcp(1.0f + rb_ex2(-kLog2e * l)) + be;
     };
     candidate();

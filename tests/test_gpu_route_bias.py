@@ -290,6 +290,74 @@ def test_route_biased_zero_bias_is_the_plain_route():
     assert (w - w0).abs().max() <= 1e-5
 
 
+def shift_free_rtol(l, ids):
+    """Relative error of softmax weights, from each logit's distance to the
+    row's largest alone.  Numerator: the distance rounded (|l - max| U32) and
+    expf (2).  Sum: 4 for a term's exponential and 2.25 |l - max| for its
+    argument (difference and product rounded, the constant's own error), as
+    the terms weigh, and the additions of positive terms, one each: at most
+    E / 16 in a lane and 5 across them.  Division and scale 2."""
+    d = l.max(1, keepdims=True) - l
+    p = np.exp(-d)
+    p /= p.sum(1, keepdims=True)
+    d_mean = (p * d).sum(1, keepdims=True)
+    return (np.take_along_axis(d, ids, 1) + 2 + 4 + 2.25 * d_mean + -(-l.shape[1] // 16) + 5 + 2) * U32
+
+
+@pytest.mark.parametrize("E,k,G,kg,M", [(8, 2, 1, 1, 40), (128, 8, 1, 1, 4200), (256, 8, 8, 4, 40),
+                                        (256, 14, 1, 1, 4200), (336, 9, 8, 4, 40), (1000, 8, 1, 1, 20),
+                                        (256, 40, 1, 1, 20)])
+@pytest.mark.parametrize("dtype,step,shifts", [("float32", 2.0 ** -4, (100.0, -1000.0, 1e4, 2.0 ** 19)),
+                                               ("bfloat16", 0.5, (120.0, -120.0))])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_biased_softmax_does_not_see_a_shift(E, k, G, kg, M, dtype, step, shifts, renorm):
+    """All logits of a call moved by a number that fp32 adds exactly: the same
+    ids and weights, and those within what the distances between logits give."""
+    rng = np.random.default_rng(E + M)
+    base = np.clip(np.round(rng.normal(size=(M, E)) * 2 / step) * step, -6, 6)
+    bias = torch.tensor(rng.normal(size=E) / E, dtype=torch.float32, device="cuda")
+    a = (k, "softmax", renorm, kg, G, 0, 2.5)
+    dt = getattr(torch, dtype)
+    w0, i0 = pkg.moe_route(torch.tensor(base, device="cuda").to(dt), *a, score_bias=bias)
+    rw, rids = oracle.route_biased(base, bias.double().cpu().numpy(), *a)
+    assert np.array_equal(i0.cpu().numpy(), rids)
+    rtol = shift_free_rtol(base, rids)
+    for shift in (0.0,) + shifts:
+        l = torch.tensor(base + shift, device="cuda").to(dt)
+        assert np.array_equal(l.double().cpu().numpy(), base + shift)
+        w, ids = pkg.moe_route(l, *a, score_bias=bias)
+        assert torch.equal(ids, i0)
+        err = np.abs(w.double().cpu().numpy() - rw)
+        assert (err <= rtol * rw).all(), (shift, (err / rw).max())
+        assert torch.equal(w, w0)
+
+
+def test_route_biased_softmax_choice_with_large_logits():
+    """Logits around 1e8 and 1e9, some equal and the others far below, and
+    biases that bring the equal ones' c to the others' within 2^-25 of a
+    score: what fp32 says of the order is less than its error."""
+    E, n, k = 64, 27, 40
+    for part in range(60):
+        rng = np.random.default_rng(part)
+        base = np.concatenate([rng.integers(1 << 23, 1 << 24, 8) * 8.0,
+                               rng.integers(1 << 23, 1 << 24, 8) * 64.0])
+        l = np.repeat(base[:, None], E, 1)
+        l[:, n:] -= 8192.0
+        top = np.float32(-1.0 / n)
+        bias = np.full(E, top, dtype=np.float32)
+        for e in range(n):
+            bias[e] = np.float32(top + rng.integers(0, 3) * 2.0 ** -28)
+        c = 1.0 / n + bias[:n].astype(np.float64)
+        bias[n:] = c[rng.integers(0, n, E - n)] + rng.uniform(-2e-9, 2e-9, E - n)
+        logits = torch.tensor(l, dtype=torch.float32, device="cuda")
+        assert np.array_equal(logits.double().cpu().numpy(), l)
+        for kk in (8, 28, k):
+            _, ids = pkg.moe_route(logits, kk, "softmax", True,
+                                   score_bias=torch.tensor(bias, device="cuda"))
+            _, rids = oracle.route_biased(l, bias.astype(np.float64), kk, "softmax", True)
+            assert np.array_equal(ids.cpu().numpy(), rids), (part, kk)
+
+
 # ------------------------------------------------------------- gradient --
 BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
         (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
