@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     // ---- groups: kept ones as a mask of the segment ----
     uint32_t kept = 0xffffffffu;
     if (grouped) {
-      float gk = -INFINITY;  // lane g: group g's score
+      // lane g: group g's score, and the size of what it is the sum of
+      float gk = -INFINITY, mag = 0.f;
       float* row_c = reinterpret_cast<float*>(sm) + (seg0 / LPT) * E;
       auto store_c = [&]() {
         __syncwarp();
@@ -482,8 +483,10 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
           b1 = fmaxf(b1, o1);
         }
-        const float v = P.group_select_mode == 0 ? b1 : b1 + b2;
-        gk = __shfl_sync(0xffffffffu, v, seg0 + min(sl * lpg, LPT - 1));
+        const bool sum2 = P.group_select_mode != 0;
+        const int from = seg0 + min(sl * lpg, LPT - 1);
+        gk = __shfl_sync(0xffffffffu, sum2 ? b1 + b2 : b1, from);
+        mag = __shfl_sync(0xffffffffu, sum2 ? fabsf(b1) + fabsf(b2) : fabsf(b1), from);
       } else {
         // by parts of a group per lane, joined in lane g
         const int parts = LPT / G, part = sl / G, g = sl - part * G;
@@ -507,10 +510,13 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           }
         }
         gk = P.group_select_mode == 0 ? b1 : b1 + b2;
+        mag = P.group_select_mode == 0 ? fabsf(b1) : fabsf(b1) + fabsf(b2);
       }
       if (sl >= G) gk = -INFINITY;
-      // rank among the groups, and the groups too close to tell apart
-      const float gerr = 3.0f * (kerr * p1 + 1.2e-7f * fabsf(gk));
+      // rank among the groups, and the groups too close to tell apart: each of the two c
+      // and their sum are rounded, 2^-24 of each, so that c of both signs leave an error
+      // that their sum's size says nothing of (the lane of the larger ones sees it)
+      const float gerr = 3.0f * (kerr * p1 + 1.2e-7f * mag);
       int rank = 0;
       uint32_t near = 0;
       for (int h = 0; h < G; ++h) {

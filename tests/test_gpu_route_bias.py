@@ -358,6 +358,42 @@ def test_route_biased_softmax_choice_with_large_logits():
             assert np.array_equal(ids.cpu().numpy(), rids), (part, kk)
 
 
+def biased_ids(logits, bias, k, method, kg, G, mode):
+    """The choice in 64 bits, by torch for many tokens (distinct c)."""
+    l = logits.double()
+    p = torch.softmax(l, 1) if method == "softmax" else torch.sigmoid(l)
+    c = p + bias.double()
+    M, E = c.shape
+    top = c.view(M, G, E // G).sort(dim=2, descending=True).values
+    score = top[:, :, 0] + top[:, :, 1] if mode else top[:, :, 0]
+    kept = score.sort(dim=1, descending=True, stable=True).indices[:, :kg]
+    keep = torch.zeros(M, G, dtype=torch.bool, device=c.device).scatter_(1, kept, True)
+    c = c.masked_fill(~keep.repeat_interleave(E // G, 1), -np.inf)
+    return c.sort(dim=1, descending=True, stable=True).indices[:, :k].int()
+
+
+@pytest.mark.parametrize("B", [4.0, 16.0, 64.0, 1000.0])
+@pytest.mark.parametrize("E,G,kg,k,M", [(16, 8, 4, 4, 400000), (256, 32, 16, 8, 100000),
+                                        (256, 8, 4, 8, 100000), (336, 8, 4, 8, 60000),
+                                        (512, 16, 8, 8, 50000), (1024, 32, 16, 8, 30000),
+                                        (256, 128, 64, 8, 2000)])
+@pytest.mark.parametrize("method", ["softmax", "sigmoid"])
+def test_route_biased_groups_with_biases_of_both_signs(E, G, kg, k, M, B, method):
+    """Group scores that are small sums of large c of both signs: their
+    rounding is the summands'."""
+    g = torch.Generator(device="cuda").manual_seed(int(B) + E + G)
+    logits = torch.randn(M, E, generator=g, device="cuda")
+    bias = torch.full((G, E // G), -B, device="cuda")
+    bias[:, 0] = B
+    bias = (bias + torch.randn(G, E // G, generator=g, device="cuda") * 1e-3).view(E)
+    for part in logits.split(50000):
+        ids = pkg.moe_route(part, k, method, True, kg, G, 1, score_bias=bias)[1]
+        assert torch.equal(ids, biased_ids(part, bias, k, method, kg, G, 1))
+    few = logits[:300]                              # (a whole warp per token)
+    assert torch.equal(pkg.moe_route(few, k, method, True, kg, G, 1, score_bias=bias)[1],
+                       biased_ids(few, bias, k, method, kg, G, 1))
+
+
 # ------------------------------------------------------------- gradient --
 BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
         (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
