@@ -559,8 +559,8 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           for (int i = sl * gs; i < sl * gs + gs; ++i) place(row_c[i], i);
         }
         const bool holds = WHOLE ? e0 < E : sl < G;
-        if (seg_unsure && holds)
-          hard |= !((P.group_select_mode == 0 ? v1 : v2) - v3 > kerr * p1 + 1.2e-7f * fabsf(v1));
+        const float least = P.group_select_mode == 0 ? v1 : v2;  // v3's rival
+        if (seg_unsure && holds) hard |= !(least - v3 > kerr * p1 + 1.2e-7f * fabsf(least));
         // the best two: keys of c and p
         uint64_t q1 = 0, q2 = 0;
         double pa = 0.0, pb = 0.0;

@@ -394,6 +394,54 @@ def test_route_biased_groups_with_biases_of_both_signs(E, G, kg, k, M, B, method
                        biased_ids(few, bias, k, method, kg, G, 1))
 
 
+@pytest.mark.parametrize("E,G,kg,k", [(64, 4, 2, 4), (256, 8, 4, 8), (336, 8, 4, 8), (512, 16, 8, 8),
+                                      (160, 5, 2, 6), (1024, 16, 4, 8)])
+@pytest.mark.parametrize("method", ["softmax", "sigmoid"])
+def test_route_biased_groups_whose_second_experts_are_large_and_near(E, G, kg, k, method):
+    """Groups alike but for a few roundings, each with one expert of a small c
+    and the others near -80 or -1000, where fp32 cannot order those others:
+    their biases differ by steps of fp32, their scores by as much."""
+    M, gs = 20000, E // G
+    g = torch.Generator(device="cuda").manual_seed(E)
+    for B, step in ((80.0, 2.0 ** -17), (1000.0, 2.0 ** -14)):
+        bias = -B + step * torch.randint(0, 5, (G, gs), generator=g, device="cuda").float()
+        # (not 0: two groups with the same pair of scores would be a tie of real
+        # numbers that 64 bits break by their rounding)
+        bias[:, 3] = 1e-6 * torch.randn(G, generator=g, device="cuda")
+        bias = bias.view(E)
+        for steps in (1, 4, 16):
+            spread = steps * step * (E / 2 if method == "softmax" else 4)
+            row = torch.randn(M, 1, generator=g, device="cuda")
+            logits = row + spread * torch.randn(M, E, generator=g, device="cuda")
+            for part in (logits, logits[:500]):
+                ids = pkg.moe_route(part, k, method, True, kg, G, 1, score_bias=bias)[1]
+                ref = biased_ids(part, bias, k, method, kg, G, 1)
+                assert torch.equal(ids, ref), (B, steps)
+
+
+@pytest.mark.parametrize("E,G,kg", [(64, 4, 1), (60, 4, 1), (256, 8, 1), (336, 8, 1), (512, 16, 1)])
+def test_route_biased_second_experts_on_both_sides_of_a_rounding(E, G, kg):
+    """Two groups, each with one expert of a small c and two near -80 that are
+    apart by less than the error of their scores but rounded apart by a whole
+    step of fp32 at -80: the step says nothing of their order."""
+    M, gs, k, step = 40000, E // G, 2, 2.0 ** -17
+    rng = np.random.default_rng(E)
+    bias = np.full((G, gs), -1000.0)
+    logits = rng.normal(size=(M, G, gs)) * 0.1
+    for grp in range(2):
+        bias[grp, 0] = 0.0
+        logits[:, grp, 0] = 0.25
+        for e, p in ((1, 0.5 + step / 2), (2, 0.875 + step / 2)):
+            bias[grp, e] = -80.0 - (p - 0.5 - step / 2)            # (c near -79.5 + step / 2)
+            exact = p + rng.uniform(-1e-7, 1e-7, M)
+            logits[:, grp, e] = np.log(exact / (1 - exact))
+    logits = torch.tensor(logits.reshape(M, E), dtype=torch.float32, device="cuda")
+    bias = torch.tensor(bias.reshape(E), dtype=torch.float32, device="cuda")
+    for part in (logits, logits[:4000]):
+        ids = pkg.moe_route(part, k, "sigmoid", True, kg, G, 1, score_bias=bias)[1]
+        assert torch.equal(ids, biased_ids(part, bias, k, "sigmoid", kg, G, 1))
+
+
 # ------------------------------------------------------------- gradient --
 BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
         (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
