@@ -448,7 +448,7 @@ GBMOE_API moe_status_t moe_quant_rows_fp8(const void* x, int64_t M, int32_t H, v
  * swiglu = 1 z = SiLU(x[:, :K]) * x[:, K:] in fp32 (gate columns first, as
  * in w13), for each row and each group of 128 columns (the last may be
  * shorter):
- *   scale = fp32(max|z| / 448), 1 where all are zero;
+ *   scale = fp32(max|z| / 448), 1 where that is 0 (and the codes then 0);
  *   q8 = e4m3(fp32(z / scale)), round to nearest even, saturating.
  * A NaN makes its group's scale and codes NaN; an infinity its scale
  * infinite, its own code NaN and the others 0.

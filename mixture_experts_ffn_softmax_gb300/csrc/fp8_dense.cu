@@ -206,7 +206,9 @@ __global__ void __launch_bounds__(kQgWarps * 32, kQgBlocks)
         s = div_fixed(m, 448.0f, 1.0f / 448.0f);
         r = __frcp_rn(s);
       } else {
-        s = m == 0.f ? 1.0f : __fdiv_rn(m, 448.0f);
+        // (0 also where z, held in fp32, is below 448 times half of fp32's smallest number)
+        s = __fdiv_rn(m, 448.0f);
+        if (s == 0.f) s = 1.0f;
       }
       if (col0 + 256 * i < K) {
         *reinterpret_cast<uint2*>(dst + 256 * i) = e4m3_codes8(z, s, r, fast);

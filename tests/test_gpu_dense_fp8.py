@@ -117,6 +117,42 @@ def test_quant_groups_views_and_rows_behind():
     assert pkg.moe_quant_groups_fp8(x[:0])[0].shape == (0, 272)
 
 
+@pytest.mark.parametrize("top", [1.4e-45, 2.8e-45, 1e-43, 3.1e-43, 3.2e-43, 6e-43, 1e-42, 1e-40])
+def test_quant_groups_swiglu_tiny_groups(top):
+    """Groups whose largest value over 448 is below the smallest fp32 number,
+    or a few of them, with zeros beside: the scale is 1 where it would be 0,
+    and nothing is NaN."""
+    K = 272
+    up = 2.0 ** -133                                       # bf16's smallest number, 9.2e-41
+    gate = 2.0 * top / up                                  # SiLU(g) is about g / 2
+    x = torch.zeros(3, 2 * K, device="cuda", dtype=torch.bfloat16)
+    x[0, [0, 5, 130, 271]] = gate
+    x[0, K:] = up
+    x[1, :K] = gate
+    x[1, K:] = up
+    x[1, K + 7::9] = 0.0
+    x[2, 3], x[2, K + 3] = -gate, -up
+    q, s = pkg.moe_quant_groups_fp8(x, swiglu=True)
+    q = q.float()
+    assert torch.isfinite(q).all() and torch.isfinite(s).all() and (s > 0).all()
+    z = oracle.swiglu_rows(f64(x))
+    pad = np.zeros((3, 384))
+    pad[:, :K] = z
+    amax = np.abs(pad).reshape(3, 3, 128).max(2)
+    tiny = 2.0 ** -149
+    got = s.double().cpu().numpy()
+    sure = amax / 448.0 < 0.45 * tiny                      # 0 whatever z's own rounding
+    assert (got[sure] == 1).all() and (q.cpu().numpy().reshape(3, -1)[:, :128][sure[:, 0]] == 0).all()
+    # elsewhere within one of the smallest numbers of amax / 448 (z is rounded to them too)
+    big = amax / 448.0 > 0.6 * tiny
+    assert (np.abs(got[big] - amax[big] / 448.0) <= tiny).all()
+    assert ((pad[:, :K] != 0) | (q.cpu().numpy() == 0)).all()
+    # and the product of such codes stays finite
+    w = torch.ones(K, 16, device="cuda").to(E4M3)
+    y = pkg.moe_matmul_fp8(q.to(E4M3), s, w, torch.ones(3, 1, device="cuda"))
+    assert torch.isfinite(y).all()
+
+
 # ----------------------------------------------------------------- product --
 SHAPES = [
     # (M, K, N)
