@@ -153,7 +153,8 @@ GBMOE_API moe_status_t moe_route_biased(const void* router_logits, int32_t logit
  * Sigmoid, and softmax with renormalize: only the chosen experts' entries
  * are nonzero; softmax without: every entry.  Every entry is written.  An
  * expert named twice in a token counts twice.  Masked logits (-inf) have a
- * gradient of 0.
+ * gradient of 0, and grad_weights of masked experts take no part, whatever
+ * they hold.
  * The pages have no counterpart to this entry point.
  *  grad_weights   device fp32 [M, top_k]
  *  router_logits  device fp32 or (logits_bf16 = 1) bf16 [M, E]

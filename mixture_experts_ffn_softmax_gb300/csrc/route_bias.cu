@@ -840,7 +840,10 @@ __global__ void __launch_bounds__(kRbWarps * 32)
     id = -1;
   }
   const float l = id >= 0 ? rb_f32(row[id]) : -INFINITY;
-  const float g = id >= 0 ? gw[t * k + sl] : 0.f;
+  // (a masked expert's weight is 0 whatever came back for it: its item takes no part.
+  // Loaded all the same, together with l: 5.64 us at 16384 x 128, 5.78 after it)
+  float g = id >= 0 ? gw[t * k + sl] : 0.f;
+  if (l == -INFINITY) g = 0.f;
   float v[EPL];
   float d;            // the item's own part of its expert's entry
   float base = 0.f;   // what the entry has without it
@@ -932,7 +935,7 @@ __global__ void __launch_bounds__(kRbWarps * 32)
       id[h] = -1;
     }
     l[h] = id[h] >= 0 ? rb_f32(row[id[h]]) : -INFINITY;
-    g[h] = id[h] >= 0 ? gw[t * k + j] : 0.f;
+    g[h] = id[h] >= 0 && l[h] != -INFINITY ? gw[t * k + j] : 0.f;
   }
   float d[2];
   if (P.method == MOE_ROUTE_SOFTMAX && !P.renormalize) {

@@ -582,6 +582,30 @@ def test_route_backward_views_and_empty():
             assert (out[:E + 1] == -5).all() and (out[E + 1 + M * E:] == -5).all()
 
 
+@pytest.mark.parametrize("M,E,k", [(5, 32, 4), (40, 256, 8), (7, 500, 20), (6, 128, 40)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("method,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+def test_route_backward_masked_items_take_no_part(M, E, k, dtype, method, renorm):
+    """Whatever grad_weights holds for experts that are masked (their weights
+    are 0 and nothing made these numbers), the token's gradient is that of the
+    others."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(M, E, generator=g, device="cuda").to(getattr(torch, dtype))
+    ids = torch.argsort(torch.rand(M, E, generator=g, device="cuda"), 1)[:, :k].int().contiguous()
+    gw = torch.randn(M, k, generator=g, device="cuda")
+    masked = torch.rand(M, k, generator=g, device="cuda") < 0.4
+    masked[0], masked[1, 0] = True, True
+    logits.scatter_(1, ids.long(), torch.where(masked, float("-inf"), logits.float().gather(
+        1, ids.long())).to(logits.dtype))
+    clean = torch.where(masked, 0.0, gw)
+    ref = pkg.moe_route_backward(clean, logits, ids, method, renorm, 1.5)
+    assert torch.isfinite(ref).all() and (ref[0] == 0).all() and (ref != 0).any()
+    check_backward(clean, logits, ids, method, renorm, 1.5)
+    for junk in (float("nan"), float("inf"), -float("inf"), 3e38):
+        got = pkg.moe_route_backward(torch.where(masked, junk, gw), logits, ids, method, renorm, 1.5)
+        assert torch.equal(got, ref), junk
+
+
 # ------------------------------------------------- streams, graphs, threads --
 def test_route_ops_on_other_streams_in_graphs_and_threads():
     a = (8, "sigmoid", True, 4, 8, 1, 2.5)
