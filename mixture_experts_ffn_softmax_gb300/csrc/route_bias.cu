@@ -160,6 +160,17 @@ __device__ __noinline__ int2 rb_choose64(const T* row, const float* bias, const 
   return id;
 }
 
+// A sigmoid, over e^top where the largest chosen logit top is below 0: scores that
+// underflow by themselves, and those below -88 where 1 / (1 + e^-l) is 0, keep their
+// ratio to the others.  (top is the token's: its lanes go one way.)
+__device__ __forceinline__ float rb_sigmoid_over(float l, float top) {
+  if (top >= 0.f) {
+    const float a = expf(-fabsf(l));
+    return (l < 0.f ? a : 1.0f) / (1.0f + a);
+  }
+  return expf(l - top) / (1.0f + expf(l));
+}
+
 // Weights of the chosen experts (lane j: chosen j and j + 32), in fp32.
 // Ratios of the chosen scores come from the logits' differences where the
 // scores themselves would underflow; a masked expert's weight is 0, and a
@@ -184,10 +195,9 @@ __device__ __noinline__ void rb_weights(const T* row, const RbParams& P, int id0
   const bool renorm = P.method == MOE_ROUTE_SIGMOID || P.renormalize;
   if (renorm) mx = rb_max(fmaxf(l0, l1));
   float p0, p1;
-  // sigmoid below -60 is exp to fp32 precision
-  if (P.method == MOE_ROUTE_SIGMOID && mx >= -60.f) {
-    p0 = 1.0f / (1.0f + expf(-l0));
-    p1 = 1.0f / (1.0f + expf(-l1));
+  if (P.method == MOE_ROUTE_SIGMOID) {
+    p0 = rb_sigmoid_over(l0, mx);
+    p1 = rb_sigmoid_over(l1, mx);
   } else {
     p0 = expf(l0 - mx);
     p1 = expf(l1 - mx);
@@ -750,7 +760,7 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     const bool renorm = !softmax || P.renormalize;
     const float top = renorm ? rb_seg_max<LPT>(chosen ? l : -INFINITY) : mx;
     const bool none = top == -INFINITY;  // nothing chosen that is not masked
-    float p = (!softmax && top >= -60.f) ? 1.0f / (1.0f + expf(-l)) : expf(l - top);
+    float p = softmax ? expf(l - top) : rb_sigmoid_over(l, top);
     if (!chosen || none) p = 0.f;
     float total = renorm ? rb_seg_sum<LPT>(p) : sum;
     if (none) total = 1.0f;

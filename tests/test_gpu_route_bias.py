@@ -442,6 +442,21 @@ def test_route_biased_second_experts_on_both_sides_of_a_rounding(E, G, kg):
         assert torch.equal(ids, biased_ids(part, bias, k, "sigmoid", kg, G, 1))
 
 
+@pytest.mark.parametrize("E,k", [(14, 14), (30, 30), (64, 64)])
+@pytest.mark.parametrize("top", [80.0, 1.0, -1.0, -17.0, -40.0, -59.0, -60.5, -87.0, -89.0, -300.0])
+def test_route_biased_sigmoid_weights_of_far_logits(E, k, top):
+    """Chosen experts whose scores are tiny, underflow in fp32, or lie on both
+    sides of that: their weights are ratios of the exact scores."""
+    rng = np.random.default_rng(k)
+    l = np.float32(top - rng.uniform(0, 85, (32, E)))
+    l[:, 0] = top
+    l[1:4, 1:] = top - np.float32([0.5, 30.0, 80.0])[:, None]
+    logits = torch.tensor(l, device="cuda")
+    bias = torch.tensor(rng.normal(size=E), dtype=torch.float32, device="cuda")
+    w, _ = check_biased(logits, bias, args(k, "sigmoid", scale=2.5))
+    assert (w > 0).all()
+
+
 # ------------------------------------------------------------- gradient --
 BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
         (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
