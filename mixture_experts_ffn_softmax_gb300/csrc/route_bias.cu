@@ -469,8 +469,13 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     // ---- groups: kept ones as a mask of the segment ----
     uint32_t kept = 0xffffffffu;
     if (grouped) {
-      // lane g: group g's score, and the size of what it is the sum of
-      float gk = -INFINITY, mag = 0.f;
+      // lane g: group g's score, and the size of what it is the sum of; -1 for a score
+      // that is -inf exactly (its experts masked, or all but one of those that it sums)
+      float gk = -INFINITY, mag = -1.f;
+      const bool sum2 = P.group_select_mode != 0;
+      auto size = [&](float b1, float b2) {
+        return (sum2 ? b2 : b1) == -INFINITY ? -1.f : sum2 ? fabsf(b1) + fabsf(b2) : fabsf(b1);
+      };
       float* row_c = reinterpret_cast<float*>(sm) + (seg0 / LPT) * E;
       auto store_c = [&]() {
         __syncwarp();
@@ -493,10 +498,9 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
           b1 = fmaxf(b1, o1);
         }
-        const bool sum2 = P.group_select_mode != 0;
         const int from = seg0 + min(sl * lpg, LPT - 1);
         gk = __shfl_sync(0xffffffffu, sum2 ? b1 + b2 : b1, from);
-        mag = __shfl_sync(0xffffffffu, sum2 ? fabsf(b1) + fabsf(b2) : fabsf(b1), from);
+        mag = __shfl_sync(0xffffffffu, size(b1, b2), from);
       } else {
         // by parts of a group per lane, joined in lane g
         const int parts = LPT / G, part = sl / G, g = sl - part * G;
@@ -519,8 +523,8 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
             b1 = fmaxf(b1, o1);
           }
         }
-        gk = P.group_select_mode == 0 ? b1 : b1 + b2;
-        mag = P.group_select_mode == 0 ? fabsf(b1) : fabsf(b1) + fabsf(b2);
+        gk = sum2 ? b1 + b2 : b1;
+        mag = size(b1, b2);
       }
       if (sl >= G) gk = -INFINITY;
       // rank among the groups, and the groups too close to tell apart: each of the two c
@@ -534,6 +538,9 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
         rank += (o > gk || (o == gk && h < sl)) ? 1 : 0;
         if (!(fabsf(o - gk) > gerr)) near |= 1u << h;
       }
+      // (-inf is below all others and the index settles its ties.  Sums that only fp32
+      // takes to -inf are near every other by their own lane, where mag is inf)
+      if (mag < 0.f) near = 0u;
       const uint32_t all = __ballot_sync(0xffffffffu, sl < G && rank < P.k_group);
       kept = LPT == 32 ? all : (all >> seg0) & ((1u << (LPT & 31)) - 1u);
       // (a group's own bit is never on the other side)
@@ -569,8 +576,9 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           for (int i = sl * gs; i < sl * gs + gs; ++i) place(row_c[i], i);
         }
         const bool holds = WHOLE ? e0 < E : sl < G;
-        const float least = P.group_select_mode == 0 ? v1 : v2;  // v3's rival
-        if (seg_unsure && holds) hard |= !(least - v3 > kerr * p1 + 1.2e-7f * fabsf(least));
+        const float least = sum2 ? v2 : v1;  // v3's rival, if it is not as masked as v3
+        if (seg_unsure && holds && least != -INFINITY)
+          hard |= !(least - v3 > kerr * p1 + 1.2e-7f * fabsf(least));
         // the best two: keys of c and p
         uint64_t q1 = 0, q2 = 0;
         double pa = 0.0, pb = 0.0;

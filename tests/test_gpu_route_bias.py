@@ -457,6 +457,55 @@ def test_route_biased_sigmoid_weights_of_far_logits(E, k, top):
     assert (w > 0).all()
 
 
+@pytest.mark.parametrize("E,G,kg,mode", [(256, 8, 4, 1), (256, 8, 4, 0), (336, 8, 4, 1), (128, 4, 2, 1)])
+@pytest.mark.parametrize("method", ["sigmoid", "softmax"])
+def test_route_biased_masked_groups(E, G, kg, mode, method):
+    """Whole groups masked, or (mode 1) all but one of a group's experts: up to
+    as many as are dropped, and more, so that some of them are kept."""
+    k, gs = 4, E // G
+    rng = np.random.default_rng(E + mode)
+    logits = rng.normal(size=(300, E)).astype(np.float32)
+    for t in range(300):
+        for g in rng.permutation(G)[:t % (G + 1)]:
+            left = rng.integers(0, 2) if t % 2 else 0
+            logits[t, g * gs + left:(g + 1) * gs] = -np.inf
+    for spread in (0.0, 0.3):
+        bias = torch.tensor(rng.normal(size=E) * spread, dtype=torch.float32, device="cuda")
+        check_biased(torch.tensor(logits, device="cuda"), bias, args(k, method, True, kg, G, mode))
+    # biases whose sums overflow in fp32 and not in 64 bits, beside masked groups
+    big = np.where(np.arange(E) // gs % 3 == 0, -3e38, 0.0) + rng.normal(size=E) * 0.3
+    check_biased(torch.tensor(logits, device="cuda"),
+                 torch.tensor(big, dtype=torch.float32, device="cuda"),
+                 args(k, method, True, kg, G, mode))
+
+
+def test_route_biased_masked_groups_stay_on_the_fast_path():
+    """Rows with masked groups (no -inf is near a finite score, and -inf ties
+    are settled by the index) take about the time of rows without: the 64-bit
+    choice of every token is 25 times that, the limit 4 times."""
+    M, E = 8192, 256
+    a = (8, "sigmoid", True, 4, 8, 1, 2.5)
+    logits = torch.randn(M, E, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    bias = torch.randn(E, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") * 0.05
+    masked = logits.clone()
+    masked[:, 64:128] = float("-inf")
+    w, ids = torch.empty(M, 8, device="cuda"), torch.empty(M, 8, dtype=torch.int32, device="cuda")
+
+    def best(l):
+        times = []
+        for _ in range(10):
+            t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            t0.record()
+            for _ in range(20):
+                pkg.moe_route(l, *a, w, ids, score_bias=bias)
+            t1.record()
+            t1.synchronize()
+            times.append(t0.elapsed_time(t1))
+        return min(times)
+    plain = best(logits)
+    assert best(masked) < 4 * plain
+
+
 # ------------------------------------------------------------- gradient --
 BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
         (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
