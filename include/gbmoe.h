@@ -475,6 +475,9 @@ GBMOE_API moe_status_t moe_quant_groups_fp8(const void* x, int64_t M, int32_t K,
  *            wait ran out of time (the output is then incomplete)
  * a, w, bias and out 16-byte aligned.  Limits: K a multiple of 16 up to 2^24,
  * N a multiple of 16 up to 2^22, M < 2^31, M * N <= 2^44.
+ * The profiler names the kernel that a product took: matmul_fp8_split16, 32, 64,
+ * 96 or 128 (rows of a tile, K split over a cluster) or matmul_fp8_pairs256 or
+ * 128 (columns of a CTA pair's tile).
  */
 GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const void* w,
                                       const float* w_scale, int32_t w_transposed,

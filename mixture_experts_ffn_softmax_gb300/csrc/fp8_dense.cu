@@ -1039,9 +1039,10 @@ moe_status_t launch_pair(const MatmulFp8Args& a, const DenseParams& P, cudaStrea
   if (moe_status_t st = dense_out_map(a, &tmO)) return st;
   const int64_t tiles = ceil_div<int64_t>(a.M, 256) * ceil_div(a.N, NT);
   const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, a.num_sms / 2));
-  prof_before("matmul_fp8", s);
+  const char* name = NT == 256 ? "matmul_fp8_pairs256" : "matmul_fp8_pairs128";
+  prof_before(name, s);
   launch_kernel(dense_fp8_pair_kernel<TR, NT>, grid, kDpThreads, DpGeo<NT>::SMEM, s, tmA, tmB, tmO, P);
-  prof_after("matmul_fp8", s);
+  prof_after(name, s);
   return check_launch("matmul_fp8");
 }
 
@@ -1101,9 +1102,14 @@ moe_status_t launch_split(const MatmulFp8Args& a, const DenseParams& P, int S, c
   cudaLaunchAttribute at[2];
   split_config<T, TR>(cfg, at, S, ceil_div(a.N, 128), ceil_div<int64_t>(a.M, T));
   cfg.stream = s;
-  prof_before("matmul_fp8", s);
+  const char* name = T == 16   ? "matmul_fp8_split16"
+                     : T == 32 ? "matmul_fp8_split32"
+                     : T == 64 ? "matmul_fp8_split64"
+                     : T == 96 ? "matmul_fp8_split96"
+                               : "matmul_fp8_split128";
+  prof_before(name, s);
   cudaLaunchKernelEx(&cfg, dense_fp8_split_kernel<T, TR>, tmA, tmB, P, S);
-  prof_after("matmul_fp8", s);
+  prof_after(name, s);
   return check_launch("matmul_fp8");
 }
 

@@ -376,6 +376,36 @@ def test_matmul_pairs_of_few_blocks_back_to_back(blocks, N):
     assert all(torch.equal(out, ref) for out in outs) and err.item() == 0
 
 
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("kernel,M,K,N", [
+    # with more K blocks per part than scales are held at a time (16), except where it says
+    ("split16", 13, 4352, 10256), ("split16", 16, 144, 16),           # (few)
+    ("split32", 30, 4352, 10256), ("split32", 17, 4336, 10240),
+    ("split64", 60, 4352, 10256), ("split64", 61, 2048, 4112),        # (few)
+    ("split96", 90, 4592, 9712), ("split96", 96, 8192, 9728), ("split96", 90, 1936, 4112),  # (few)
+    ("split128", 125, 8176, 9712), ("split128", 256, 7168, 4096), ("split128", 255, 7152, 4080),
+    ("split128", 128, 5120, 9728),
+    # K blocks many times the stages; several tiles per pair in the second of each
+    ("pairs128", 500, 7152, 4080), ("pairs128", 12790, 2064, 384),
+    ("pairs256", 8200, 7184, 512), ("pairs256", 2601, 5136, 4112)])
+def test_matmul_exact_inputs_by_kernel(kernel, M, K, N, transposed):
+    """Each kernel by its name, over what only many K blocks reach: the scales'
+    second helping, the rings of stages and accumulators gone round."""
+    a, sa, w, sw, bias, y = exact_case(M, K, N, transposed, M + K)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.full((M + 2, N), 7.0, device="cuda", dtype=dt)
+        pkg.profiler_start()
+        try:
+            pkg.moe_matmul_fp8(a, sa, w, sw, bias, transposed, out=out[1:M + 1], error_word=err)
+        finally:
+            took = pkg.profiler_stop()
+        assert list(took) == ["matmul_fp8_" + kernel]
+        assert torch.equal(out[1:M + 1], (y + bias.double()).to(dt))
+        assert (out[0] == 7).all() and (out[M + 1] == 7).all()
+    assert err.item() == 0
+
+
 # ----------------------------------------------------------- together --
 def shared_oracle(x, w13, w2, s13, s2, b13=None, b2=None):
     q, s = quantised(x)
