@@ -451,6 +451,10 @@ GBMOE_API moe_status_t moe_quant_rows_fp8(const void* x, int64_t M, int32_t H, v
  * shorter):
  *   scale = fp32(max|z| / 448), 1 where that is 0 (and the codes then 0);
  *   q8 = e4m3(fp32(z / scale)), round to nearest even, saturating.
+ * The quotients by 448 and by the scale are correctly rounded.  SiLU is within
+ * 5.5 * 2^-24 of the exact one (relative; 0 for gates below -88, where e^-gate
+ * is beyond fp32) and its product with up rounded once, so that a code of z next
+ * to a border may be its neighbour.
  * A NaN makes its group's scale and codes NaN; an infinity its scale
  * infinite, its own code NaN and the others 0.
  *  x      device bf16 [M, K], or [M, 2K] for swiglu

@@ -153,6 +153,22 @@ def test_quant_groups_swiglu_tiny_groups(top):
     assert torch.isfinite(y).all()
 
 
+def test_quant_groups_swiglu_of_every_gate():
+    """SiLU of every bf16 gate (those whose e^-g fp32 holds), read off the scales
+    of groups that hold one gate each, with an up of 1."""
+    gate = torch.arange(1 << 16, device="cuda", dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    keep = torch.isfinite(gate) & (gate > -86) & (gate.abs() > 1e-30)
+    gate = torch.where(keep, gate, torch.ones_like(gate))
+    x = torch.zeros(512, 2, 128, 128, device="cuda", dtype=torch.bfloat16)
+    x[:, 0, :, 5] = gate.view(512, 128)
+    x[:, 1, :, 5] = 1.0
+    _, s = pkg.moe_quant_groups_fp8(x.view(512, -1), swiglu=True)
+    ref = np.abs(oracle.silu(f64(gate))).reshape(512, 128) / 448.0
+    # 2^-h 2.5 (measured: 2.45; its share of 1 + e^-g is below 1), 1 - t, the sum,
+    # the quotient and the scale's 1 each; the product with 1 is exact
+    assert (np.abs(s.double().cpu().numpy() - ref) <= 6.5 * U32 * ref).all()
+
+
 # ----------------------------------------------------------------- product --
 SHAPES = [
     # (M, K, N)
