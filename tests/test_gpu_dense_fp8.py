@@ -422,6 +422,57 @@ def test_matmul_exact_inputs_by_kernel(kernel, M, K, N, transposed):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_quant_groups_past_32_bits(swiglu):
+    K = 1936
+    M, n = (1 << 31) // K + 3000, 100
+    x = torch.zeros(M, 2 * K if swiglu else K, device="cuda", dtype=torch.bfloat16)
+    rows = torch.randn(n, x.shape[1], generator=gen(5), device="cuda").to(torch.bfloat16)
+    x[:n], x[-n:] = rows, rows
+    q, s = pkg.moe_quant_groups_fp8(x, swiglu)
+    q0, s0 = pkg.moe_quant_groups_fp8(rows, swiglu)
+    for part in (slice(0, n), slice(M - n, M)):
+        assert torch.equal(q[part].view(torch.uint8), q0.view(torch.uint8))
+        assert torch.equal(s[part], s0)
+
+
+@pytest.mark.parametrize("M,K,N", [((1 << 31) // 4096 + 700, 272, 4096),   # the output, by pairs
+                                   ((1 << 31) // 4112 + 300, 4112, 144),   # the activations
+                                   (33, 4096, (1 << 19) + 4112),           # the weight, by tiles of few rows
+                                   (2600, 528, 1 << 20)])                  # the output, 4096 column tiles
+@pytest.mark.parametrize("transposed", [False, True])
+def test_matmul_past_32_bits(M, K, N, transposed):
+    """Sums that are exact and so do not depend on the kernel: the last rows and
+    columns as in calls of their own."""
+    g = gen(M)
+    KB, NB = -(-K // 128), -(-N // 128)
+    codes = torch.arange(-4, 5, device="cuda").float().to(E4M3).view(torch.uint8)
+
+    def some(rows, cols):                      # (in parts: randint makes 64-bit numbers)
+        t = torch.empty(rows, cols, device="cuda", dtype=torch.uint8)
+        for p in t.split(max(1, (1 << 28) // cols)):
+            p.copy_(codes[torch.randint(0, 9, p.shape, generator=g, device="cuda", dtype=torch.int32)])
+        return t
+    a, sa = some(M, K), torch.exp2(torch.randint(-2, 3, (M, KB), generator=g, device="cuda").float())
+    shape, sshape = ((N, K), (NB, KB)) if transposed else ((K, N), (KB, NB))
+    w, sw = some(*shape), torch.exp2(torch.randint(-2, 3, sshape, generator=g, device="cuda").float())
+    out = pkg.moe_matmul_fp8(a, sa, w, sw, transposed=transposed)
+    m, n = min(M, 37), 144
+    nb = (N - n) // 128 * 128                  # whole scale blocks of columns
+    if transposed:
+        wn, sn = w[nb:], sw[nb // 128:]
+    else:
+        wn, sn = w[:, nb:].contiguous(), sw[:, nb // 128:].contiguous()
+    rows = pkg.moe_matmul_fp8(a[-m:].clone(), sa[-m:].clone(), w, sw, transposed=transposed)
+    cols = pkg.moe_matmul_fp8(a, sa, wn, sn, transposed=transposed)
+    assert torch.equal(out[-m:], rows) and torch.equal(out[:, nb:], cols)
+    wd = wn.view(E4M3).double() if not transposed else wn.view(E4M3).double().t()
+    sd = (sn if not transposed else sn.t()).double()
+    ref = (a[-m:].view(E4M3).double() * sa[-m:].double().repeat_interleave(128, 1)[:, :K]) @ (
+        wd * sd.repeat_interleave(128, 0)[:K].repeat_interleave(128, 1)[:, :N - nb])
+    assert torch.equal(rows[:, nb:], ref.to(torch.bfloat16))
+
+
 # ----------------------------------------------------------- together --
 def shared_oracle(x, w13, w2, s13, s2, b13=None, b2=None):
     q, s = quantised(x)

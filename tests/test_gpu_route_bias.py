@@ -670,6 +670,32 @@ def test_route_backward_masked_items_take_no_part(M, E, k, dtype, method, renorm
         assert torch.equal(got, ref), junk
 
 
+@pytest.mark.parametrize("method,renorm,E,k,kg,G", [("sigmoid", True, 256, 8, 4, 8),
+                                                    ("softmax", False, 257, 8, 1, 1),
+                                                    ("softmax", False, 128, 34, 1, 1)])
+def test_route_ops_past_32_bits(method, renorm, E, k, kg, G):
+    """More than 2^31 logits: the last rows as in a call of their own (all rows
+    but the first and last are of one logit)."""
+    M, n = (1 << 31) // E + 5000, 200
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.zeros(M, E, device="cuda", dtype=torch.bfloat16)
+    rows = torch.randn(n, E, generator=g, device="cuda").to(torch.bfloat16)
+    gw = torch.randn(M, k, generator=g, device="cuda")
+    logits[:n], logits[-n:] = rows, rows
+    bias = torch.randn(E, generator=g, device="cuda") * 0.05
+    a = (k, method, renorm, kg, G, 0, 2.5)
+    w, ids = pkg.moe_route(logits, *a, score_bias=bias)
+    w0, i0 = check_biased(rows, bias, args(k, method, renorm, kg, G, 0, 2.5))
+    # (a few tokens may be summed in another order)
+    rtol = 2 * weight_rtol(rows.double().cpu().numpy(), E)
+    for part in (slice(0, n), slice(M - n, M)):
+        assert torch.equal(ids[part], i0)
+        assert ((w[part] - w0).abs() <= rtol * w0).all()
+    gl = pkg.moe_route_backward(gw, logits, ids, method, renorm, 2.5)
+    for part in (slice(0, n), slice(M - n, M)):
+        assert torch.equal(gl[part], pkg.moe_route_backward(gw[part], rows, i0, method, renorm, 2.5))
+
+
 # ------------------------------------------------- streams, graphs, threads --
 def test_route_ops_on_other_streams_in_graphs_and_threads():
     a = (8, "sigmoid", True, 4, 8, 1, 2.5)
