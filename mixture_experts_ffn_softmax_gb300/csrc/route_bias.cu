@@ -476,6 +476,9 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
       auto size = [&](float b1, float b2) {
         return (sum2 ? b2 : b1) == -INFINITY ? -1.f : sum2 ? fabsf(b1) + fabsf(b2) : fabsf(b1);
       };
+      auto score = [&](float b1, float b2) {  // (inf - inf counts as -inf)
+        return !sum2 ? b1 : b2 == -INFINITY ? -INFINITY : b1 + b2;
+      };
       float* row_c = reinterpret_cast<float*>(sm) + (seg0 / LPT) * E;
       auto store_c = [&]() {
         __syncwarp();
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           b1 = fmaxf(b1, o1);
         }
         const int from = seg0 + min(sl * lpg, LPT - 1);
-        gk = __shfl_sync(0xffffffffu, sum2 ? b1 + b2 : b1, from);
+        gk = __shfl_sync(0xffffffffu, score(b1, b2), from);
         mag = __shfl_sync(0xffffffffu, size(b1, b2), from);
       } else {
         // by parts of a group per lane, joined in lane g
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
             b1 = fmaxf(b1, o1);
           }
         }
-        gk = sum2 ? b1 + b2 : b1;
+        gk = score(b1, b2);
         mag = size(b1, b2);
       }
       if (sl >= G) gk = -INFINITY;
@@ -599,6 +602,7 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           }
         };
         order(q1, pa, q2, pb);
+        uint64_t q3 = 0;  // the best that the group's two leave out
         if constexpr (WHOLE) {
           for (int o = 1; o < 1 << P.lpg_log; o <<= 1) {
             uint64_t o1 = __shfl_xor_sync(0xffffffffu, q1, o), o2 = __shfl_xor_sync(0xffffffffu, q2, o);
@@ -606,7 +610,14 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
             order(q1, pa, o1, oa);
             order(q2, pb, o1, oa);
             order(q2, pb, o2, ob);
+            q3 = max(max(q3, __shfl_xor_sync(0xffffffffu, q3, o)), max(o1, o2));
           }
+        }
+        // softmax: the sum's error could have put another one among them
+        if (softmax) {
+          if (!sum2) q3 = max(q2, q3);
+          if (seg_unsure && q3 > rb_key64(-INFINITY))
+            hard |= !(static_cast<float>(rb_value64(sum2 ? q2 : q1) - rb_value64(q3)) > 6e-7f * p1);
         }
         double c64 = rb_value64(q1), p64 = pa;
         if (P.group_select_mode == 1) {
@@ -746,21 +757,35 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
       const double c64 = l == -INFINITY ? -INFINITY : p64 + be + 0.0;
       const uint64_t mykey = mine ? rb_key64(c64) : 0;
       uint64_t next = 0;  // the largest key below this lane's, and its p
-      double pnext = 0.0;
+      const uint64_t pbits = static_cast<uint64_t>(__double_as_longlong(p64));
+      uint64_t pnext = 0, peq = 0;  // peq: the largest p among equal c of different p
       rank = 0;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const uint64_t o = __shfl_sync(0xffffffffu, mykey, seg0 + j);
         const int oe = __shfl_sync(0xffffffffu, e, seg0 + j);
-        const double op = __shfl_sync(0xffffffffu, p64, seg0 + j);
+        // (p are positive: their bits order as they do, off the slow FP64 unit)
+        const uint64_t op = __shfl_sync(0xffffffffu, pbits, seg0 + j);
         rank += (o > mykey || (o == mykey && oe < e)) ? 1 : 0;
         if (o < mykey && o > next) {
           next = o;
           pnext = op;
         }
+        if (o == mykey && op != pbits) peq = max(peq, max(op, pbits));
+      }
+      // All pairs are decided if each candidate is from the next below it, the ones
+      // that are not chosen too: gaps and differences of p add up along the order.
+      // Equal c of different p are equal by this inverse only, unless both p vanish in c
+      // (below half a step of a bias, whatever the inverse).
+      if (softmax && mykey > rb_key64(-INFINITY)) {
+        if (peq != 0)
+          open = static_cast<float>(__longlong_as_double(static_cast<long long>(peq))) >
+                 5e-17f * fabsf(static_cast<float>(c64));
+        if (next != 0)
+          open |= undecided(c64 - rb_value64(next),
+                            p64 - __longlong_as_double(static_cast<long long>(pnext)));
       }
       if (mine == 0u) rank = LPT;
-      if (softmax && rank < k && next != 0) open = undecided(c64 - rb_value64(next), p64 - pnext);
     }
     const uint32_t hards = __ballot_sync(0xffffffffu, (hard || open) && live);
     // ---- weights (as rb_weights) ----

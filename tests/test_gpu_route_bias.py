@@ -506,6 +506,40 @@ def test_route_biased_masked_groups_stay_on_the_fast_path():
     assert best(masked) < 4 * plain
 
 
+@pytest.mark.parametrize("E,k,G,kg,mode,M", [(16, 13, 8, 7, 0, 400), (64, 8, 1, 1, 0, 400), (256, 1, 1, 1, 0, 400),
+                                             (24, 9, 8, 3, 0, 400), (256, 8, 8, 4, 1, 400), (256, 8, 8, 4, 0, 4200),
+                                             (60, 8, 5, 3, 1, 400), (128, 8, 8, 3, 1, 4200), (336, 9, 8, 4, 1, 300)])
+@pytest.mark.parametrize("spread", [8.0, 30.0])
+def test_route_biased_near_certain_softmax_and_biases_in_steps(E, k, G, kg, mode, M, spread):
+    """Rows whose largest score is 1 but for 1e-5 to 1e-60, and biases in steps of
+    a half: 1 - 1e-9 - 0.5 against 0.5 + 1e-40, which an fp32 sum of the exponentials
+    calls equal."""
+    for seed in range(3):
+        rng = np.random.default_rng(seed + E)
+        logits = rng.normal(size=(M, E)) * spread
+        bias = torch.tensor(np.round(rng.normal(size=E) * 2) / 2, dtype=torch.float32, device="cuda")
+        for dt in (torch.float32, torch.bfloat16):
+            l = torch.tensor(logits, device="cuda").to(dt)
+            # 64 bits define the sum of a row, and with it a score near 1, up to the order
+            # of E additions, 1e-13 at most: left out are rows that such an error could
+            # change.  Nothing does where all else vanishes beside 1, nor where the largest
+            # score lacks more of 1 than the error (the other c are steps of a half plus
+            # what they hold of the lack), unless its group's second makes up for it.
+            x = l.double().cpu().numpy()
+            ex = np.exp(x - x.max(1, keepdims=True))
+            rows, best = np.arange(M), x.argmax(1)
+            ex[rows, best] = 0.0
+            lack = ex.sum(1)
+            ex[rows, best] = 1.0
+            c = ex / ex.sum(1, keepdims=True) + bias.double().cpu().numpy()
+            two = np.sort(c.reshape(M, G, -1), 2)[:, :, -2:].sum(2)
+            d = np.abs(two - two[rows, best // (E // G)][:, None])
+            d[rows, best // (E // G)] = 1.0
+            fine = (lack < 1e-17) | ((lack > 1e-12) & (d > 1e-13).all(1))
+            assert fine.sum() > M // 5
+            check_biased(l[torch.tensor(fine, device="cuda")], bias, args(k, "softmax", True, kg, G, mode))
+
+
 # ------------------------------------------------------------- gradient --
 BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
         (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
