@@ -450,8 +450,11 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
 #pragma unroll
     for (int i = 0; i < EPL; ++i) hard |= c[i] != c[i];
     // softmax: 1 / sum of exp(l - mx) for what is compared in 64 bits.  The sum stays
-    // in fp32, each term within 2 ulp and their additions compensated, 2^-21 in all:
-    // common to all scores, it moves a difference of two c by 2^-21 of that of their p.
+    // in fp32.  Its error, in 2^-24: a term's expf 4 and its argument's d (below 4.5 in
+    // the mean, as above), the additions compensated in a lane and 5 across lanes, 13.5
+    // in all and below sum_err: common to all scores, it moves a difference of two c by
+    // as much of that of their p.
+    constexpr float sum_err = 1e-6f;
     auto inv64 = [&]() {
       float s = 0.f, comp = 0.f;
 #pragma unroll 1
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     };
     // such a difference dc is open where the sum's error could turn it
     auto undecided = [&](double dc, double dp) {
-      return softmax && dp != 0.0 && !(fabsf(static_cast<float>(dc)) > 6e-7f * fabsf(static_cast<float>(dp)));
+      return softmax && dp != 0.0 && !(fabsf(static_cast<float>(dc)) > sum_err * fabsf(static_cast<float>(dp)));
     };
     // ---- groups: kept ones as a mask of the segment ----
     uint32_t kept = 0xffffffffu;
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
         if (softmax) {
           if (!sum2) q3 = max(q2, q3);
           if (seg_unsure && q3 > rb_key64(-INFINITY))
-            hard |= !(static_cast<float>(rb_value64(sum2 ? q2 : q1) - rb_value64(q3)) > 6e-7f * p1);
+            hard |= !(static_cast<float>(rb_value64(sum2 ? q2 : q1) - rb_value64(q3)) > sum_err * p1);
         }
         double c64 = rb_value64(q1), p64 = pa;
         if (P.group_select_mode == 1) {
