@@ -449,21 +449,31 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     bool hard = false;  // needs rb_choose64
 #pragma unroll
     for (int i = 0; i < EPL; ++i) hard |= c[i] != c[i];
-    // softmax: 1 / sum of exp(l - mx) for what is compared in 64 bits.  The sum stays
-    // in fp32.  Its error, in 2^-24: a term's expf 4 and its argument's d (below 4.5 in
-    // the mean, as above), the additions compensated in a lane and 5 across lanes, 13.5
-    // in all and below sum_err: common to all scores, it moves a difference of two c by
-    // as much of that of their p.
-    constexpr float sum_err = 1e-6f;
+    // softmax: 1 / sum of exp(l - mx) for what is compared in 64 bits.  The sum stays in
+    // pairs of fp32: a term is expf (2 ulp, 4 in 2^-24) with what l - mx lost in its
+    // rounding put back (a rounding, 1), the additions' errors are kept.  5 in all, below
+    // sum_err: common to all scores, it moves a difference of two c by as much of that
+    // of their p.  (The tokens that this leaves open are what a call's end waits for.)
+    constexpr float sum_err = 3.2e-7f;
     auto inv64 = [&]() {
       float s = 0.f, comp = 0.f;
+      auto add = [&](float x, float more) {  // (the same bits with its operands exchanged:
+        const float y = s + x;               // all lanes get one inverse)
+        comp = (comp + more) + (s >= x ? (s - y) + x : (x - y) + s);
+        s = y;
+      };
 #pragma unroll 1
       for (int i = sl; i < E; i += LPT) {
-        const float x = expf(rb_f32(row[i]) - mx), y = s + x;
-        comp += s >= x ? (s - y) + x : (x - y) + s;
-        s = y;
+        const float l = rb_f32(row[i]), d = l - mx, back = d + mx;
+        // l - mx - d, exactly (Knuth's sum of two)
+        const float r = d > -200.f ? (l - back) + ((back - d) - mx) : 0.f;
+        const float x = expf(d);
+        add(fmaf(x, r, x), 0.f);
       }
-      return 1.0 / (static_cast<double>(rb_seg_sum<LPT>(s)) + rb_seg_sum<LPT>(comp));
+#pragma unroll
+      for (int o = LPT / 2; o > 0; o >>= 1)
+        add(__shfl_xor_sync(0xffffffffu, s, o), __shfl_xor_sync(0xffffffffu, comp, o));
+      return 1.0 / (static_cast<double>(s) + comp);
     };
     // such a difference dc is open where the sum's error could turn it
     auto undecided = [&](double dc, double dp) {
