@@ -757,18 +757,23 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
     int rank = sl;  // of the lane's candidate
     bool open = false;
     int n = k + 2;
+    // (what another token of the warp needs changes nothing here, the order of the
+    // weights' sum neither: a token's results do not depend on its neighbours)
+    const uint32_t own_lanes = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << seg0;
     const uint32_t mores = __ballot_sync(0xffffffffu, sl < k && reached() && live);
+    const bool more = (mores & own_lanes) != 0u;
     if (mores != 0u) {  // as many candidates as lanes
       for (; n < LPT; ++n) round(n);
       if (sl < k && reached()) hard = true;
-      candidate();
+      if (more) candidate();
     }
-    if ((__ballot_sync(0xffffffffu, close && live) | mores) != 0u) {
+    const uint32_t closes = __ballot_sync(0xffffffffu, close && live) | mores;
+    if (closes != 0u) {
       // in 64 bits among the candidates
       const double inv = softmax ? inv64() : 1.0;
       const double p64 = rb_score64(l, softmax, mx) * inv;
       const double c64 = l == -INFINITY ? -INFINITY : p64 + be + 0.0;
-      const uint64_t mykey = mine ? rb_key64(c64) : 0;
+      const uint64_t mykey = mine != 0u && (more || sl < k + 2) ? rb_key64(c64) : 0;
       uint64_t next = 0;  // the largest key below this lane's, and its p
       const uint64_t pbits = static_cast<uint64_t>(__double_as_longlong(p64));
       uint64_t pnext = 0, peq = 0;  // peq: the largest p among equal c of different p
@@ -798,7 +803,11 @@ __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72
           open |= undecided(c64 - rb_value64(next),
                             p64 - __longlong_as_double(static_cast<long long>(pnext)));
       }
-      if (mine == 0u) rank = LPT;
+      if (mykey == 0) rank = LPT;
+      if ((closes & own_lanes) == 0u) {
+        rank = sl;
+        open = false;
+      }
     }
     const uint32_t hards = __ballot_sync(0xffffffffu, (hard || open) && live);
     // ---- weights (as rb_weights) ----

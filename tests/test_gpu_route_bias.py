@@ -540,6 +540,26 @@ def test_route_biased_near_certain_softmax_and_biases_in_steps(E, k, G, kg, mode
             check_biased(l[torch.tensor(fine, device="cuda")], bias, args(k, "softmax", True, kg, G, mode))
 
 
+@pytest.mark.parametrize("E,k,G,kg,mode", [(80, 14, 5, 5, 0), (160, 14, 5, 3, 0), (128, 4, 8, 7, 1), (200, 14, 2, 2, 0),
+                                           (256, 14, 16, 11, 1), (32, 4, 1, 1, 0)])
+@pytest.mark.parametrize("method", ["sigmoid", "softmax"])
+def test_route_biased_tokens_do_not_see_their_neighbours(E, k, G, kg, mode, method):
+    """Two tokens share a warp: one with non-finite scores, or with near ones that
+    take further rounds, leaves the other's ids and weights as they are, to the bit."""
+    M = 4500
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(M, E, generator=g, device="cuda")
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1
+    a = (k, method, True, kg, G, mode)
+    w0, i0 = pkg.moe_route(logits, *a, score_bias=bias)
+    rows = torch.arange(M, device="cuda") % 2 == 0
+    for other in (torch.full_like(logits, float("nan")), torch.zeros_like(logits), logits * 2.0 ** -22,
+                  torch.where(torch.rand(M, E, generator=g, device="cuda") < 0.02, float("inf"), logits)):
+        for hit in (rows, ~rows):
+            w, ids = pkg.moe_route(torch.where(hit[:, None], other, logits), *a, score_bias=bias)
+            assert torch.equal(ids[~hit], i0[~hit]) and torch.equal(w[~hit], w0[~hit])
+
+
 # ------------------------------------------------------------- gradient --
 BACK = [(1, 1, 1), (3, 8, 2), (130, 8, 8), (33, 17, 5), (64, 64, 33), (65, 128, 8), (257, 256, 8),
         (31, 384, 6), (9, 1000, 64), (5, 1024, 16)]
