@@ -226,8 +226,11 @@ def moe_route_backward(grad_weights: torch.Tensor, router_logits: torch.Tensor,
                        error_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of moe_route's weights: grad_weights fp32 [M, k] for the
     experts topk_ids int32 [M, k] -> grad_logits [M, E] in the logits' type.
-    The choice of experts is held fixed.  error_word: int32 [1], set where an
-    id is outside [0, E) (such items take no part)."""
+    The choice of experts is held fixed.  grad_weights are the products of the
+    layer's output gradient with the chosen experts' outputs, which the forward
+    does not keep: they come from the caller's backward pass of the experts.
+    error_word: int32 [1], set where an id is outside [0, E) (such items take
+    no part, nor do those of masked experts)."""
     M, E = _matrix(router_logits, "router_logits")
     k = _matrix(topk_ids, "topk_ids")[1]
     dev = router_logits.get_device()

@@ -373,9 +373,13 @@ __device__ __forceinline__ void rb_load(const bf16* p, float (&l)[N]) {
 // lanes to a group).  Otherwise every LPT-th expert, so that loads of rows of any length
 // are whole lines.
 //
-// Bound: issue slots and, for few tokens, the chain of one token (2.9 us of a graph
-// node with 256 experts).  8192 tokens x 256 experts, 8 of 4 of 8 groups, from 281 us
-// (every token by rb_choose64) to 11.3 us; 16384 x 128 bf16, 8 chosen, 298 to 11.2 us.
+// Bound: latency.  A warp takes its tokens one after the other with nothing loaded ahead,
+// and the blocks of many tokens are little more than are resident: 8192 x 256 are 1.12
+// waves (6 blocks of four warps per SM at 80 registers), issue slots 44 % busy, loads the
+// largest stall; 16384 x 128 are 1.92 waves (7 per SM at 72), 57 %.  The last warp is often
+// one whose token needed 64 bits.  In a graph, over 24 seeds: 8192 tokens x 256 experts, 8
+// of 4 of 8 groups, 9.5 to 13.0 us (every token by rb_choose64: 281); 16384 x 128 bf16
+// softmax, 8 chosen, 10.1 to 17.2 (298); one token of 256 experts 3.0.
 template <int EPL, int LPT, bool WHOLE, typename T>
 __global__ void __launch_bounds__(kRbWarps * 32, EPL <= 16 ? 6 : 1)  // (six: 72-80 registers)
     route_biased_kernel(const T* __restrict__ logits, const float* __restrict__ bias, RbParams P,
@@ -1069,7 +1073,8 @@ void launch_fast(const RouteArgs& a, const float* bias, RbParams P, cudaStream_t
   const bool whole =
       a.E % EPL == 0 && (a.k_group == a.group_count ||
                          (gs == lpg * EPL && (lpg & (lpg - 1)) == 0));
-  // at most the 16 blocks of four warps that an SM holds, on 152 of them
+  // (a bound of 16 blocks for each of 152 SMs, of which 6 to 8 are resident at 64 to 80
+  // registers: warps of larger calls go through several tokens, their biases loaded once)
   launch_kernel(whole ? route_biased_kernel<EPL, LPT, true, T>
                       : route_biased_kernel<EPL, LPT, false, T>,
                 static_cast<unsigned>(std::min<int64_t>(blocks, 152 * 16)), warps * 32, smem, s,
