@@ -126,8 +126,9 @@ GBMOE_API moe_status_t moe_route_bf16(const void* router_logits, int64_t M, int3
  * c is compared as in 64-bit arithmetic (experts whose c agree there are
  * ties; what the order of a row's additions leaves open there, about 1e-16 of
  * a score near 1, is open here).  A group whose sum is inf - inf counts as
- * -inf.  Weights are computed in fp32, about 1e-7 of themselves from the exact
- * ones.  An expert with logit -inf is masked: it is chosen only after every
+ * -inf.  Weights are computed in fp32: off by about 1e-7 of themselves, and by
+ * 6e-8 more for each 1 that their logit lies below the row's largest.  An
+ * expert with logit -inf is masked: it is chosen only after every
  * other expert of the kept groups, with weight 0, and a token whose chosen
  * experts are all masked has weights of 0.  A NaN score is chosen as late;
  * its weight, and with renormalised weights the token's, are NaN; in a

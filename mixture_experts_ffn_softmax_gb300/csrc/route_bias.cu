@@ -367,7 +367,7 @@ __device__ __forceinline__ void rb_load(const bf16* p, float (&l)[N]) {
 // groups that are too close likewise, from their two best experts.  Where that does not
 // settle it, or a score is NaN, the warp takes the token by rb_choose64 (20 us for one
 // token of 512 experts, which is why the steps before it are there: 10804 x 336 softmax,
-// 13 of 4 of 8 groups, with two such tokens 80 us, now 27).
+// 13 of 4 of 8 groups, with two such tokens 80 us, now 25).
 //
 // WHOLE: lanes hold EPL consecutive experts or none, of one group (a power of two of
 // lanes to a group).  Otherwise every LPT-th expert, so that loads of rows of any length
