@@ -502,6 +502,44 @@ GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const
                                       int32_t out_f32, void* out, int32_t* error_word,
                                       moe_stream_t stream);
 
+/* ---------------------------- products of rows sorted by expert, MX FP4 --
+ * moe_swiglu: z[r, i] = w[r] SiLU(gate_up[r, i]) gate_up[r, I + i], rounded once
+ * from fp32 (w = 1 for row_weights = NULL).  moe_swiglu_backward, from grad_z =
+ * dL/dz and with g, u, sig(g) = 1 / (1 + e^-g):
+ *   grad_gate_up[r, i]     = w[r] grad_z u sig(g) (1 + g (1 - sig(g)))
+ *   grad_gate_up[r, I + i] = w[r] grad_z SiLU(g)
+ *   grad_weights[r]        = sum_i grad_z SiLU(g) u      (fp32; NULL: not wanted)
+ * With the routing weight on the second product's input (y = (w z) W2, grad_z =
+ * dy W2^T) grad_weights is what moe_route_backward takes, row by routed item.
+ *  gate_up device bf16 [R, 2I] (gate first); z, grad_z bf16 [R, I]; row_weights fp32
+ *  [R] or NULL.  Infinite and NaN inputs give what the formulas do in fp32.
+ * grad_gate_up may be gate_up itself; no other overlap.  I a multiple of 8 up to
+ * 2^22, R < 2^31; bf16 tensors 16-byte aligned.
+ */
+GBMOE_API moe_status_t moe_swiglu(const void* gate_up, const float* row_weights, int64_t R,
+                                  int32_t I, void* z, moe_stream_t stream);
+GBMOE_API moe_status_t moe_swiglu_backward(const void* grad_z, const void* gate_up,
+                                           const float* row_weights, int64_t R, int32_t I,
+                                           void* grad_gate_up, float* grad_weights,
+                                           moe_stream_t stream);
+
+/* moe_quant_mx_fp4: MX FP4 (OCP Microscaling Formats) of z = x, or for swiglu = 1
+ * z = SiLU(x[:, :K]) * x[:, K:] in fp32, per row and block of 32 columns:
+ *   scale = 2^(floor(log2 max|z|) - 2), stored as its exponent + 127 (UE8M0), not
+ *           below 0; 255 (NaN) where z has a NaN or an infinity, the codes then 0
+ *   code  = E2M1 value nearest to z / scale, ties to even, magnitudes above 6 at 6
+ * For x these are exact; SiLU is as in moe_quant_groups_fp8, so that a z next to a
+ * border may take its neighbour.
+ *  x       device bf16 [M, K], or [M, 2K] for swiglu
+ *  q4      device uint8 [M, K / 2], written: column 2j in the low nibble of byte j
+ *  scale   device uint8 [M, K / 32], written
+ *  values  device bf16 [M, K] or NULL: the values that codes and scales stand for
+ *          (exact), as the gradients of a product in FP4 take them
+ * No output may overlap x.  K a multiple of 32 up to 2^22, M < 2^31; all 16-byte aligned.
+ */
+GBMOE_API moe_status_t moe_quant_mx_fp4(const void* x, int64_t M, int32_t K, int32_t swiglu,
+                                        void* q4, void* scale, void* values, moe_stream_t stream);
+
 /* ---------------------------------------------- weight-only quantised --
  * Expert weights stored quantised, activations bf16.  Defines: "fused_moe.py
  * 分析" (FlagDoc), "WNA16 路径" and "5. 特殊量化格式处理": int8 / int4

@@ -482,6 +482,85 @@ def moe_shared_expert_fp8(hidden: torch.Tensor, w13_q: torch.Tensor, w2_q: torch
                           error_word=error_word, stream=stream)
 
 
+_U8 = (torch.uint8,)
+
+
+def moe_swiglu(gate_up: torch.Tensor, row_weights: Optional[torch.Tensor] = None,
+               z: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """z = row_weights * SiLU(gate) * up: gate_up bf16 [R, 2I] (gate first),
+    row_weights fp32 [R] -> bf16 [R, I]."""
+    R, cols = _matrix(gate_up, "gate_up")
+    dev = gate_up.get_device()
+    if not (gate_up.dtype is torch.bfloat16 and gate_up.is_contiguous()):
+        _tensor(gate_up, "gate_up", _BF16, (R, cols), dev)
+    if cols % 2:
+        raise ValueError("gate_up needs an even number of columns")
+    if row_weights is not None:
+        _tensor(row_weights, "row_weights", _F32, (R,), dev)
+    z = _out(z, "z", torch.bfloat16, (R, cols // 2), dev, stream)
+    _call("moe_swiglu", dev, stream, gate_up.data_ptr(),
+          None if row_weights is None else row_weights.data_ptr(), R, cols // 2, z.data_ptr())
+    return z
+
+
+def moe_swiglu_backward(grad_z: torch.Tensor, gate_up: torch.Tensor,
+                        row_weights: Optional[torch.Tensor] = None,
+                        grad_gate_up: Optional[torch.Tensor] = None,
+                        grad_weights: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of moe_swiglu: grad_z bf16 [R, I], gate_up bf16 [R, 2I] ->
+    (grad_gate_up bf16 [R, 2I], grad_weights fp32 [R]; None without row_weights
+    unless the tensor is given).  Row by routed item, grad_weights is what
+    moe_route_backward takes.  grad_gate_up may be gate_up itself."""
+    R, cols = _matrix(gate_up, "gate_up")
+    dev = gate_up.get_device()
+    if cols % 2:
+        raise ValueError("gate_up needs an even number of columns")
+    try:
+        fine = (gate_up.dtype is torch.bfloat16 and gate_up.is_contiguous()
+                and grad_z.dtype is torch.bfloat16 and grad_z.shape == (R, cols // 2)
+                and grad_z.is_contiguous() and grad_z.get_device() == dev)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(gate_up, "gate_up", _BF16, (R, cols), dev)
+        _tensor(grad_z, "grad_z", _BF16, (R, cols // 2), dev)
+    if row_weights is not None:
+        _tensor(row_weights, "row_weights", _F32, (R,), dev)
+    grad_gate_up = _out(grad_gate_up, "grad_gate_up", torch.bfloat16, (R, cols), dev, stream)
+    if row_weights is not None or grad_weights is not None:
+        grad_weights = _out(grad_weights, "grad_weights", torch.float32, (R,), dev, stream)
+    _call("moe_swiglu_backward", dev, stream, grad_z.data_ptr(), gate_up.data_ptr(),
+          None if row_weights is None else row_weights.data_ptr(), R, cols // 2,
+          grad_gate_up.data_ptr(), None if grad_weights is None else grad_weights.data_ptr())
+    return grad_gate_up, grad_weights
+
+
+MX_BLOCK = 32
+
+
+def moe_quant_mx_fp4(x: torch.Tensor, swiglu: bool = False, q4: Optional[torch.Tensor] = None,
+                     scale: Optional[torch.Tensor] = None,
+                     values: Optional[torch.Tensor] = None, stream=None):
+    """MX FP4 of x bf16 [M, K] -> (codes uint8 [M, K/2], column 2j in the low
+    nibble of byte j; scales uint8 [M, K/32], UE8M0).  swiglu: x is [M, 2K], and
+    SiLU(x[:, :K]) * x[:, K:] is what is quantised.  values: bf16 [M, K] that
+    takes the values the codes and scales stand for."""
+    M, cols = _matrix(x, "x")
+    dev = x.get_device()
+    if not (x.dtype is torch.bfloat16 and x.is_contiguous()):
+        _tensor(x, "x", _BF16, (M, cols), dev)
+    if cols % (2 * MX_BLOCK if swiglu else MX_BLOCK):
+        raise ValueError(f"rows of {cols} columns are not whole blocks of {MX_BLOCK}")
+    K = cols // 2 if swiglu else cols
+    q4 = _out(q4, "q4", torch.uint8, (M, K // 2), dev, stream)
+    scale = _out(scale, "scale", torch.uint8, (M, K // MX_BLOCK), dev, stream)
+    if values is not None:
+        _tensor(values, "values", _BF16, (M, K), dev)
+    _call("moe_quant_mx_fp4", dev, stream, x.data_ptr(), M, K, int(bool(swiglu)), q4.data_ptr(),
+          scale.data_ptr(), None if values is None else values.data_ptr())
+    return q4, scale
+
+
 WQ_FORMATS = {"int4": 0, "int8": 1, "mxfp4": 2, "mxfp6_e3m2": 3, "mxfp6_e2m3": 4}
 
 
@@ -730,7 +809,8 @@ def profiler_stop():
 
 
 __all__ = ["moe_route", "moe_route_backward", "moe_quant_groups_fp8", "moe_matmul_fp8",
-           "moe_shared_expert_fp8", "moe_router_logits", "moe_layer", "moe_align", "moe_forward",
+           "moe_shared_expert_fp8", "moe_swiglu", "moe_swiglu_backward", "moe_quant_mx_fp4",
+           "moe_router_logits", "moe_layer", "moe_align", "moe_forward",
            "moe_forward_host", "HostStaging", "set_gather_mode", "set_pdl", "set_wq_decode",
            "set_item_rows", "set_host_out_direct", "set_small_path",
            "moe_forward_batched", "moe_forward_fp8", "workspace_size_fp8", "moe_quant_rows_fp8",

@@ -1156,6 +1156,66 @@ moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const void* w,
   return launch_matmul_fp8(g, stream);
 }
 
+// ------------------------------- products by expert, MX FP4, SiLU * up --
+moe_status_t moe_quant_mx_fp4(const void* x, int64_t M, int32_t K, int32_t swiglu, void* q4,
+                              void* scale, void* values, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (M < 0 || M >= (int64_t(1) << 31)) return set_error(MOE_ERR_INVALID_ARG, "M=%lld", (long long)M);
+  if (K < 32 || K % 32 != 0 || K > (1 << 22))
+    return set_error(MOE_ERR_INVALID_ARG, "K=%d not a positive multiple of 32 up to 2^22", K);
+  if (swiglu != 0 && swiglu != 1) return set_error(MOE_ERR_INVALID_ARG, "swiglu=%d", swiglu);
+  if (M == 0) return MOE_OK;
+  if (!x || !q4 || !scale) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(q4) || !aligned16(scale) || !aligned16(values))
+    return set_error(MOE_ERR_INVALID_ARG, "x, q4, scale and values must be 16-byte aligned");
+  int sms = 0;
+  if (moe_status_t st = check_device(&sms)) return st;
+  const QuantMxFp4Args a{static_cast<const bf16*>(x), M, K, swiglu, static_cast<uint8_t*>(q4),
+                         static_cast<uint8_t*>(scale), static_cast<bf16*>(values), sms};
+  return launch_quant_mx_fp4(a, stream);
+}
+
+namespace {
+moe_status_t validate_swiglu(int64_t R, int32_t I) {
+  if (R < 0 || R >= (int64_t(1) << 31)) return set_error(MOE_ERR_INVALID_ARG, "R=%lld", (long long)R);
+  if (I < 8 || I % 8 != 0 || I > (1 << 22))
+    return set_error(MOE_ERR_INVALID_ARG, "I=%d not a positive multiple of 8 up to 2^22", I);
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status_t moe_swiglu(const void* gate_up, const float* row_weights, int64_t R, int32_t I,
+                        void* z, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (moe_status_t st = validate_swiglu(R, I)) return st;
+  if (R == 0) return MOE_OK;
+  if (!gate_up || !z) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(gate_up) || !aligned16(z) || !aligned_to(row_weights, 4))
+    return set_error(MOE_ERR_INVALID_ARG, "gate_up and z must be 16-byte aligned");
+  int sms = 0;
+  if (moe_status_t st = check_device(&sms)) return st;
+  const SwigluArgs a{static_cast<const bf16*>(gate_up), row_weights, R, I, static_cast<bf16*>(z),
+                     sms};
+  return launch_swiglu(a, stream);
+}
+
+moe_status_t moe_swiglu_backward(const void* grad_z, const void* gate_up, const float* row_weights,
+                                 int64_t R, int32_t I, void* grad_gate_up, float* grad_weights,
+                                 moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (moe_status_t st = validate_swiglu(R, I)) return st;
+  if (R == 0) return MOE_OK;
+  if (!grad_z || !gate_up || !grad_gate_up) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(grad_z) || !aligned16(gate_up) || !aligned16(grad_gate_up) ||
+      !aligned_to(row_weights, 4) || !aligned_to(grad_weights, 4))
+    return set_error(MOE_ERR_INVALID_ARG,
+                     "grad_z, gate_up and grad_gate_up must be 16-byte aligned");
+  if (moe_status_t st = check_device(nullptr)) return st;
+  const SwigluBackwardArgs a{static_cast<const bf16*>(grad_z), static_cast<const bf16*>(gate_up),
+                             row_weights, R, I, static_cast<bf16*>(grad_gate_up), grad_weights};
+  return launch_swiglu_backward(a, stream);
+}
+
 // ------------------------------------------- weight-only quantised --
 namespace {
 moe_status_t validate_wq_format(int32_t format, int32_t G, const void* zero) {

@@ -162,6 +162,39 @@ struct MatmulFp8Args {
 };
 moe_status_t launch_matmul_fp8(const MatmulFp8Args& a, cudaStream_t s);
 
+// SiLU(gate) * up of routed rows and its gradient (swiglu.cu).
+struct SwigluArgs {
+  const bf16* gate_up;   // [R, 2I]
+  const float* weights;  // [R] or null (1)
+  int64_t R;
+  int32_t I;
+  bf16* z;               // [R, I]
+  int32_t num_sms;
+};
+moe_status_t launch_swiglu(const SwigluArgs& a, cudaStream_t s);
+struct SwigluBackwardArgs {
+  const bf16* dz;        // [R, I]
+  const bf16* gate_up;   // [R, 2I]
+  const float* weights;  // [R] or null (1)
+  int64_t R;
+  int32_t I;
+  bf16* d_gate_up;       // [R, 2I]
+  float* d_weights;      // [R] or null
+};
+moe_status_t launch_swiglu_backward(const SwigluBackwardArgs& a, cudaStream_t s);
+
+// MX FP4 codes (two per byte) and UE8M0 scales per 32 columns (mx_fp4.cu).
+struct QuantMxFp4Args {
+  const bf16* x;   // [M, K], or [M, 2K] for swiglu
+  int64_t M;
+  int32_t K, swiglu;
+  uint8_t* q4;     // [M, K / 2]
+  uint8_t* scale;  // [M, K / 32]
+  bf16* values;    // [M, K] or null
+  int32_t num_sms;
+};
+moe_status_t launch_quant_mx_fp4(const QuantMxFp4Args& a, cudaStream_t s);
+
 struct AlignArgs {
   const int32_t* ids;   // [R] expert id per item
   int64_t R;            // items

@@ -7,5 +7,7 @@ from .moe_oracle import *  # noqa: F401,F403
 from .moe_oracle import __all__ as _layer
 from .dense_oracle import *  # noqa: F401,F403
 from .dense_oracle import __all__ as _dense
+from .grouped_oracle import *  # noqa: F401,F403
+from .grouped_oracle import __all__ as _grouped
 
-__all__ = _layer + _dense
+__all__ = _layer + _dense + _grouped

@@ -1,0 +1,117 @@
+"""CPU tests of the products by expert, their gradients and MX FP4: the oracle
+against independent computations, and the refusals of the C ABI and of the
+binding."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_softmax_gb300 as pkg
+import oracle
+
+OK, INVALID, NO_DEVICE = 0, 1, 7
+
+
+# ------------------------------------------------------------- oracle pins --
+def test_oracle_grouped_matmul_and_gradients_by_autograd():
+    rng = np.random.default_rng(0)
+    offsets, K, N = [1, 4, 4, 9], 5, 3
+    x, w, b = rng.normal(size=(11, K)), rng.normal(size=(3, K, N)), rng.normal(size=(3, N))
+    y = oracle.grouped_matmul(x, w, offsets, np.full((11, N), 7.0), b)
+    assert (y[[0, 9, 10]] == 7).all()
+    tx, tw = torch.tensor(x, requires_grad=True), torch.tensor(w, requires_grad=True)
+    expert = torch.tensor([0, 0, 0, 2, 2, 2, 2, 2])
+    ty = torch.einsum("rk,rkn->rn", tx[1:9], tw[expert]) + torch.tensor(b)[expert]
+    np.testing.assert_allclose(y[1:9], ty.detach().numpy(), rtol=1e-12)
+    dy = rng.normal(size=(11, N))
+    (ty * torch.tensor(dy[1:9])).sum().backward()
+    np.testing.assert_allclose(oracle.grouped_weight_grad(x, dy, offsets), tw.grad.numpy(), rtol=1e-12)
+    dx = oracle.grouped_matmul(dy, w.transpose(0, 2, 1), offsets, np.zeros((11, K)))
+    np.testing.assert_allclose(dx, tx.grad.numpy(), rtol=1e-12)
+
+
+def test_oracle_swiglu_backward_by_differences():
+    """Central differences: error O(h^2) + O(eps / h)."""
+    rng = np.random.default_rng(1)
+    gu, dz, w, h = rng.normal(size=(3, 8)), rng.normal(size=(3, 4)), rng.normal(size=3), 1e-5
+    d, dw = oracle.swiglu_backward(dz, gu, w)
+    loss = lambda a, b: (oracle.swiglu(a, b) * dz).sum()  # noqa: E731
+    for i in np.ndindex(gu.shape):
+        e = np.zeros_like(gu)
+        e[i] = h
+        assert abs((loss(gu + e, w) - loss(gu - e, w)) / (2 * h) - d[i]) < 1e-8
+    for r in range(3):
+        e = np.zeros(3)
+        e[r] = h
+        assert abs((loss(gu, w + e) - loss(gu, w - e)) / (2 * h) - dw[r]) < 1e-8
+
+
+def test_oracle_mx_fp4_definition():
+    z = np.zeros((5, 32))
+    z[0, :10] = [6, 5, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25, -5, -0.25]      # ties, scale 1
+    z[1, :3] = [7.9, 4, 0.3]                                            # above 6: held at 6
+    z[2, 0] = 2.0 ** 20
+    z[3, 0], z[3, 1] = 2.0 ** -126, -2.0 ** -128                        # the scale's lower end
+    code, scale = oracle.quant_mx_fp4(z)
+    assert scale.ravel().tolist() == [127, 127, 145, 0, 0]
+    assert code[0, :10].tolist() == [7, 6, 6, 4, 4, 2, 2, 0, 14, 8]
+    assert code[1, :3].tolist() == [7, 6, 1]
+    assert code[2, 0] == 6 and code[3, :2].tolist() == [4, 9] and not code[4].any()
+    v = oracle.mx_fp4_values(oracle.pack_fp4(code), scale)
+    assert v[0, :10].tolist() == [6, 4, 4, 2, 2, 1, 1, 0, -4, 0]
+    assert v[2, 0] == 2.0 ** 20 and v[3, :2].tolist() == [2.0 ** -126, -2.0 ** -128]
+    # the library's weight-only decoding of the same codes
+    packed = oracle.pack_fp4(code)
+    assert np.array_equal(oracle.unpack_nibbles(packed), code)
+
+
+# --------------------------------------------------------- C ABI refusals --
+def _p(v=4096):
+    return ctypes.c_void_p(v)
+
+
+def test_swiglu_and_quant_refusals():
+    lib, p, odd = pkg.lib(), _p(), _p(4104)
+    fwd = lambda R=4, I=64, gu=p, w=None, z=p: lib.moe_swiglu(gu, w, R, I, z, None)  # noqa: E731
+    bwd = lambda R=4, I=64, dz=p, gu=p, w=None, d=p, dw=None: lib.moe_swiglu_backward(  # noqa: E731
+        dz, gu, w, R, I, d, dw, None)
+    for call in (fwd, bwd):
+        assert call(R=-1) == INVALID and call(R=1 << 31) == INVALID
+        assert call(I=0) == INVALID and call(I=12) == INVALID and call(I=(1 << 22) + 8) == INVALID
+        assert call(gu=None) == INVALID and call(gu=odd) == INVALID and call(w=_p(4098)) == INVALID
+        assert call(R=0) == OK
+    assert fwd(z=None) == INVALID and fwd(z=odd) == INVALID
+    assert bwd(dz=None) == INVALID and bwd(d=odd) == INVALID and bwd(dw=_p(4098)) == INVALID
+
+    def quant(M=4, K=64, s=0, x=p, q=p, sc=p, v=None):
+        return lib.moe_quant_mx_fp4(x, M, K, s, q, sc, v, None)
+    assert quant(M=-1) == INVALID and quant(M=1 << 31) == INVALID
+    assert quant(K=0) == INVALID and quant(K=48) == INVALID and quant(K=(1 << 22) + 32) == INVALID
+    assert quant(s=2) == INVALID
+    assert quant(x=None) == INVALID and quant(q=odd) == INVALID and quant(sc=odd) == INVALID
+    assert quant(v=odd) == INVALID
+    assert quant(M=0) == OK
+
+
+# --------------------------------------------------------- binding refusals --
+def _raises(text, f, *a, **k):
+    with pytest.raises(ValueError, match=text):
+        f(*a, **k)
+
+
+def test_binding_refusals_of_swiglu_and_quant():
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    _raises("even number", pkg.moe_swiglu, bf(4, 33))
+    _raises("row_weights has shape", pkg.moe_swiglu, bf(4, 32), torch.zeros(3))
+    _raises("CUDA device", pkg.moe_swiglu, bf(4, 32))
+    _raises("grad_z has shape", pkg.moe_swiglu_backward, bf(4, 32), bf(4, 32))
+    _raises("grad_weights has shape", pkg.moe_swiglu_backward, bf(4, 16), bf(4, 32),
+            grad_weights=torch.zeros(4, 1))
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    q = pkg.moe_quant_mx_fp4
+    _raises("whole blocks", q, bf(4, 48))
+    _raises("whole blocks", q, bf(4, 96), swiglu=True)
+    _raises("q4 has shape", q, bf(4, 64), q4=u8(4, 31))
+    _raises("values must", q, bf(4, 64), values=torch.zeros(4, 64))
+    _raises("CUDA device", q, bf(4, 64))
