@@ -503,7 +503,65 @@ GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const
                                       moe_stream_t stream);
 
 /* ---------------------------- products of rows sorted by expert, MX FP4 --
- * moe_swiglu: z[r, i] = w[r] SiLU(gate_up[r, i]) gate_up[r, I + i], rounded once
+ * The parts of the experts' forward and backward passes, for callers that keep
+ * what lies between them: rows sorted by expert (as moe_align with block_m = 1
+ * orders the routed items), row r of expert e where
+ *   expert_offsets[e] <= r < expert_offsets[e + 1].
+ *  expert_offsets  device int32 [E + 1], ascending from >= 0 to <= R; experts
+ *                  may have no rows.  Rows of x outside all groups take no part;
+ *                  rows of out outside all groups are not written.  Offsets that
+ *                  descend or leave 0..R are clipped to it and set the error word to
+ *                  MOE_ERR_INVALID_ARG (what the rows then hold is not defined, but
+ *                  nothing outside the tensors is read or written).
+ *  error_word      device int32 or NULL; also MOE_ERR_TIMEOUT if a pipeline wait ran
+ *                  out of time (the output is then incomplete)
+ * Results do not depend on timing.  out must not overlap the inputs; operands, bias,
+ * scales and out 16-byte aligned.  Limits: E <= 1024, R <= 2^31 - 1024, K and N up to
+ * 2^22, R * N <= 2^44, E ceil(K/256) ceil(N/256) < 2^30.
+ *
+ * moe_grouped_matmul: out[r, n] = sum_k x[r, k] W[e][k, n] + bias[e, n].
+ *  x     device bf16 [R, K]
+ *  w     w_transposed = 0: device bf16 [E, K, N], the orientation of w13 and w2;
+ *        1: [E, N, K].  One stored weight so serves y = x W and dx = dy W^T.
+ *  bias  device bf16 [E, N] or NULL
+ *  out   device bf16 [R, N], or fp32 with out_f32 = 1 (sums rounded to nearest at
+ *        least every 512 of K)
+ * K and N multiples of 8.
+ */
+GBMOE_API moe_status_t moe_grouped_matmul(const void* x, const void* w,
+                                          const int32_t* expert_offsets, int32_t w_transposed,
+                                          const void* bias, int64_t R, int32_t E, int32_t K,
+                                          int32_t N, int32_t out_f32, void* out,
+                                          int32_t* error_word, moe_stream_t stream);
+
+/* moe_grouped_weight_grad: out[e, k, n] = sum over expert e's rows of
+ * x[r, k] dy[r, n], plus what out held with accumulate = 1; zeros (or what it
+ * held) for an expert without rows.  For a weight stored as [E, N, K], exchange x
+ * and dy.
+ *  x, dy  device bf16 [R, K], [R, N];  out  device bf16 or fp32 [E, K, N]
+ * K and N multiples of 8; also R * K <= 2^44.
+ */
+GBMOE_API moe_status_t moe_grouped_weight_grad(const void* x, const void* dy,
+                                               const int32_t* expert_offsets, int64_t R, int32_t E,
+                                               int32_t K, int32_t N, int32_t out_f32,
+                                               int32_t accumulate, void* out, int32_t* error_word,
+                                               moe_stream_t stream);
+
+/* moe_matmul_fp4: out[r, n] = sum_b 2^(a_scale[r, b] - 127) 2^(w_scale[e, n, b] - 127)
+ * (sum over k in block b of a[r, k] w[e, n, k]), blocks of 32, on the tensor cores'
+ * MX FP4 path.
+ *  a         device uint8 [R, K / 2], a_scale uint8 [R, K / 32] (moe_quant_mx_fp4)
+ *  w         device uint8 [E, N, K / 2], w_scale uint8 [E, N, K / 32]: rows of K
+ *  expert_offsets  as above, or NULL for one dense weight (E = 1, all R rows)
+ *  out       device bf16 [R, N], or fp32 with out_f32 = 1
+ * A scale of 255 makes NaN of what it takes part in.  K a multiple of 32, N of 8.
+ */
+GBMOE_API moe_status_t moe_matmul_fp4(const void* a, const void* a_scale, const void* w,
+                                      const void* w_scale, const int32_t* expert_offsets,
+                                      int64_t R, int32_t E, int32_t K, int32_t N, int32_t out_f32,
+                                      void* out, int32_t* error_word, moe_stream_t stream);
+
+/* moe_swiglu: z[r, i] = w[r] SiLU(gate_up[r, i]) gate_up[r, I + i], rounded once
  * from fp32 (w = 1 for row_weights = NULL).  moe_swiglu_backward, from grad_z =
  * dL/dz and with g, u, sig(g) = 1 / (1 + e^-g):
  *   grad_gate_up[r, i]     = w[r] grad_z u sig(g) (1 + g (1 - sig(g)))

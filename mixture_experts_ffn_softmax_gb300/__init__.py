@@ -485,6 +485,103 @@ def moe_shared_expert_fp8(hidden: torch.Tensor, w13_q: torch.Tensor, w2_q: torch
 _U8 = (torch.uint8,)
 
 
+def _stack(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-dimensional tensor")
+    shape = t.shape
+    if max(shape) >= 1 << 31:
+        raise ValueError(f"{name} has shape {tuple(shape)}: sizes are below 2^31")
+    return shape
+
+
+def moe_grouped_matmul(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, transposed: bool = False,
+                       out_dtype: torch.dtype = torch.bfloat16,
+                       out: Optional[torch.Tensor] = None,
+                       error_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Product of rows sorted by expert with their expert's weight: x bf16
+    [R, K], w bf16 [E, K, N] (transposed: [E, N, K]) -> [R, N] in out_dtype (bf16
+    or fp32; `out` decides where given).  Expert e's rows are
+    expert_offsets[e]..expert_offsets[e + 1] (int32 [E + 1], as moe_align with
+    block_m=1 gives them with the order of the items); other rows of the output
+    are not written.  bias bf16 [E, N]."""
+    R, K = _matrix(x, "x")
+    E, rows, cols = _stack(w, "w")
+    N = rows if transposed else cols
+    dev = x.get_device()
+    try:
+        fine = (x.dtype is torch.bfloat16 and x.is_contiguous() and w.dtype is torch.bfloat16
+                and w.is_contiguous() and (cols if transposed else rows) == K
+                and w.get_device() == dev and expert_offsets.dtype is torch.int32
+                and expert_offsets.shape == (E + 1,) and expert_offsets.is_contiguous()
+                and expert_offsets.get_device() == dev)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(x, "x", _BF16, (R, K), dev)
+        _tensor(w, "w", _BF16, (E, N, K) if transposed else (E, K, N), dev)
+        _tensor(expert_offsets, "expert_offsets", _I32, (E + 1,), dev)
+    if bias is not None:
+        _tensor(bias, "bias", _BF16, (E, N), dev)
+    if error_word is not None:
+        _tensor(error_word, "error_word", _I32, (1,), dev)
+    if out is not None:
+        out_dtype = getattr(out, "dtype", None)
+    if out_dtype not in _LOGITS:
+        raise ValueError("the output is torch.bfloat16 or torch.float32")
+    out = _out(out, "out", out_dtype, (R, N), dev, stream)
+    _call("moe_grouped_matmul", dev, stream, x.data_ptr(), w.data_ptr(),
+          expert_offsets.data_ptr(), int(bool(transposed)),
+          None if bias is None else bias.data_ptr(), R, E, K, N,
+          int(out_dtype == torch.float32), out.data_ptr(),
+          None if error_word is None else error_word.data_ptr())
+    return out
+
+
+def moe_grouped_weight_grad(x: torch.Tensor, dy: torch.Tensor, expert_offsets: torch.Tensor,
+                            out_dtype: torch.dtype = torch.float32, accumulate: bool = False,
+                            out: Optional[torch.Tensor] = None,
+                            error_word: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """Gradient of moe_grouped_matmul's weight: x bf16 [R, K], dy bf16 [R, N],
+    rows sorted by expert -> [E, K, N] in out_dtype (fp32 or bf16; `out` decides
+    where given), x_e^T dy_e over each expert's rows, zeros for an expert without
+    any.  accumulate: added to what `out` holds.  For weights stored as [E, N, K]
+    exchange x and dy."""
+    R, K = _matrix(x, "x")
+    N = _matrix(dy, "dy")[1]
+    dev = x.get_device()
+    try:
+        fine = (x.dtype is torch.bfloat16 and x.is_contiguous() and dy.dtype is torch.bfloat16
+                and dy.is_contiguous() and dy.shape[0] == R and dy.get_device() == dev
+                and expert_offsets.dtype is torch.int32 and expert_offsets.dim() == 1
+                and expert_offsets.is_contiguous() and expert_offsets.get_device() == dev)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(x, "x", _BF16, (R, K), dev)
+        _tensor(dy, "dy", _BF16, (R, N), dev)
+        size = expert_offsets.numel() if isinstance(expert_offsets, torch.Tensor) else 1
+        _tensor(expert_offsets, "expert_offsets", _I32, (size,), dev)
+    E = expert_offsets.shape[0] - 1
+    if E < 1:
+        raise ValueError("expert_offsets has at least two entries")
+    if error_word is not None:
+        _tensor(error_word, "error_word", _I32, (1,), dev)
+    if out is not None:
+        out_dtype = getattr(out, "dtype", None)
+    elif accumulate:
+        raise ValueError("accumulate needs `out`")
+    if out_dtype not in _LOGITS:
+        raise ValueError("the output is torch.bfloat16 or torch.float32")
+    out = _out(out, "out", out_dtype, (E, K, N), dev, stream)
+    _call("moe_grouped_weight_grad", dev, stream, x.data_ptr(), dy.data_ptr(),
+          expert_offsets.data_ptr(), R, E, K, N, int(out_dtype == torch.float32),
+          int(bool(accumulate)), out.data_ptr(),
+          None if error_word is None else error_word.data_ptr())
+    return out
+
+
 def moe_swiglu(gate_up: torch.Tensor, row_weights: Optional[torch.Tensor] = None,
                z: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """z = row_weights * SiLU(gate) * up: gate_up bf16 [R, 2I] (gate first),
@@ -559,6 +656,56 @@ def moe_quant_mx_fp4(x: torch.Tensor, swiglu: bool = False, q4: Optional[torch.T
     _call("moe_quant_mx_fp4", dev, stream, x.data_ptr(), M, K, int(bool(swiglu)), q4.data_ptr(),
           scale.data_ptr(), None if values is None else values.data_ptr())
     return q4, scale
+
+
+def moe_matmul_fp4(a_q: torch.Tensor, a_scale: torch.Tensor, w_q: torch.Tensor,
+                   w_scale: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None,
+                   out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                   error_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Product of MX FP4 matrices -> [R, N] in out_dtype (bf16 or fp32; `out`
+    decides where given).  a_q uint8 [R, K/2] with a_scale uint8 [R, K/32]
+    (moe_quant_mx_fp4); w_q uint8 [N, K/2] with w_scale [N, K/32], or with
+    expert_offsets [E, N, K/2] and [E, N, K/32], rows as in moe_grouped_matmul."""
+    R, half = _matrix(a_q, "a_q")
+    dev = a_q.get_device()
+    if expert_offsets is None:
+        E, N = 1, _matrix(w_q, "w_q")[0]
+        lead = (N,)
+    else:
+        E, N, _ = _stack(w_q, "w_q")
+        lead = (E, N)
+    groups = half // (MX_BLOCK // 2)
+    try:
+        fine = (a_q.dtype is torch.uint8 and a_q.is_contiguous()
+                and a_scale.dtype is torch.uint8 and a_scale.shape == (R, groups)
+                and a_scale.is_contiguous() and a_scale.get_device() == dev
+                and w_q.dtype is torch.uint8 and w_q.shape[-1] == half and w_q.is_contiguous()
+                and w_q.get_device() == dev and w_scale.dtype is torch.uint8
+                and w_scale.shape == (*lead, groups) and w_scale.is_contiguous()
+                and w_scale.get_device() == dev)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(a_q, "a_q", _U8, (R, half), dev)
+        _tensor(a_scale, "a_scale", _U8, (R, groups), dev)
+        _tensor(w_q, "w_q", _U8, (*lead, half), dev)
+        _tensor(w_scale, "w_scale", _U8, (*lead, groups), dev)
+    if half % (MX_BLOCK // 2):
+        raise ValueError(f"rows of {2 * half} codes are not whole blocks of {MX_BLOCK}")
+    if expert_offsets is not None:
+        _tensor(expert_offsets, "expert_offsets", _I32, (E + 1,), dev)
+    if error_word is not None:
+        _tensor(error_word, "error_word", _I32, (1,), dev)
+    if out is not None:
+        out_dtype = getattr(out, "dtype", None)
+    if out_dtype not in _LOGITS:
+        raise ValueError("the output is torch.bfloat16 or torch.float32")
+    out = _out(out, "out", out_dtype, (R, N), dev, stream)
+    _call("moe_matmul_fp4", dev, stream, a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(),
+          w_scale.data_ptr(), None if expert_offsets is None else expert_offsets.data_ptr(), R, E,
+          2 * half, N, int(out_dtype == torch.float32), out.data_ptr(),
+          None if error_word is None else error_word.data_ptr())
+    return out
 
 
 WQ_FORMATS = {"int4": 0, "int8": 1, "mxfp4": 2, "mxfp6_e3m2": 3, "mxfp6_e2m3": 4}
@@ -809,7 +956,8 @@ def profiler_stop():
 
 
 __all__ = ["moe_route", "moe_route_backward", "moe_quant_groups_fp8", "moe_matmul_fp8",
-           "moe_shared_expert_fp8", "moe_swiglu", "moe_swiglu_backward", "moe_quant_mx_fp4",
+           "moe_shared_expert_fp8", "moe_grouped_matmul", "moe_grouped_weight_grad", "moe_swiglu",
+           "moe_swiglu_backward", "moe_quant_mx_fp4", "moe_matmul_fp4",
            "moe_router_logits", "moe_layer", "moe_align", "moe_forward",
            "moe_forward_host", "HostStaging", "set_gather_mode", "set_pdl", "set_wq_decode",
            "set_item_rows", "set_host_out_direct", "set_small_path",

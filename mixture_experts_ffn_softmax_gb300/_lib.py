@@ -65,6 +65,12 @@ SIGNATURES = {
     "moe_quant_groups_fp8": (c_i32, [c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp]),
     "moe_matmul_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32,
                                c_vp, c_vp, c_vp]),
+    "moe_grouped_matmul": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_vp, c_i64, c_i32, c_i32, c_i32,
+                                   c_i32, c_vp, c_vp, c_vp]),
+    "moe_grouped_weight_grad": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_i32,
+                                        c_i32, c_vp, c_vp, c_vp]),
+    "moe_matmul_fp4": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_i32,
+                               c_vp, c_vp, c_vp]),
     "moe_swiglu": (c_i32, [c_vp, c_vp, c_i64, c_i32, c_vp, c_vp]),
     "moe_swiglu_backward": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp]),
     "moe_quant_mx_fp4": (c_i32, [c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]),

@@ -1157,6 +1157,100 @@ moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const void* w,
 }
 
 // ------------------------------- products by expert, MX FP4, SiLU * up --
+namespace {
+// What the grouped products share: rows, experts and the sizes of the weight.
+moe_status_t validate_grouped(int64_t R, int32_t E, int32_t K, int32_t N, int32_t k_unit,
+                              int32_t out_f32) {
+  if (R < 0 || R > (int64_t(1) << 31) - 1024)
+    return set_error(MOE_ERR_INVALID_ARG, "R=%lld not in 0..2^31 - 1024", (long long)R);
+  if (E < 1 || E > 1024) return set_error(MOE_ERR_INVALID_ARG, "E=%d not in 1..1024", E);
+  if (K < k_unit || K % k_unit != 0 || K > (1 << 22))
+    return set_error(MOE_ERR_INVALID_ARG, "K=%d not a positive multiple of %d up to 2^22", K, k_unit);
+  if (N < 8 || N % 8 != 0 || N > (1 << 22))
+    return set_error(MOE_ERR_INVALID_ARG, "N=%d not a positive multiple of 8 up to 2^22", N);
+  if (out_f32 != 0 && out_f32 != 1) return set_error(MOE_ERR_INVALID_ARG, "out_f32=%d", out_f32);
+  // (tiles of the output are counted in 32 bits)
+  if (R > (int64_t(1) << 44) / N)
+    return set_error(MOE_ERR_INVALID_ARG, "R=%lld times N=%d above 2^44", (long long)R, N);
+  if (int64_t(E) * ceil_div(K, 256) * ceil_div(N, 256) >= (int64_t(1) << 30))
+    return set_error(MOE_ERR_INVALID_ARG, "E=%d weights of %d x %d are too many tiles", E, K, N);
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status_t moe_grouped_matmul(const void* x, const void* w, const int32_t* expert_offsets,
+                                int32_t w_transposed, const void* bias, int64_t R, int32_t E,
+                                int32_t K, int32_t N, int32_t out_f32, void* out,
+                                int32_t* error_word, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (moe_status_t st = validate_grouped(R, E, K, N, 8, out_f32)) return st;
+  if (w_transposed != 0 && w_transposed != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "w_transposed=%d", w_transposed);
+  if (R == 0) return MOE_OK;
+  if (!x || !w || !expert_offsets || !out) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(out) || (bias && !aligned16(bias)) ||
+      !aligned_to(expert_offsets, 4) || !aligned_to(error_word, 4))
+    return set_error(MOE_ERR_INVALID_ARG,
+                     "x, w, bias and out must be 16-byte aligned, expert_offsets to 4 bytes");
+  int sms = 0;
+  if (moe_status_t st = check_device(&sms)) return st;
+  const GroupedProductArgs a{x, w, expert_offsets, static_cast<const bf16*>(bias), nullptr, nullptr,
+                             R, E, K, N, w_transposed, out_f32, 0, out, error_word, sms};
+  return launch_grouped_matmul(a, stream);
+}
+
+moe_status_t moe_grouped_weight_grad(const void* x, const void* dy, const int32_t* expert_offsets,
+                                     int64_t R, int32_t E, int32_t K, int32_t N, int32_t out_f32,
+                                     int32_t accumulate, void* out, int32_t* error_word,
+                                     moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (moe_status_t st = validate_grouped(R, E, K, N, 8, out_f32)) return st;
+  if (accumulate != 0 && accumulate != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "accumulate=%d", accumulate);
+  if (R > (int64_t(1) << 44) / K)
+    return set_error(MOE_ERR_INVALID_ARG, "R=%lld times K=%d above 2^44", (long long)R, K);
+  if (!out || (R > 0 && (!x || !dy || !expert_offsets)))
+    return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(dy) || !aligned16(out) || !aligned_to(expert_offsets, 4) ||
+      !aligned_to(error_word, 4))
+    return set_error(MOE_ERR_INVALID_ARG,
+                     "x, dy and out must be 16-byte aligned, expert_offsets to 4 bytes");
+  int sms = 0;
+  if (moe_status_t st = check_device(&sms)) return st;
+  if (R == 0) {  // no expert has rows: the gradients are zeros
+    if (!accumulate &&
+        cudaMemsetAsync(out, 0, size_t(E) * K * N * (out_f32 ? 4 : 2), stream) != cudaSuccess)
+      return set_error(MOE_ERR_CUDA, "grouped_weight_grad: %s",
+                       cudaGetErrorString(cudaGetLastError()));
+    return MOE_OK;
+  }
+  const GroupedProductArgs a{x, dy, expert_offsets, nullptr, nullptr, nullptr, R, E, K, N, 0,
+                             out_f32, accumulate, out, error_word, sms};
+  return launch_grouped_weight_grad(a, stream);
+}
+
+moe_status_t moe_matmul_fp4(const void* a, const void* a_scale, const void* w, const void* w_scale,
+                            const int32_t* expert_offsets, int64_t R, int32_t E, int32_t K,
+                            int32_t N, int32_t out_f32, void* out, int32_t* error_word,
+                            moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (moe_status_t st = validate_grouped(R, E, K, N, 32, out_f32)) return st;
+  if (!expert_offsets && E != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "E=%d without expert_offsets", E);
+  if (R == 0) return MOE_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out) || !aligned16(a_scale) ||
+      !aligned16(w_scale) || !aligned_to(expert_offsets, 4) || !aligned_to(error_word, 4))
+    return set_error(MOE_ERR_INVALID_ARG,
+                     "codes, scales and out must be 16-byte aligned, expert_offsets to 4 bytes");
+  int sms = 0;
+  if (moe_status_t st = check_device(&sms)) return st;
+  const GroupedProductArgs g{a, w, expert_offsets, nullptr, static_cast<const uint8_t*>(a_scale),
+                             static_cast<const uint8_t*>(w_scale), R, E, K, N, 1, out_f32, 0, out,
+                             error_word, sms};
+  return launch_matmul_fp4(g, stream);
+}
+
 moe_status_t moe_quant_mx_fp4(const void* x, int64_t M, int32_t K, int32_t swiglu, void* q4,
                               void* scale, void* values, moe_stream_t stream) {
   g_detail[0] = 0;

@@ -195,6 +195,26 @@ struct QuantMxFp4Args {
 };
 moe_status_t launch_quant_mx_fp4(const QuantMxFp4Args& a, cudaStream_t s);
 
+// Products of rows sorted by expert, their weight gradients and the MX FP4
+// product (grouped.cu).
+struct GroupedProductArgs {
+  const void* x;           // bf16 [R, K]; FP4: codes [R, K / 2]
+  const void* w;           // bf16 [E, K, N] or transposed [E, N, K]; FP4: codes [E, N, K / 2];
+                           // weight gradient: dy bf16 [R, N]
+  const int32_t* offsets;  // [E + 1] or null (E = 1, all rows)
+  const bf16* bias;        // [E, N] or null
+  const uint8_t* x_scale;  // FP4: [R, K / 32]
+  const uint8_t* w_scale;  // FP4: [E, N, K / 32]
+  int64_t R;
+  int32_t E, K, N, transposed, out_f32, accumulate;
+  void* out;               // bf16 or fp32 [R, N]; weight gradient: [E, K, N]
+  int32_t* error_word;
+  int32_t num_sms;
+};
+moe_status_t launch_grouped_matmul(const GroupedProductArgs& a, cudaStream_t s);
+moe_status_t launch_grouped_weight_grad(const GroupedProductArgs& a, cudaStream_t s);
+moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s);
+
 struct AlignArgs {
   const int32_t* ids;   // [R] expert id per item
   int64_t R;            // items

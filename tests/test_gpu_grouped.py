@@ -1,0 +1,365 @@
+"""GPU parity of the products of rows sorted by expert and their weight
+gradients: bit-exact on integers whose sums are exact, within rounding bounds
+otherwise; and the training step of a layer made of them."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_softmax_gb300 as pkg
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+U16, U32 = 2.0 ** -8, 2.0 ** -24        # half a step, relative
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def ints(seed, *shape, top=2):
+    """bf16 integers in -top..top: sums of up to 2^24 / top^2 products are exact."""
+    return torch.randint(-top, top + 1, shape, generator=gen(seed), device="cuda").to(BF16)
+
+
+def offsets_of(counts, first=0):
+    return torch.tensor([first, *(first + np.cumsum(counts))], dtype=torch.int32, device="cuda")
+
+
+def reference(x, w, offsets, out, transposed=False, bias=None):
+    y = out.double().clone()
+    o = offsets.tolist()
+    for e, (a, b) in enumerate(zip(o, o[1:])):
+        m = w[e].double()
+        y[a:b] = x[a:b].double() @ (m.t() if transposed else m)
+        if bias is not None:
+            y[a:b] += bias[e].double()
+    return y.to(out.dtype)
+
+
+def weight_reference(x, dy, offsets):
+    o = offsets.tolist()
+    return torch.stack([x[a:b].double().t() @ dy[a:b].double() for a, b in zip(o, o[1:])])
+
+
+# no rows, one, either side of what the MMA and a tile take, many experts, one with all rows
+COUNTS = [[1], [0, 3, 0], [31, 32, 33, 1, 0, 16], [255, 256, 257], [0, 0, 1000, 5, 0],
+          [300, 1, 513], [3] * 70, [0] * 40 + [7]]
+SIZES = [(8, 8), (64, 64), (72, 256), (136, 264), (520, 136), (1000, 520)]
+
+
+# ------------------------------------------------------------------ product --
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("K,N", SIZES)
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{max(c)}")
+def test_product_exact(counts, K, N, transposed):
+    """Rows that belong to nobody, before and behind the groups, hold NaN and
+    are not written; both output types; with and without a bias."""
+    E, R = len(counts), sum(counts) + 5
+    off = offsets_of(counts, 2)
+    x = ints(1, R, K)
+    x[:2], x[-3:] = float("nan"), float("nan")
+    w = ints(2, E, N, K) if transposed else ints(2, E, K, N)
+    bias = ints(3, E, N)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt, b in ((BF16, None), (F32, bias)):
+        out = torch.full((R, N), 7.0, device="cuda", dtype=dt)
+        got = pkg.moe_grouped_matmul(x, w, off, bias=b, transposed=transposed, out=out,
+                                     error_word=err)
+        assert got is out
+        ref = reference(x, w, off, torch.full_like(out, 7.0), transposed, b)
+        assert torch.equal(out, ref)
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("K,N,counts", [(4096, 512, [700, 0, 90]), (14336, 256, [20, 12]),
+                                        (520, 264, [33, 1, 300])])
+def test_product_within_rounding(K, N, counts, dtype):
+    """fp32 sums: an MMA adds 16 products, whose sum and addition each drop at
+    most 2^-23 of what is there (truncation, twice the rounding's half step);
+    in fp32 outputs at most 32 such additions follow one another before the sum
+    is added in a register with 2^-24."""
+    x = torch.randn(sum(counts), K, generator=gen(K), device="cuda").to(BF16)
+    w = (torch.randn(len(counts), K, N, generator=gen(N), device="cuda") * 0.02).to(BF16)
+    off = offsets_of(counts)
+    y = pkg.moe_grouped_matmul(x, w, off, out_dtype=dtype).double()
+    z = torch.zeros(len(x), N, device="cuda", dtype=torch.float64)
+    ref, size = reference(x, w, off, z), reference(x.abs(), w.abs(), off, z)
+    adds = 2 * K / 16 if dtype is BF16 else 2 * 32 + K / 512
+    half = U16 if dtype is BF16 else U32
+    assert ((y - ref).abs() <= half * ref.abs() * (1 + 1e-3) + (adds + 2) * 2 * U32 * size).all()
+    if dtype is F32:
+        # the additions' truncation has one sign; 1.0e-9 of the sum per K without the registers
+        assert ((y - ref).norm() / ref.norm()).item() < 1e-6
+
+
+def test_product_of_many_experts_and_ragged_rows():
+    rng = np.random.default_rng(0)
+    counts = rng.integers(0, 9, 1024) * (rng.random(1024) < 0.4)
+    counts[[0, 511, 1023]] = 300, 0, 1
+    x, w, off = ints(4, int(counts.sum()), 64), ints(5, 1024, 64, 72), offsets_of(counts)
+    out = torch.zeros(len(x), 72, device="cuda")
+    assert torch.equal(pkg.moe_grouped_matmul(x, w, off, out=out), reference(x, w, off, out * 0))
+
+
+def test_product_rows_do_not_touch_each_other():
+    """A row's NaN or infinity stays in its own output row, an expert's weight in
+    its own rows."""
+    x, w, off = ints(6, 90, 128), ints(7, 3, 128, 64), offsets_of([40, 10, 40])
+    y = pkg.moe_grouped_matmul(x, w, off)
+    x2, w2 = x.clone(), w.clone()
+    x2[41, 3], x2[0, 0] = float("nan"), float("inf")
+    w2[1, 5, 7] = float("inf")
+    y2 = pkg.moe_grouped_matmul(x2, w2, off)
+    assert torch.isnan(y2[41]).all() and not torch.isfinite(y2[0]).any()  # inf * 0 is NaN
+    rows = [r for r in range(90) if r not in (0, 41)]
+    cols = [c for c in range(64) if c != 7]
+    assert torch.equal(y2[rows][:, cols], y[rows][:, cols])
+    assert torch.equal(y2[1:40], y[1:40]) and torch.equal(y2[50:], y[50:])
+
+
+def test_product_same_rows_in_any_company():
+    """A row's result does not depend on the rows beside it (as a padded batch
+    and its unpadded form have to agree)."""
+    w = torch.randn(1, 256, 264, generator=gen(8), device="cuda").to(BF16)
+    x = torch.randn(700, 256, generator=gen(9), device="cuda").to(BF16)
+    full = pkg.moe_grouped_matmul(x, w, offsets_of([700]))
+    for n in (1, 33, 256, 511):
+        assert torch.equal(pkg.moe_grouped_matmul(x[:n].clone(), w, offsets_of([n])), full[:n])
+
+
+def test_empty_calls():
+    w, off = ints(1, 2, 64, 32), offsets_of([0, 0])
+    assert pkg.moe_grouped_matmul(ints(2, 0, 64), w, off).shape == (0, 32)
+    out = torch.full((2, 64, 32), 5.0, device="cuda")
+    pkg.moe_grouped_weight_grad(ints(2, 0, 64), ints(3, 0, 32), off, out=out, accumulate=True)
+    assert (out == 5).all()
+    pkg.moe_grouped_weight_grad(ints(2, 0, 64), ints(3, 0, 32), off, out=out)
+    assert (out == 0).all()
+    rest = pkg.moe_grouped_matmul(ints(2, 4, 64), w, off, out=torch.full((4, 32), 3.0, device="cuda"))
+    assert (rest == 3).all()
+
+
+@pytest.mark.parametrize("bad", [[0, 5, 3, 8], [-2, 3, 4, 8], [0, 3, 4, 9], [4, 3, 2, 1]])
+def test_offsets_out_of_order_or_range_set_the_error_word(bad):
+    x, w, dy = ints(1, 8, 64), ints(2, 3, 64, 32), ints(3, 8, 32)
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    guard = torch.full((3, 8, 32), 7.0, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkg.moe_grouped_matmul(x, w, off, out=guard[1], error_word=err)
+    assert err.item() == 1 and (guard[0] == 7).all() and (guard[2] == 7).all()
+    err.zero_()
+    pkg.moe_grouped_weight_grad(x, dy, off, error_word=err)
+    assert err.item() == 1
+
+
+# ---------------------------------------------------------- weight gradient --
+@pytest.mark.parametrize("K,N", [(8, 8), (64, 136), (136, 64), (264, 264), (520, 8)])
+@pytest.mark.parametrize("counts", [[1], [0, 15, 16, 17], [63, 64, 65, 0, 1], [200, 0, 448, 33],
+                                    [3] * 70, [1000]], ids=lambda c: f"{len(c)}x{max(c)}")
+def test_weight_grad_exact(counts, K, N):
+    """Rows of nobody hold NaN, as do x and dy of other experts' rows in turn:
+    neither reaches an expert's sum."""
+    E, R = len(counts), sum(counts) + 5
+    off = offsets_of(counts, 2)
+    x, dy = ints(1, R, K), ints(2, R, N)
+    for t in (x, dy):
+        t[:2], t[-3:] = float("nan"), float("inf")
+    ref = weight_reference(x, dy, off)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (F32, BF16):
+        out = torch.full((E, K, N), 9.0, device="cuda", dtype=dt)
+        pkg.moe_grouped_weight_grad(x, dy, off, out=out, error_word=err)
+        assert torch.equal(out, ref.to(dt))
+        pkg.moe_grouped_weight_grad(x, dy, off, out=out, accumulate=True, error_word=err)
+        assert torch.equal(out, (ref.to(dt).double() + ref).to(dt))
+    o = off.tolist()
+    for e in range(0, E, max(1, E // 3)):
+        if counts[e]:
+            x2, dy2 = x.clone(), dy.clone()
+            x2[o[e]:o[e + 1]], dy2[o[e + 1] - 1] = float("nan"), float("inf")
+            got = pkg.moe_grouped_weight_grad(x2, dy2, off)
+            others = [i for i in range(E) if i != e]
+            assert torch.isnan(got[e]).all() and torch.equal(got[others].double(), ref[others])
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_weight_grad_within_rounding(dtype):
+    """As for the product, the reduced side being an expert's rows: up to 20000."""
+    counts, K, N = [20000, 37, 900], 264, 136
+    x = torch.randn(sum(counts), K, generator=gen(1), device="cuda").to(BF16)
+    dy = torch.randn(sum(counts), N, generator=gen(2), device="cuda").to(BF16)
+    off = offsets_of(counts)
+    got = pkg.moe_grouped_weight_grad(x, dy, off, out_dtype=dtype).double()
+    ref, size = weight_reference(x, dy, off), weight_reference(x.abs(), dy.abs(), off)
+    for e, m in enumerate(counts):
+        adds = 2 * m / 16 if dtype is BF16 else 2 * 32 + m / 512
+        half = U16 if dtype is BF16 else U32
+        bound = half * ref[e].abs() * (1 + 1e-3) + (adds + 2) * 2 * U32 * size[e]
+        assert ((got[e] - ref[e]).abs() <= bound).all()
+        if dtype is F32:
+            assert ((got[e] - ref[e]).norm() / ref[e].norm()).item() < 1e-6
+
+
+# ----------------------------------------------------------------- together --
+def sorted_rows(ids, E):
+    """Items sorted by expert and the experts' offsets, as moe_align orders them."""
+    plan = pkg.moe_align(ids, E, block_m=1)
+    return plan["sorted_token_ids"].long(), plan["expert_offsets"]
+
+
+@pytest.mark.parametrize("M,H,I,E,k", [(37, 128, 72, 6, 2), (200, 264, 136, 16, 4)])
+def test_training_step_of_a_layer(M, H, I, E, k):
+    """Routing, the experts forward and backward, the router's gradient: against
+    autograd in 64 bits on the same weights.  Intermediate tensors are bf16: gate
+    and up, z, dz, their gradients, a rounding of 2^-9 of each element on either
+    side of products that average them, so that the relative error of a result
+    in the norm is a few times 2^-9 (0.2 %); 1.5 % allows for seven of them."""
+    f = lambda s, *shape: (torch.randn(*shape, generator=gen(s), device="cuda") * 0.3).to(BF16)  # noqa: E731
+    x, w13, w2, logits, dy = (f(1, M, H), f(2, E, H, 2 * I), f(3, E, I, H), f(4, M, E).float() * 4,
+                              f(5, M, H))
+    weights, ids = pkg.moe_route(logits, k, "softmax", renormalize=True)
+    order, off = sorted_rows(ids, E)
+    token = order // k
+    row_w = weights.reshape(-1)[order].contiguous()
+    xs, dys = x[token], dy[token]
+    gate_up = pkg.moe_grouped_matmul(xs, w13, off)
+    z = pkg.moe_swiglu(gate_up, row_w)
+    y = torch.zeros(M, H, device="cuda").index_add_(0, token, pkg.moe_grouped_matmul(
+        z, w2, off, out_dtype=F32))
+    dz = pkg.moe_grouped_matmul(dys, w2, off, transposed=True)
+    dgu, drow = pkg.moe_swiglu_backward(dz, gate_up, row_w)
+    dw2 = pkg.moe_grouped_weight_grad(z, dys, off)
+    dw13 = pkg.moe_grouped_weight_grad(xs, dgu, off)
+    dx = torch.zeros(M, H, device="cuda").index_add_(0, token, pkg.moe_grouped_matmul(
+        dgu, w13, off, transposed=True, out_dtype=F32))
+    gw = torch.empty_like(weights)
+    gw.view(-1)[order] = drow
+    dl = pkg.moe_route_backward(gw, logits, ids, "softmax", renormalize=True)
+
+    t = [v.double().requires_grad_() for v in (x, w13, w2, logits)]
+    p = torch.softmax(t[3], 1).gather(1, ids.long())
+    p = p / p.sum(1, keepdim=True)
+    h = torch.einsum("mh,mkhi->mki", t[0], t[1][ids.long()])
+    a = torch.nn.functional.silu(h[..., :I]) * h[..., I:] * p[..., None]
+    ry = torch.einsum("mki,mkih->mh", a, t[2][ids.long()])
+    (ry * dy.double()).sum().backward()
+    for got, ref in ((y, ry.detach()), (dx, t[0].grad), (dw13, t[1].grad), (dw2, t[2].grad),
+                     (dl, t[3].grad)):
+        assert ((got.double() - ref).norm() / ref.norm()).item() < 0.015
+    # the library's own forward of the layer
+    own = pkg.moe_forward(x, weights, ids, w13, w2)
+    assert ((own.double() - y.double()).norm() / y.double().norm()).item() < 0.015
+
+
+def step(x, w, dy, off):
+    y = pkg.moe_grouped_matmul(x, w, off)
+    d = pkg.moe_grouped_matmul(dy, w, off, transposed=True)
+    z = pkg.moe_swiglu(y)
+    g, _ = pkg.moe_swiglu_backward(z, y)
+    return y, d, z, g, pkg.moe_grouped_weight_grad(x, dy, off)
+
+
+def step_inputs(seed, counts=(40, 0, 300, 7)):
+    R = sum(counts)
+    return (torch.randn(R, 136, generator=gen(seed), device="cuda").to(BF16),
+            torch.randn(len(counts), 136, 272, generator=gen(seed + 1), device="cuda").to(BF16),
+            torch.randn(R, 272, generator=gen(seed + 2), device="cuda").to(BF16),
+            offsets_of(list(counts)))
+
+
+def test_captured_steps_replay_on_new_inputs():
+    """Two captured graphs of the same calls, replayed in turn and with other
+    offsets, equal eager calls bit for bit."""
+    a, b = step_inputs(1), step_inputs(50, (0, 347, 0, 0))
+    static = [t.clone() for t in a]
+    graphs, outs = [], []
+    step(*static)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(*static))
+        graphs.append(g)
+    for inputs in (a, b, a):
+        for s, t in zip(static, inputs):
+            s.copy_(t)
+        for g in graphs:
+            g.replay()
+        ref = step(*inputs)
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(o, r) for o, r in zip(out, ref))
+
+
+def test_streams_and_threads():
+    """Calls on streams of the caller's and from several host threads."""
+    inputs = [step_inputs(10 * i) for i in range(3)]
+    refs = [step(*i) for i in inputs]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    x, w, dy, off = inputs[0]
+    s.wait_stream(torch.cuda.current_stream())
+    y = pkg.moe_grouped_matmul(x, w, off, stream=s)
+    g = pkg.moe_grouped_weight_grad(x, dy, off, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, refs[0][0]) and torch.equal(g, refs[0][4])
+    bad = []
+
+    def run(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                out = step(*inputs[i])
+        st.synchronize()
+        if not all(torch.equal(o, r) for o, r in zip(out, refs[i])):
+            bad.append(i)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_repeated_calls_give_the_same_bits():
+    inputs = step_inputs(77, (1000, 3, 0, 900))
+    ref = step(*inputs)
+    for _ in range(10):
+        assert all(torch.equal(o, r) for o, r in zip(step(*inputs), ref))
+
+
+@pytest.mark.parametrize("counts,K,N", [([(1 << 31) // 4096 + 700], 64, 4096),       # the output
+                                        ([(1 << 31) // 4096 + 700], 4096, 8),        # the rows
+                                        ([5, 300], 4096, (1 << 19) + 4096)])         # the weight
+def test_product_past_32_bits(counts, K, N):
+    R, off = sum(counts), offsets_of(counts)
+    x = torch.empty(R, K, device="cuda", dtype=BF16)
+    w = torch.empty(len(counts), K, N, device="cuda", dtype=BF16)
+    for t in (x, w):
+        for p in t.view(-1).split(1 << 28):
+            p.copy_(torch.randint(-1, 2, p.shape, generator=gen(1), device="cuda", dtype=torch.int8))
+    y = pkg.moe_grouped_matmul(x, w, off)
+    m, n = min(R, 40), min(N, 136)
+    e = len(counts) - 1
+    ref = x[-m:].double() @ w[e, :, -n:].double()
+    assert torch.equal(y[-m:, -n:], ref.to(BF16))
+
+
+def test_weight_grad_past_32_bits():
+    R, K, N = (1 << 31) // 2048 + 100, 2048, 8
+    x = torch.zeros(R, K, device="cuda", dtype=BF16)
+    dy = torch.zeros(R, N, device="cuda", dtype=BF16)
+    x[-50:], dy[-50:] = ints(1, 50, K), ints(2, 50, N)
+    off = torch.tensor([0, R - 30, R], dtype=torch.int32, device="cuda")
+    got = pkg.moe_grouped_weight_grad(x, dy, off)
+    assert torch.equal(got[1].double(), x[-30:].double().t() @ dy[-30:].double())
+    assert torch.equal(got[0].double(), x[-50:-30].double().t() @ dy[-50:-30].double())
+    E, K, N = 40, 8192, 8192                                    # the output: 2.7e9 elements
+    x, dy = ints(3, E * 2, K), ints(4, E * 2, N)
+    got = pkg.moe_grouped_weight_grad(x, dy, offsets_of([2] * E), out_dtype=BF16)
+    assert torch.equal(got[-1], (x[-2:].double().t() @ dy[-2:].double()).to(BF16))

@@ -17,6 +17,10 @@ def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
 
+def offsets_of(counts, first=0):
+    return torch.tensor([first, *(first + np.cumsum(counts))], dtype=torch.int32, device="cuda")
+
+
 # ------------------------------------------------------------ quantisation --
 QUANT = [(1, 32), (3, 96), (2, 128), (5, 160), (1, 7168), (33, 256), (129, 2048), (17, 1952),
          (1000, 384), (7, 18432)]
@@ -100,3 +104,185 @@ def test_quant_past_32_bits():
         q0, s0 = pkg.moe_quant_mx_fp4(rows, swiglu)
         for part in (slice(0, n), slice(M - n, M)):
             assert torch.equal(q[part], q0) and torch.equal(s[part], s0)
+
+
+# ----------------------------------------------------------------- product --
+TABLE = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6],
+                     dtype=torch.float64)
+
+
+def values64(q, s):
+    t = TABLE.to(q.device)
+    v = torch.stack([t[(q & 15).long()], t[(q >> 4).long()]], -1).flatten(-2)
+    return v * torch.exp2(s.double() - 127).repeat_interleave(32, -1)
+
+
+def codes(seed, lead, K, low=126, high=128):
+    """All codes, scales 2^(low - 127)..2^(high - 127): products are multiples of
+    2^(2 (low - 127) - 2), so that sums of some thousand are exact in fp32."""
+    q = torch.randint(0, 256, (*lead, K // 2), generator=gen(seed), device="cuda", dtype=torch.uint8)
+    s = torch.randint(low, high + 1, (*lead, K // 32), generator=gen(seed + 1), device="cuda",
+                      dtype=torch.uint8)
+    return q, s
+
+
+def reference(a, w, off, out):
+    y = out.double().clone()
+    for e, (i, j) in enumerate(zip(off, off[1:])):
+        y[i:j] = a[i:j] @ w[e].t()
+    return y
+
+
+@pytest.mark.parametrize("K", [32, 64, 96, 128, 256, 288, 512, 640, 1024, 2080])
+@pytest.mark.parametrize("N", [8, 64, 256, 264])
+@pytest.mark.parametrize("R", [1, 33, 224, 225, 700])
+def test_dense_product_exact(R, N, K):
+    a, sa = codes(1, (R,), K)
+    w, sw = codes(3, (N,), K)
+    ref = values64(a, sa) @ values64(w, sw).t()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (F32, BF16):
+        out = torch.full((R + 2, N), 7.0, device="cuda", dtype=dt)
+        pkg.moe_matmul_fp4(a, sa, w, sw, out=out[1:-1], error_word=err)
+        assert torch.equal(out[1:-1], ref.to(dt))
+        assert (out[0] == 7).all() and (out[-1] == 7).all()
+    assert err.item() == 0
+
+
+COUNTS = [[1], [0, 3, 0], [31, 32, 33, 1, 0, 16], [223, 224, 225], [0, 0, 1000, 5, 0], [3] * 70]
+
+
+@pytest.mark.parametrize("K,N", [(32, 8), (288, 264), (1024, 520)])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{max(c)}")
+def test_grouped_product_exact(counts, K, N):
+    """Rows of nobody have NaN scales and are not written."""
+    E, R = len(counts), sum(counts) + 5
+    off = offsets_of(counts, 2)
+    a, sa = codes(1, (R,), K)
+    sa[:2], sa[-3:] = 255, 255
+    w, sw = codes(3, (E, N), K)
+    out = torch.full((R, N), 7.0, device="cuda")
+    pkg.moe_matmul_fp4(a, sa, w, sw, off, out=out)
+    assert torch.equal(out, reference(values64(a, sa), values64(w, sw), off.tolist(),
+                                      torch.full_like(out, 7.0)).float())
+
+
+def test_product_every_scale():
+    """Scales over their range, of either operand, the other 1: products of normal
+    fp32 size scale exactly."""
+    K, N = 256, 64
+    a, _ = codes(1, (200,), K)
+    w, _ = codes(3, (N,), K)
+    one_a, one_w = (torch.full((n, K // 32), 127, device="cuda", dtype=torch.uint8) for n in (200, N))
+    base = pkg.moe_matmul_fp4(a, one_a, w, one_w, out_dtype=F32).double()
+    e = torch.arange(20, 220, device="cuda", dtype=torch.uint8)
+    got = pkg.moe_matmul_fp4(a, e[:, None].expand(200, K // 32).contiguous(), w, one_w, out_dtype=F32)
+    assert torch.equal(got.double(), base * torch.exp2(e.double() - 127)[:, None])
+    e = torch.arange(90, 90 + N, device="cuda", dtype=torch.uint8)
+    got = pkg.moe_matmul_fp4(a, one_a, w, e[:, None].expand(N, K // 32).contiguous(), out_dtype=F32)
+    assert torch.equal(got.double(), base * torch.exp2(e.double() - 127))
+
+
+def test_product_nan_scales():
+    K, N = 320, 72
+    a, sa = codes(1, (50,), K)
+    w, sw = codes(3, (N,), K)
+    base = pkg.moe_matmul_fp4(a, sa, w, sw)
+    sa2, sw2, a2 = sa.clone(), sw.clone(), a.clone()
+    sa2[7, 3], sw2[11, 9] = 255, 255
+    a2[7, 48:64] = 0                                       # as the quantisation leaves such a block
+    y = pkg.moe_matmul_fp4(a2, sa2, w, sw2)
+    assert torch.isnan(y[7]).all() and torch.isnan(y[:, 11]).all()
+    rows, cols = [r for r in range(50) if r != 7], [c for c in range(N) if c != 11]
+    assert torch.equal(y[rows][:, cols], base[rows][:, cols])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("R,N,K", [(300, 520, 7168), (5, 264, 14336)])
+def test_product_within_rounding(R, N, K, dtype):
+    """Quantised normals.  An MMA adds 64 products; its sum and addition drop at
+    most 2^-23 each of what is there; fp32 outputs add 2048 of K at a time."""
+    x = torch.randn(R, K, generator=gen(1), device="cuda").to(BF16)
+    v = (torch.randn(N, K, generator=gen(2), device="cuda") * 0.02).to(BF16)
+    a, w = pkg.moe_quant_mx_fp4(x), pkg.moe_quant_mx_fp4(v)
+    y = pkg.moe_matmul_fp4(*a, *w, out_dtype=dtype).double()
+    a64, w64 = values64(*a), values64(*w)
+    ref, size = a64 @ w64.t(), a64.abs() @ w64.abs().t()
+    adds = 2 * K / 64 if dtype is BF16 else 2 * 32 + K / 2048
+    half = U16 if dtype is BF16 else U32
+    assert ((y - ref).abs() <= half * ref.abs() * (1 + 1e-3) + (adds + 2) * 2 * U32 * size).all()
+    if dtype is F32:
+        assert ((y - ref).norm() / ref.norm()).item() < 1e-6
+
+
+def test_rows_do_not_depend_on_company():
+    w, sw = codes(3, (264,), 640, 110, 140)
+    a, sa = codes(1, (700,), 640, 110, 140)
+    full = pkg.moe_matmul_fp4(a, sa, w, sw)
+    for n in (1, 33, 224, 511):
+        assert torch.equal(pkg.moe_matmul_fp4(a[:n].clone(), sa[:n].clone(), w, sw), full[:n])
+
+
+def test_experts_forward_and_the_gradient_of_their_weight():
+    """Rows quantised, multiplied by quantised experts, SiLU * up quantised and
+    multiplied again; and the weight gradient from the values the codes stand
+    for.  Each step against 64 bits on what the step before gave: bf16 results
+    are off by 2^-9 in the mean at most, 0.4 % in the norm with room; a code of a
+    z next to a border, 8 * 2^-24 wide, may be its neighbour."""
+    E, H, I, counts = 4, 256, 96, [40, 0, 111, 2]
+    off = offsets_of(counts)
+    x = torch.randn(sum(counts), H, generator=gen(1), device="cuda").to(BF16)
+    w13 = (torch.randn(E, 2 * I, H, generator=gen(2), device="cuda") * 0.1).to(BF16)
+    w2 = (torch.randn(E, H, I, generator=gen(3), device="cuda") * 0.1).to(BF16)
+    q13 = [t.view(E, 2 * I, -1) for t in pkg.moe_quant_mx_fp4(w13.view(-1, H))]
+    q2 = [t.view(E, H, -1) for t in pkg.moe_quant_mx_fp4(w2.view(-1, I))]
+    xv = torch.empty_like(x)
+    xq = pkg.moe_quant_mx_fp4(x, values=xv)
+    h = pkg.moe_matmul_fp4(*xq, *q13, off)
+    zq = pkg.moe_quant_mx_fp4(h, swiglu=True)
+    y = pkg.moe_matmul_fp4(*zq, *q2, off, out_dtype=F32)
+    zeros = lambda n: torch.zeros(len(x), n, device="cuda")  # noqa: E731
+    o = off.tolist()
+    rh = reference(values64(*xq), values64(*q13), o, zeros(2 * I))
+    assert ((h.double() - rh).norm() / rh.norm()).item() < 0.004
+    # the second product from the library's codes of its own gate and up
+    ry = reference(values64(*zq), values64(*q2), o, zeros(H))
+    assert ((y.double() - ry).norm() / ry.norm()).item() < 1e-6
+    # and the codes those of bf16 gate and up
+    code, scale = oracle.quant_mx_fp4(oracle.swiglu(h.double().cpu().numpy()))
+    same = (zq[0].cpu().numpy() == oracle.pack_fp4(code)).mean()
+    assert same > 0.999 and (zq[1].cpu().numpy() == scale).mean() > 0.999
+    dh = torch.randn(len(x), 2 * I, generator=gen(4), device="cuda").to(BF16)
+    g = pkg.moe_grouped_weight_grad(xv, dh, off).double()
+    rg = torch.stack([xv[i:j].double().t() @ dh[i:j].double() for i, j in zip(o, o[1:])])
+    assert ((g - rg).norm() / rg.norm()).item() < 1e-6
+
+
+def test_captured_calls_replay():
+    K, N, counts = 640, 264, [50, 0, 300]
+    off = offsets_of(counts)
+    x = torch.randn(350, K, generator=gen(1), device="cuda").to(BF16)
+    w = codes(3, (3, N), K)
+    run = lambda: pkg.moe_matmul_fp4(*pkg.moe_quant_mx_fp4(x), *w, off)  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for seed in (5, 6):
+        x.copy_(torch.randn(350, K, generator=gen(seed), device="cuda"))
+        off.copy_(offsets_of([3, 300, 47] if seed == 6 else counts))
+        g.replay()
+        assert torch.equal(out, run())
+
+
+@pytest.mark.parametrize("R,N,K", [((1 << 31) // 4096 + 700, 4096, 64),      # the output
+                                   ((1 << 32) // 8192 + 700, 8, 8192),       # the rows' codes
+                                   (40, (1 << 32) // 8192 + 4096, 8192)])    # the weight's
+def test_product_past_32_bits(R, N, K):
+    a, sa = codes(1, (R,), K, 127, 128)
+    w, sw = codes(3, (N,), K, 127, 128)
+    y = pkg.moe_matmul_fp4(a, sa, w, sw)
+    m, n = min(R, 40), min(N, 136)
+    ref = values64(a[-m:], sa[-m:]) @ values64(w[-n:], sw[-n:]).t()
+    assert torch.equal(y[-m:, -n:], ref.to(BF16))

@@ -71,6 +71,48 @@ def _p(v=4096):
     return ctypes.c_void_p(v)
 
 
+def _product(R=8, E=2, K=64, N=64, t=0, f32=0, x=4096, w=4096, off=4096, bias=0, out=4096, err=0):
+    return pkg.lib().moe_grouped_matmul(_p(x), _p(w), _p(off), t, _p(bias), R, E, K, N, f32,
+                                        _p(out), _p(err), None)
+
+
+def _grad(R=8, E=2, K=64, N=64, f32=0, acc=0, x=4096, dy=4096, off=4096, out=4096, err=0):
+    return pkg.lib().moe_grouped_weight_grad(_p(x), _p(dy), _p(off), R, E, K, N, f32, acc,
+                                             _p(out), _p(err), None)
+
+
+def _fp4(R=8, E=2, K=64, N=64, f32=0, a=4096, sa=4096, w=4096, sw=4096, off=4096, out=4096, err=0):
+    return pkg.lib().moe_matmul_fp4(_p(a), _p(sa), _p(w), _p(sw), _p(off), R, E, K, N, f32,
+                                    _p(out), _p(err), None)
+
+
+@pytest.mark.parametrize("call,unit", [(_product, 8), (_grad, 8), (_fp4, 32)])
+def test_grouped_refusals(call, unit):
+    assert call(R=-1) == INVALID and call(R=(1 << 31) - 1023) == INVALID
+    assert call(E=0) == INVALID and call(E=1025) == INVALID
+    assert call(K=0) == INVALID and call(K=unit // 2) == INVALID and call(K=64 + unit // 2) == INVALID
+    assert call(K=(1 << 22) + 32) == INVALID
+    assert call(N=0) == INVALID and call(N=60) == INVALID and call(N=(1 << 22) + 8) == INVALID
+    assert call(f32=2) == INVALID
+    assert call(R=1 << 30, N=1 << 20) == INVALID                      # R * N
+    assert call(E=1024, K=1 << 20, N=1 << 18) == INVALID              # tiles of the weights
+    for name in ("x", "w", "out", "off") if call is _product else (
+            ("x", "dy", "out", "off") if call is _grad else ("a", "sa", "w", "sw", "out")):
+        assert call(**{name: 0}) == INVALID
+        assert call(**{name: 4098}) == INVALID                        # alignment
+    assert call(err=4098) == INVALID
+    if call is _product:
+        assert call(t=2) == INVALID and call(bias=4104) == INVALID
+    if call is _grad:
+        assert call(acc=2) == INVALID and call(R=1 << 30, K=1 << 20) == INVALID
+    if call is _fp4:
+        assert call(off=0) == INVALID                                 # dense: one weight
+    if call is not _grad:
+        assert call(R=0, E=1) == OK
+    if not torch.cuda.is_available():
+        assert call() == NO_DEVICE
+
+
 def test_swiglu_and_quant_refusals():
     lib, p, odd = pkg.lib(), _p(), _p(4104)
     fwd = lambda R=4, I=64, gu=p, w=None, z=p: lib.moe_swiglu(gu, w, R, I, z, None)  # noqa: E731
@@ -115,3 +157,39 @@ def test_binding_refusals_of_swiglu_and_quant():
     _raises("q4 has shape", q, bf(4, 64), q4=u8(4, 31))
     _raises("values must", q, bf(4, 64), values=torch.zeros(4, 64))
     _raises("CUDA device", q, bf(4, 64))
+
+
+def test_binding_refusals_of_grouped_products():
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    off = torch.tensor([0, 3, 8], dtype=torch.int32)
+    x, w = bf(8, 64), bf(2, 64, 32)
+    f = pkg.moe_grouped_matmul
+    _raises("x must be", f, x.float(), w, off)
+    _raises("2-dimensional", f, x[0], w, off)
+    _raises("w must be a 3-dim", f, x, w[0], off)
+    _raises("w has shape", f, x, bf(2, 56, 32), off)
+    _raises("w has shape", f, x, w, off, transposed=True)
+    _raises("contiguous", f, x, bf(2, 32, 64).transpose(1, 2), off)
+    _raises("expert_offsets has shape", f, x, w, off[:2])
+    _raises("expert_offsets must", f, x, w, off.long())
+    _raises("bias has shape", f, x, w, off, bias=bf(2, 31))
+    _raises("the output is", f, x, w, off, out_dtype=torch.float16)
+    _raises("out has shape", f, x, w, off, out=bf(8, 31))
+    _raises("error_word", f, x, w, off, error_word=off)
+    _raises("CUDA device", f, x, w, off)
+    g = pkg.moe_grouped_weight_grad
+    _raises("dy has shape", g, x, bf(7, 32), off)
+    _raises("accumulate needs", g, x, bf(8, 32), off, accumulate=True)
+    _raises("at least two", g, x, bf(8, 32), off[:1])
+    _raises("expert_offsets must", g, x, bf(8, 32), None)
+    _raises("out has shape", g, x, bf(8, 32), off, out=bf(3, 64, 32))
+    _raises("CUDA device", g, x, bf(8, 32), off)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    m = pkg.moe_matmul_fp4
+    _raises("a_q must", m, u8(4, 32).float(), u8(4, 2), u8(8, 32), u8(8, 2))
+    _raises("a_scale has shape", m, u8(4, 32), u8(4, 1), u8(8, 32), u8(8, 2))
+    _raises("w_q must be a 2-dim", m, u8(4, 32), u8(4, 2), u8(2, 8, 32), u8(2, 8, 2))
+    _raises("w_q must be a 3-dim", m, u8(8, 32), u8(8, 2), u8(8, 32), u8(8, 2), off)
+    _raises("w_scale has shape", m, u8(8, 32), u8(8, 2), u8(2, 8, 32), u8(8, 2), off)
+    _raises("whole blocks", m, u8(4, 24), u8(4, 1), u8(8, 24), u8(8, 1))
+    _raises("CUDA device", m, u8(8, 32), u8(8, 2), u8(2, 8, 32), u8(2, 8, 2), off)
