@@ -26,6 +26,8 @@ enum Mode { kProduct, kProductT, kWeightGrad, kFp4 };  // W [E, K, N], [E, N, K]
 constexpr int kGrThreads = 128 + 256;  // TMA, MMA, two helper warps; 8 output warps
 constexpr int kGrMaxExperts = 1024;
 constexpr int kGrGroup = 8;            // row tiles of a raster group
+constexpr int kGrStaging = 2048;       // an output warp's: 16 rows by 32 columns of fp32
+constexpr int kGrRelay = 16;           // bytes by which the odd CTA signals the even one
 // Registers: as in the dense FP8 pairs, the first warpgroup gives up what the output
 // warps, with up to 128 sums each, need.
 constexpr int kGrRegsLaunch = 168, kGrRegsFew = 88, kGrRegsMany = 208;
@@ -41,18 +43,24 @@ struct GrGeo {
   static constexpr int TM = FP4 ? 224 : 256;
   static constexpr int SCALES = FP4 ? 3072 : 0;  // of a stage: 128 + 256 rows by 8 bytes
   static constexpr int STAGE = 32768 + SCALES;
-  static constexpr int STAGES = 6;
-  static constexpr size_t SMEM = 1024 + STAGES * STAGE;
+  static constexpr int STAGES = FP4 ? 5 : 6;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE + 8 * kGrStaging;
 };
 constexpr uint32_t kScaleCol = 448;  // TMEM columns of FP4's scales, 24 for each of two stages
 
 template <int MODE>
 struct GrCtl {
   static constexpr int S = GrGeo<MODE>::STAGES;
-  uint64_t full[S], empty[S], tail[S];
+  uint64_t full[S], empty[S];
+  uint64_t tail[S];               // weight grad: the expert's last rows; FP4: the odd CTA's scales
   uint64_t tmem_full[2], tmem_empty[2];
   uint32_t tmem_base;
   int32_t abort;
+  // the odd CTA signals by a copy of 16 bytes into relay[stage] of the even one, which
+  // completes on that CTA's full barrier the way its loads do (an arrival with release at
+  // cluster scope waits for the thread's memory operations in flight, ~1000 cycles)
+  alignas(16) uint8_t relay[S][kGrRelay];
+  alignas(16) uint8_t relay_src[kGrRelay];
   int64_t blocks;                 // stages that this CTA's loads went through
   int32_t total;                  // tiles
   int32_t start[kGrMaxExperts];   // first row and rows of each expert
@@ -126,19 +134,24 @@ __device__ __forceinline__ int gr_blocks(const GrParams& P, const GrTile& tl) {
 // ---- MX FP4 instructions ----
 // Scales from shared memory to TMEM: 128 rows by 4 bytes, row r at (r % 32) * 16 + r / 32 * 4,
 // become 4 columns, repeated for the four warps' lanes, in both CTAs of the pair.
-__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t saddr) {
+__device__ __forceinline__ void copy_scales_pair_if(uint32_t go, uint32_t tmem, uint32_t saddr) {
   // no swizzle, 8-row groups 128 bytes apart
-  const uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | uint64_t(8) << 32 | uint64_t(1) << 46;
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
-}
-__device__ __forceinline__ void mma_mxfp4_pair(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                               uint32_t idesc, uint32_t sa, uint32_t sb,
-                                               uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)
+      "{\n\t.reg .pred q;\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tsetp.ne.b32 q, %3, 0;\n\t"
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(tmem),
+      "r"(saddr >> 4), "r"(8u | 1u << 14), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void mma_mxfp4_pair_if(uint32_t go, uint32_t d_tmem, uint32_t a_lo,
+                                                  uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                                  uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %8, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%6], [%7], p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb),
+      "r"(go)
       : "memory");
 }
 // Instruction descriptor for kind::mxf4: bits 4-5 the byte pair of B's scales, 7-9 and
@@ -160,13 +173,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   uint8_t* tiles = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  // the odd CTA's word that stage's part of it is in place
+  auto relay = [&](int stage) {
+    ptx::bulk_copy_to_cluster(ptx::mapa_shared(ptx::smem_u32(ctl.relay[stage]), 0), ctl.relay_src,
+                              kGrRelay, ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0));
+  };
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::STAGES; ++i) {
-      // full: the loads of both CTAs (one arrival); weight grad: one more, so that the two
-      // CTAs' tail fixes can stand in for the pair; FP4: two scale warps of each CTA
-      ptx::mbar_init(&ctl.full[i], G::WG ? 2 : G::FP4 ? 5 : 1);
+      // full: the loads of both CTAs (one arrival); weight grad: one more, for the even CTA's
+      // tail; FP4: two more, for its scale warps
+      ptx::mbar_init(&ctl.full[i], G::WG ? 2 : G::FP4 ? 3 : 1);
       ptx::mbar_init(&ctl.empty[i], 1);
-      ptx::mbar_init(&ctl.tail[i], 1);
+      ptx::mbar_init(&ctl.tail[i], G::FP4 ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&ctl.tmem_full[i], 1);
@@ -225,53 +243,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGrRegsFew));
-    if (warp == 0 && lane == 0) {
+    // (The loading and the issuing warp run their loops as one, an elected lane issuing: in a
+    // branch of one lane an MMA took 70 cycles to issue, the loop 730 for the 512 that a stage
+    // of 256 columns computes.  8 x 1024 rows, K 4096, N 28672: 1193 us so, 1077 as here;
+    // the weight gradient of 128 x 1024 rows, 2048 x 1536: 726 and 597.  A wait that ran out
+    // does not end a loop: once it has, all others end at once, and the loop runs out.)
+    if (warp == 0) {
       // ---- loads ----
+      const uint32_t go = ptx::elect_one();
+      const uint32_t tiles0 = ptx::smem_u32(tiles);
       int stage = 0;
       uint32_t phase = 0;
       int64_t blocks = 0;
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
+      for (int t = unit; t < total; t += units) {
         const GrTile tl = gr_tile(ctl, P, t);
         const int KB = gr_blocks<MODE>(P, tl);
         const int half = tl.T / 2;
         const int n = tl.n0 + rank * 128, c = static_cast<int>(tl.c0) + rank * half;
         const uint32_t bytes = 16384u + static_cast<uint32_t>(half) * 128u;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = tiles + stage * G::STAGE;
-          uint8_t* sb = sa + 16384;
+          dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
+          const uint32_t sa = tiles0 + stage * G::STAGE, sb = sa + 16384;
           // both CTAs' copies complete on the even CTA's barrier
           uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0);
           if (G::WG && kb == KB - 1 && tl.rows % 16 != 0) {
             // the last rows of the expert: to this CTA's tail barrier, and on from there
             bar = ptx::mapa_shared(ptx::smem_u32(&ctl.tail[stage]), rank);
-            ptx::mbar_arrive_expect_tx(&ctl.tail[stage], bytes);
+            ptx::mbar_arrive_expect_tx_if(go, &ctl.tail[stage], bytes);
+            if (rank == 0) ptx::mbar_arrive_expect_tx_if(go, &ctl.full[stage], kGrRelay);
           } else if (rank == 0) {
-            ptx::mbar_arrive_expect_tx(&ctl.full[stage], 2 * bytes);
-            if (G::WG) ptx::mbar_arrive(&ctl.full[stage]);
+            ptx::mbar_arrive_expect_tx_if(go, &ctl.full[stage],
+                                          2 * bytes + (G::FP4 ? kGrRelay : 0));
+            if (G::WG) ptx::mbar_arrive_if(go, &ctl.full[stage]);
           }
           if constexpr (G::WG) {
             const int r = tl.r0 + kb * 64;
-            for (int i = 0; i < 2; ++i) ptx::tma_load_2d_pair(sa + i * 8192, &tmA, bar, n + i * 64, r);
-            for (int i = 0; i < half / 64; ++i)
-              ptx::tma_load_2d_pair(sb + i * 8192, &tmB, bar, c + i * 64, r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              ptx::tma_load_2d_pair_if(go, sa + i * 8192, &tmA, bar, n + i * 64, r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (i < half / 64)
+                ptx::tma_load_2d_pair_if(go, sb + i * 8192, &tmB, bar, c + i * 64, r);
           } else {
             const int k = kb * (G::FP4 ? 128 : 64);  // bytes, or elements
             if constexpr (MODE == kProduct) {
+#pragma unroll
               for (int i = 0; i < 2; ++i)
-                ptx::tma_load_3d_pair(sa + i * 8192, &tmA, bar, n + i * 64, k, tl.e);
+                ptx::tma_load_3d_pair_if(go, sa + i * 8192, &tmA, bar, n + i * 64, k, tl.e);
             } else {
-              ptx::tma_load_3d_pair(sa, &tmA, bar, k, n, tl.e);
+              ptx::tma_load_3d_pair_if(go, sa, &tmA, bar, k, n, tl.e);
             }
             if (tl.T == G::TM) {
-              ptx::tma_load_2d_pair(sb, &tmB, bar, k, c);
+              ptx::tma_load_2d_pair_if(go, sb, &tmB, bar, k, c);
             } else {
               for (int i = 0; i < half; i += 16)
-                ptx::tma_load_2d_pair(sb + i * 128, &tmB16, bar, k, c + i);
+                ptx::tma_load_2d_pair_if(go, sb + i * 128, &tmB16, bar, k, c + i);
             }
           }
           ++blocks;
@@ -281,62 +308,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
           }
         }
       }
-      ctl.blocks = blocks;
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+      if (lane == 0) ctl.blocks = blocks;
+    } else if (warp == 1 && rank == 0) {
       // ---- MMAs ----
+      const uint32_t go = ptx::elect_one();
+      const uint32_t tiles0 = ptx::smem_u32(tiles);
+      constexpr uint32_t HI = 64u | 1u << 14 | 2u << 29;  // (8-row groups 1024 bytes apart)
+      // K-major: 32 bytes of a row per step; MN-major: 16 rows, chunks of 64 columns 8192 apart
+      constexpr uint32_t A_STEP = G::A_MN ? 128 : 2, B_STEP = G::WG ? 128 : 2;
+      constexpr uint32_t A_LO = (G::A_MN ? 512u : 1u) << 16, B_LO = (G::WG ? 512u : 1u) << 16;
       int stage = 0;
       uint32_t phase = 0, acc = 0, turn = 0, block = 0;
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
+      for (int t = unit; t < total; t += units) {
         const GrTile tl = gr_tile(ctl, P, t);
         const int KB = gr_blocks<MODE>(P, tl);
         const uint32_t idesc = ptx::idesc_bf16_f32(256, tl.T, G::A_MN, G::WG);
         int in_chunk = 0;
         for (int kb = 0; kb < KB; ++kb, ++block) {
-          if ((in_chunk == 0 &&
-               !dense_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word)) ||
-              !dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word)) {
-            ok = false;
-            break;
-          }
+          if (in_chunk == 0)
+            dense_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word);
+          dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word);
           ptx::tc_fence_after();
-          const uint32_t sa = ptx::smem_u32(tiles + stage * G::STAGE), sb = sa + 16384;
+          const uint32_t sa = tiles0 + stage * G::STAGE;
+          const uint32_t a = (sa >> 4) + A_LO, b = ((sa + 16384) >> 4) + B_LO;
           const uint32_t d = tmem + acc * static_cast<uint32_t>(G::TM);
           if constexpr (G::FP4) {
             const uint32_t sc = tmem + kScaleCol + (block & 1u) * 24u, ss = sa + 32768;
 #pragma unroll
             for (int ka = 0; ka < 2; ++ka) {
-              copy_scales_pair(sc + ka * 4, ss + ka * 512);
-              copy_scales_pair(sc + 8 + ka * 8, ss + 1024 + ka * 1024);
-              copy_scales_pair(sc + 12 + ka * 8, ss + 1536 + ka * 1024);
+              copy_scales_pair_if(go, sc + ka * 4, ss + ka * 512);
+              copy_scales_pair_if(go, sc + 8 + ka * 8, ss + 1024 + ka * 1024);
+              copy_scales_pair_if(go, sc + 12 + ka * 8, ss + 1536 + ka * 1024);
             }
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_mxfp4_pair(d, ptx::smem_desc_sw128(sa + ks * 32, 16, 1024),
-                             ptx::smem_desc_sw128(sb + ks * 32, 16, 1024),
-                             idesc_mxfp4(256, tl.T, (ks & 1) * 2), sc + (ks >> 1) * 4,
-                             sc + 8 + (ks >> 1) * 8, (in_chunk | ks) != 0);
+              mma_mxfp4_pair_if(go, d, a + ks * A_STEP, b + ks * B_STEP, HI,
+                                idesc_mxfp4(256, tl.T, (ks & 1) * 2), sc + (ks >> 1) * 4,
+                                sc + 8 + (ks >> 1) * 8, (in_chunk | ks) != 0);
           } else {
             // weight grad: the last block's MMAs end with the expert's rows
             const int steps = G::WG && kb == KB - 1 ? ceil_div(tl.rows - kb * 64, 16) : 4;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              if (ks >= steps) break;
-              const uint64_t ad = G::A_MN ? ptx::smem_desc_sw128(sa + ks * 2048, 8192, 1024)
-                                          : ptx::smem_desc_sw128(sa + ks * 32, 16, 1024);
-              const uint64_t bd = G::WG ? ptx::smem_desc_sw128(sb + ks * 2048, 8192, 1024)
-                                        : ptx::smem_desc_sw128(sb + ks * 32, 16, 1024);
-              ptx::mma_bf16_pair(d, ad, bd, idesc, (in_chunk | ks) != 0);
-            }
+            for (int ks = 0; ks < 4; ++ks)
+              if (ks < steps)
+                ptx::mma_bf16_pair_if(go, d, a + ks * A_STEP, b + ks * B_STEP, HI, idesc,
+                                      (in_chunk | ks) != 0);
           }
           const bool last = ++in_chunk == P.chunk || kb == KB - 1;
-          if (last) ptx::mma_commit_pair(&ctl.tmem_full[acc], 0x3);
-          ptx::mma_commit_pair(&ctl.empty[stage], 0x3);
+          if (last) ptx::mma_commit_pair_if(go, &ctl.tmem_full[acc], 0x3);
+          ptx::mma_commit_pair_if(go, &ctl.empty[stage], 0x3);
           if (last) {
             in_chunk = 0;
             acc ^= 1u;
             turn ^= acc == 0 ? 1u : 0u;
           }
+          if (++stage == G::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    } else if (G::FP4 && warp == 1 && lane == 0) {
+      // ---- odd CTA: a stage's scales are in place ----
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        const int KB = gr_blocks<MODE>(P, gr_tile(ctl, P, t));
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!dense_wait(&ctl.tail[stage], phase, &ctl.abort, P.error_word)) {
+            ok = false;
+            break;
+          }
+          relay(stage);
           if (++stage == G::STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -372,8 +416,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
-          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0));
+        if (lane == 0) {
+          if (rank == 0)
+            ptx::mbar_arrive(&ctl.full[stage]);
+          else
+            relay(stage);
+        }
       }
     } else if (G::FP4 && warp >= 2) {
       // ---- scales: each lane two of the weight's 128 rows and four of the tile's 256, 16
@@ -456,8 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0)
-              ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0));
+            if (lane == 0) ptx::mbar_arrive(rank == 0 ? &ctl.full[stage] : &ctl.tail[stage]);
             if (++stage == G::STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -471,6 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGrRegsMany));
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tmem_empty[0]), 0);
+    uint8_t* staging = tiles + G::STAGES * G::STAGE + (warp - 4) * kGrStaging;
     uint32_t acc = 0, turn = 0;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
@@ -515,39 +563,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
         turn ^= acc == 0 ? 1u : 0u;
       }
       if (!ok) break;
-      // a warp's store is 32 neighbouring columns of one row
+      // 16 rows by the warp's 32 columns at a time through its staging block and out in
+      // 16-byte stores (each lane storing its own column's elements, one warp's store 64 or
+      // 128 bytes, took 60 of 1210 us at 8 x 1024 rows, K 4096, N 28672, and 170 of 880 us
+      // in the weight gradient of 8 x 1024 rows, 14336 x 4096)
       const int first = part * groups * 16;
-      const int64_t at = ((G::WG ? static_cast<int64_t>(tl.e) * P.K : 0) + tl.c0 + first) * P.N + n;
+      const int64_t row0 = (G::WG ? static_cast<int64_t>(tl.e) * P.K : 0) + tl.c0 + first;
       const int left = min(tl.cols - first, groups * 16);
+      const int nw = tl.n0 + rank * 128 + q * 32;  // the warp's first column
       auto put = [&](auto* out) {
         using O = std::remove_pointer_t<decltype(out)>;
-        out += at;
+        constexpr bool F32 = sizeof(O) == 4;
+        constexpr int PER = 16 / sizeof(O);        // elements of a store
+        constexpr int LANES = 32 / PER;            // lanes of a row
+        constexpr int STEP = 32 / LANES;           // rows of a store
+        const int ln = lane % LANES * PER, lr = lane / LANES;
+        O* dst = out + (row0 + lr) * P.N + nw + ln;
+        const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll
         for (int i = 0; i < G::TM / 32; ++i) {
           if (16 * i >= left) break;
-          float old[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            old[j] = G::WG && P.accumulate && 16 * i + j < left
-                         ? static_cast<float>(out[static_cast<int64_t>(16 * i + j) * P.N])
-                         : 0.f;
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            const float2 o = unpair(sum[8 * i + j / 2]);
-            const int c = 16 * i + j;
-            if (c < left) out[static_cast<int64_t>(c) * P.N] = static_cast<O>(o.x + old[j]);
-            if (c + 1 < left)
-              out[static_cast<int64_t>(c + 1) * P.N] = static_cast<O>(o.y + old[j + 1]);
+            float2 o = unpair(sum[8 * i + j / 2]);
+            if (!F32 && G::WG && P.accumulate && nw + lane < P.N) {  // (added before it is rounded)
+              const O* old = out + (row0 + 16 * i + j) * P.N + nw + lane;
+              if (16 * i + j < left) o.x += static_cast<float>(old[0]);
+              if (16 * i + j + 1 < left) o.y += static_cast<float>(old[P.N]);
+            }
+            if constexpr (F32) {
+              *reinterpret_cast<float*>(staging + j * 128 + lane * 4) = o.x;
+              *reinterpret_cast<float*>(staging + j * 128 + 128 + lane * 4) = o.y;
+            } else {
+              // row j of two columns in even lanes, row j + 1 of them in odd ones
+              const uint32_t mine = pack2(o.x, o.y), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+              *reinterpret_cast<uint32_t*>(staging + (j + (lane & 1)) * 64 + (lane & ~1) * 2) =
+                  __byte_perm(mine, other, sel);
+            }
+          }
+          __syncwarp();
+          if (nw + ln < P.N) {  // (N is a multiple of 8)
+#pragma unroll
+            for (int r = 0; r < 16; r += STEP) {
+              if (16 * i + r + lr < left) {
+                uint4 v = *reinterpret_cast<const uint4*>(staging + r * 32 * sizeof(O) + lane * 16);
+                uint4* at = reinterpret_cast<uint4*>(dst + static_cast<int64_t>(16 * i + r) * P.N);
+                if (F32 && G::WG && P.accumulate) {
+                  const uint4 old = *at;
+                  v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(old.x));
+                  v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(old.y));
+                  v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(old.z));
+                  v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(old.w));
+                }
+                *at = v;
+              }
+            }
           }
         }
       };
-      if (n < P.N) {
-        if (P.out_f32)
-          put(static_cast<float*>(P.out));
-        else
-          put(static_cast<bf16*>(P.out));
-      }
-      __syncwarp();
+      if (P.out_f32)
+        put(static_cast<float*>(P.out));
+      else
+        put(static_cast<bf16*>(P.out));
     }
   }
   __syncwarp();
