@@ -27,6 +27,7 @@ constexpr int kGrThreads = 128 + 256;  // TMA, MMA, two helper warps; 8 output w
 constexpr int kGrMaxExperts = 1024;
 constexpr int kGrGroup = 8;            // row tiles of a raster group
 constexpr int kGrStaging = 2048;       // an output warp's: 16 rows by 32 columns of fp32
+constexpr int kScaleChunks = 3;        // FP4: chunks of 512 elements whose scales are on their way
 constexpr int kGrRelay = 16;           // bytes by which the odd CTA signals the even one
 // Registers: as in the dense FP8 pairs, the first warpgroup gives up what the output
 // warps, with up to 128 sums each, need.
@@ -44,7 +45,8 @@ struct GrGeo {
   static constexpr int SCALES = FP4 ? 3072 : 0;  // of a stage: 128 + 256 rows by 8 bytes
   static constexpr int STAGE = 32768 + SCALES;
   static constexpr int STAGES = FP4 ? 5 : 6;
-  static constexpr size_t SMEM = 1024 + STAGES * STAGE + 8 * kGrStaging;
+  static constexpr size_t SMEM =
+      1024 + STAGES * STAGE + 8 * kGrStaging + (FP4 ? kScaleChunks * 6144 : 0);
 };
 constexpr uint32_t kScaleCol = 448;  // TMEM columns of FP4's scales, 24 for each of two stages
 
@@ -425,16 +427,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       }
     } else if (G::FP4 && warp >= 2) {
       // ---- scales: each lane two of the weight's 128 rows and four of the tile's 256, 16
-      // bytes (512 elements, two stages) of each at a time, the next ones' loads in flight ----
+      // bytes (512 elements, two stages) of each at a time ----
+      // They come by asynchronous copies into a ring of the lane's own, kScaleChunks ahead and
+      // across tiles (held in registers one chunk ahead, their latency was in every
+      // chunk: 8192 x 7168 x 4096 155 us, 119 with the ring), and go from there to where
+      // the tensor core's copy takes them.
       const int w = warp - 2;
       const int KG = P.K / 32;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
-        const GrTile tl = gr_tile(ctl, P, t);
-        const int KB = gr_blocks<MODE>(P, tl);
-        const uint8_t* src[6];  // null: no such row
+      uint8_t* ring = tiles + G::STAGES * G::STAGE + 8 * kGrStaging + (w * 32 + lane) * 16;
+      constexpr int ROW = 64 * 16, CHUNK = 6 * ROW;  // a row of both warps' lanes, six of them
+      int ft = unit, fg = 0, fslot = 0;  // what is fetched next: tile, scale of K, slot
+      const uint8_t* src[6];             // its rows; null: no such row
+      auto rows = [&]() {
+        const GrTile tl = gr_tile(ctl, P, ft);
 #pragma unroll
         for (int i = 0; i < 6; ++i) {
           if (i < 2) {
@@ -445,44 +450,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             src[i] = c < tl.T && tl.c0 + c < P.R ? P.x_scale + (tl.c0 + c) * KG : nullptr;
           }
         }
-        // (past K the codes are zeros, and a scale of 0 is 2^-127)
-        auto load = [&](int g, uint32_t (&v)[6][4]) {
+      };
+      // (zeros for rows that are not there and past K, where the codes are zeros: 2^-127)
+      auto fetch = [&]() {
+        if (ft < total) {
+          uint8_t* dst = ring + fslot * CHUNK;
 #pragma unroll
           for (int i = 0; i < 6; ++i) {
+            const uint8_t* from = src[i] != nullptr ? src[i] + fg : P.w_scale;
             if (KG % 16 == 0) {
-              const uint4 u = src[i] != nullptr && g < KG
-                                  ? __ldg(reinterpret_cast<const uint4*>(src[i] + g))
-                                  : make_uint4(0, 0, 0, 0);
-              v[i][0] = u.x;
-              v[i][1] = u.y;
-              v[i][2] = u.z;
-              v[i][3] = u.w;
+              ptx::cp_async_16(dst + i * ROW, from, src[i] != nullptr ? 16 : 0);
             } else if (KG % 4 == 0) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[i][j] = src[i] != nullptr && g + 4 * j < KG
-                              ? __ldg(reinterpret_cast<const uint32_t*>(src[i] + g + 4 * j))
-                              : 0u;
+              for (int j = 0; j < 4; ++j) {
+                const bool in = src[i] != nullptr && fg + 4 * j < KG;
+                ptx::cp_async_4(dst + i * ROW + 4 * j, in ? from + 4 * j : P.w_scale, in ? 4 : 0);
+              }
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                v[i][j] = 0;
+                uint32_t v = 0;
                 for (int q = 0; q < 4; ++q)
-                  if (src[i] != nullptr && g + 4 * j + q < KG)
-                    v[i][j] |= static_cast<uint32_t>(__ldg(src[i] + g + 4 * j + q)) << (8 * q);
+                  if (src[i] != nullptr && fg + 4 * j + q < KG)
+                    v |= static_cast<uint32_t>(__ldg(from + 4 * j + q)) << (8 * q);
+                *reinterpret_cast<uint32_t*>(dst + i * ROW + 4 * j) = v;
               }
             }
           }
-        };
-        uint32_t next[6][4];
-        load(0, next);
+          fslot = fslot + 1 == kScaleChunks ? 0 : fslot + 1;
+          fg += 16;
+          if (fg >= KG) {
+            fg = 0;
+            ft += units;
+            if (ft < total) rows();
+          }
+        }
+        ptx::cp_async_commit();  // (of nothing, at the end: the count of groups stays)
+      };
+      if (ft < total) rows();
+#pragma unroll
+      for (int i = 0; i < kScaleChunks; ++i) fetch();
+      int stage = 0, slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        const int KB = ceil_div(P.K, G::BK);
         for (int kb = 0; kb < KB && ok; kb += 2) {
-          uint32_t v[6][4];
+          uint4 v[6];
+          ptx::cp_async_wait<kScaleChunks - 1>();
 #pragma unroll
           for (int i = 0; i < 6; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = next[i][j];
-          if (kb + 2 < KB) load((kb + 2) * 8, next);
+            v[i] = *reinterpret_cast<const uint4*>(ring + slot * CHUNK + i * ROW);
+          slot = slot + 1 == kScaleChunks ? 0 : slot + 1;
+          fetch();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (kb + h >= KB) break;
@@ -493,14 +513,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             }
             uint8_t* sc = tiles + stage * G::STAGE + 32768 + lane * 16;
 #pragma unroll
-            for (int ka = 0; ka < 2; ++ka) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<uint32_t*>(sc + ka * 512 + (w * 2 + i) * 4) = v[i][h * 2 + ka];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint32_t*>(sc + 1024 + ka * 1024 + w * 512 + i * 4) =
-                    v[2 + i][h * 2 + ka];
+            for (int i = 0; i < 6; ++i) {
+              uint8_t* at = i < 2 ? sc + (w * 2 + i) * 4 : sc + 1024 + w * 512 + (i - 2) * 4;
+              const int next = i < 2 ? 512 : 1024;  // the second 128 elements of the stage
+              *reinterpret_cast<uint32_t*>(at) = h == 0 ? v[i].x : v[i].z;
+              *reinterpret_cast<uint32_t*>(at + next) = h == 0 ? v[i].y : v[i].w;
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -512,6 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
           }
         }
       }
+      ptx::cp_async_wait<0>();
     }
   } else {
     // ---- output: 32 columns n of the weight (lanes) by half of the tile's columns a warp ----
