@@ -26,8 +26,8 @@ enum Mode { kProduct, kProductT, kWeightGrad, kFp4 };  // W [E, K, N], [E, N, K]
 constexpr int kGrThreads = 128 + 256;  // TMA, MMA, two helper warps; 8 output warps
 constexpr int kGrMaxExperts = 1024;
 constexpr int kGrGroup = 8;            // row tiles of a raster group
-constexpr int kGrStaging = 2048;       // an output warp's: 16 rows by 32 columns of fp32
-constexpr int kScaleChunks = 3;        // FP4: chunks of 512 elements whose scales are on their way
+constexpr int kScaleChunks = 3;        // FP4: chunks of 1024 elements whose scales are on their way
+constexpr int kScaleChunkBytes = 384 * 32;
 constexpr int kGrRelay = 16;           // bytes by which the odd CTA signals the even one
 // Registers: as in the dense FP8 pairs, the first warpgroup gives up what the output
 // warps, with up to 128 sums each, need.
@@ -46,9 +46,15 @@ struct GrGeo {
   static constexpr int STAGE = 32768 + SCALES;
   static constexpr int STAGES = FP4 ? 5 : 6;
   static constexpr size_t SMEM =
-      1024 + STAGES * STAGE + 8 * kGrStaging + (FP4 ? kScaleChunks * 6144 : 0);
+      1024 + STAGES * STAGE + (FP4 ? kScaleChunks * kScaleChunkBytes : 0);
 };
 constexpr uint32_t kScaleCol = 448;  // TMEM columns of FP4's scales, 24 for each of two stages
+
+// Where a row's half of a chunk is among 32 rows: the halves change places with every fourth
+// row, so that 8 rows' halves, read together, are in all banks.
+__device__ __forceinline__ int scale_place(int row, int half) {
+  return row * 32 + ((half ^ (row >> 2 & 1)) << 4);
+}
 
 template <int MODE>
 struct GrCtl {
@@ -56,6 +62,7 @@ struct GrCtl {
   uint64_t full[S], empty[S];
   uint64_t tail[S];               // weight grad: the expert's last rows; FP4: the odd CTA's scales
   uint64_t tmem_full[2], tmem_empty[2];
+  uint64_t scales_full[kScaleChunks], scales_empty[kScaleChunks];  // FP4
   uint32_t tmem_base;
   int32_t abort;
   // the odd CTA signals by a copy of 16 bytes into relay[stage] of the even one, which
@@ -82,6 +89,12 @@ struct GrParams {
   int out_f32, accumulate;
   int chunk;               // stages summed in the tensor core before they go to registers
   int32_t* error_word;
+};
+
+// Tensor maps: the weight (or dy), the rows in boxes of half a tile's columns and of 16, and
+// FP4's scales of both.
+struct GrMaps {
+  CUtensorMap a, b, b16, sa, sb;
 };
 
 struct GrTile {
@@ -128,6 +141,18 @@ __device__ __forceinline__ GrTile gr_tile(const GrCtl<MODE>& ctl, const GrParams
   return tl;
 }
 
+// The tile as one value of the warp, for loops whose values have to be known as uniform:
+// a reduction's result is, a shared-memory load's is not (with loop bounds loaded from there
+// an MMA of the weight gradient took 80 cycles to issue, 26 with these).
+__device__ __forceinline__ int warp_value(int v) {
+  return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v)));
+}
+__device__ __forceinline__ GrTile warp_value(const GrTile& t) {  // (all fields are >= 0)
+  return GrTile{warp_value(t.e),    warp_value(t.n0), warp_value(static_cast<int>(t.c0)),
+                warp_value(t.cols), warp_value(t.T),  warp_value(t.r0),
+                warp_value(t.rows)};
+}
+
 template <int MODE>
 __device__ __forceinline__ int gr_blocks(const GrParams& P, const GrTile& tl) {
   return ceil_div(GrGeo<MODE>::WG ? tl.rows : P.K, GrGeo<MODE>::BK);
@@ -166,8 +191,7 @@ __device__ __forceinline__ uint32_t idesc_mxfp4(int M, int N, uint32_t scale_id)
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmB16, const GrParams P) {
+    grouped_kernel(const __grid_constant__ GrMaps maps, const GrParams P) {
   using G = GrGeo<MODE>;
   pdl_begin();
   extern __shared__ uint8_t smem_raw[];
@@ -183,10 +207,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::STAGES; ++i) {
       // full: the loads of both CTAs (one arrival); weight grad: one more, for the even CTA's
-      // tail; FP4: two more, for its scale warps
-      ptx::mbar_init(&ctl.full[i], G::WG ? 2 : G::FP4 ? 3 : 1);
+      // tail; FP4: one more, for its scales
+      ptx::mbar_init(&ctl.full[i], G::WG || G::FP4 ? 2 : 1);
       ptx::mbar_init(&ctl.empty[i], 1);
-      ptx::mbar_init(&ctl.tail[i], G::FP4 ? 2 : 1);
+      ptx::mbar_init(&ctl.tail[i], 1);
+    }
+    for (int i = 0; i < kScaleChunks; ++i) {
+      ptx::mbar_init(&ctl.scales_full[i], 1);
+      ptx::mbar_init(&ctl.scales_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&ctl.tmem_full[i], 1);
@@ -195,9 +223,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
     ctl.abort = 0;
     ctl.blocks = 0;
     ptx::fence_barrier_init();
-    ptx::prefetch_tmap(&tmA);
-    ptx::prefetch_tmap(&tmB);
-    ptx::prefetch_tmap(&tmB16);
+    ptx::prefetch_tmap(&maps.a);
+    ptx::prefetch_tmap(&maps.b);
+    ptx::prefetch_tmap(&maps.b16);
+    if (G::FP4) {
+      ptx::prefetch_tmap(&maps.sa);
+      ptx::prefetch_tmap(&maps.sb);
+    }
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(&ctl.tmem_base, 512);
@@ -239,8 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
   __syncthreads();
   ptx::cluster_sync();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl.tmem_base;
-  const int total = ctl.total;
+  const uint32_t tmem = warp_value(ctl.tmem_base);
+  const int total = warp_value(ctl.total);
   const int unit = static_cast<int>(blockIdx.x >> 1), units = static_cast<int>(gridDim.x >> 1);
 
   if (warp < 4) {
@@ -257,8 +289,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       int64_t blocks = 0;
+      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(&ctl.full[0]), 0);
+      const uint32_t tail0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tail[0]), rank);
       for (int t = unit; t < total; t += units) {
-        const GrTile tl = gr_tile(ctl, P, t);
+        const GrTile tl = warp_value(gr_tile(ctl, P, t));
         const int KB = gr_blocks<MODE>(P, tl);
         const int half = tl.T / 2;
         const int n = tl.n0 + rank * 128, c = static_cast<int>(tl.c0) + rank * half;
@@ -267,10 +301,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
           dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
           const uint32_t sa = tiles0 + stage * G::STAGE, sb = sa + 16384;
           // both CTAs' copies complete on the even CTA's barrier
-          uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0);
+          uint32_t bar = full0 + stage * 8;
           if (G::WG && kb == KB - 1 && tl.rows % 16 != 0) {
             // the last rows of the expert: to this CTA's tail barrier, and on from there
-            bar = ptx::mapa_shared(ptx::smem_u32(&ctl.tail[stage]), rank);
+            bar = tail0 + stage * 8;
             ptx::mbar_arrive_expect_tx_if(go, &ctl.tail[stage], bytes);
             if (rank == 0) ptx::mbar_arrive_expect_tx_if(go, &ctl.full[stage], kGrRelay);
           } else if (rank == 0) {
@@ -282,25 +316,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             const int r = tl.r0 + kb * 64;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              ptx::tma_load_2d_pair_if(go, sa + i * 8192, &tmA, bar, n + i * 64, r);
+              ptx::tma_load_2d_pair_if(go, sa + i * 8192, &maps.a, bar, n + i * 64, r);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               if (i < half / 64)
-                ptx::tma_load_2d_pair_if(go, sb + i * 8192, &tmB, bar, c + i * 64, r);
+                ptx::tma_load_2d_pair_if(go, sb + i * 8192, &maps.b, bar, c + i * 64, r);
           } else {
             const int k = kb * (G::FP4 ? 128 : 64);  // bytes, or elements
             if constexpr (MODE == kProduct) {
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                ptx::tma_load_3d_pair_if(go, sa + i * 8192, &tmA, bar, n + i * 64, k, tl.e);
+                ptx::tma_load_3d_pair_if(go, sa + i * 8192, &maps.a, bar, n + i * 64, k, tl.e);
             } else {
-              ptx::tma_load_3d_pair_if(go, sa, &tmA, bar, k, n, tl.e);
+              ptx::tma_load_3d_pair_if(go, sa, &maps.a, bar, k, n, tl.e);
             }
             if (tl.T == G::TM) {
-              ptx::tma_load_2d_pair_if(go, sb, &tmB, bar, k, c);
+              ptx::tma_load_2d_pair_if(go, sb, &maps.b, bar, k, c);
             } else {
               for (int i = 0; i < half; i += 16)
-                ptx::tma_load_2d_pair_if(go, sb + i * 128, &tmB16, bar, k, c + i);
+                ptx::tma_load_2d_pair_if(go, sb + i * 128, &maps.b16, bar, k, c + i);
             }
           }
           ++blocks;
@@ -322,11 +356,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       int stage = 0;
       uint32_t phase = 0, acc = 0, turn = 0, block = 0;
       for (int t = unit; t < total; t += units) {
-        const GrTile tl = gr_tile(ctl, P, t);
+        const GrTile tl = warp_value(gr_tile(ctl, P, t));
         const int KB = gr_blocks<MODE>(P, tl);
         const uint32_t idesc = ptx::idesc_bf16_f32(256, tl.T, G::A_MN, G::WG);
         int in_chunk = 0;
-        for (int kb = 0; kb < KB; ++kb, ++block) {
+        // one stage's MMAs, of `rows` of K; end: the tile's last
+        auto stage_mmas = [&](auto rows, bool end) {
+          [[maybe_unused]] const int steps = rows;
           if (in_chunk == 0)
             dense_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word);
           dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word);
@@ -348,15 +384,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
                                 idesc_mxfp4(256, tl.T, (ks & 1) * 2), sc + (ks >> 1) * 4,
                                 sc + 8 + (ks >> 1) * 8, (in_chunk | ks) != 0);
           } else {
-            // weight grad: the last block's MMAs end with the expert's rows
-            const int steps = G::WG && kb == KB - 1 ? ceil_div(tl.rows - kb * 64, 16) : 4;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              if (ks < steps)
-                ptx::mma_bf16_pair_if(go, d, a + ks * A_STEP, b + ks * B_STEP, HI, idesc,
-                                      (in_chunk | ks) != 0);
+              ptx::mma_bf16_pair_if(ks * 16 < steps ? go : 0, d, a + ks * A_STEP, b + ks * B_STEP,
+                                    HI, idesc, (in_chunk | ks) != 0);
           }
-          const bool last = ++in_chunk == P.chunk || kb == KB - 1;
+          const bool last = ++in_chunk == P.chunk || end;
           if (last) ptx::mma_commit_pair_if(go, &ctl.tmem_full[acc], 0x3);
           ptx::mma_commit_pair_if(go, &ctl.empty[stage], 0x3);
           if (last) {
@@ -368,7 +401,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             stage = 0;
             phase ^= 1u;
           }
-        }
+          ++block;
+        };
+        // (the weight gradient's last stage by itself: with MMAs that depend on its rows
+        // in the loop, a stage took 740 cycles, 579 so)
+        for (int kb = 0; kb < KB - G::WG; ++kb)
+          stage_mmas(std::integral_constant<int, 64>{}, !G::WG && kb == KB - 1);
+        if (G::WG && KB > 0) stage_mmas(tl.rows - (KB - 1) * 64, true);
       }
     } else if (G::FP4 && warp == 1 && lane == 0) {
       // ---- odd CTA: a stage's scales are in place ----
@@ -425,118 +464,137 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             relay(stage);
         }
       }
-    } else if (G::FP4 && warp >= 2) {
-      // ---- scales: each lane two of the weight's 128 rows and four of the tile's 256, 16
-      // bytes (512 elements, two stages) of each at a time ----
-      // They come by asynchronous copies into a ring of the lane's own, kScaleChunks ahead and
-      // across tiles (held in registers one chunk ahead, their latency was in every
-      // chunk: 8192 x 7168 x 4096 155 us, 119 with the ring), and go from there to where
-      // the tensor core's copy takes them.
-      const int w = warp - 2;
+    } else if (G::FP4 && warp == 2) {
+      // ---- scales into shared memory, of the weight's 128 rows and the tile's 256, 32 bytes
+      // of a row (a chunk: 1024 elements, four stages) at a time, into a ring ----
+      // By TMA where rows of scales are whole 16 bytes (K a multiple of 512).  Loads by the
+      // warp's lanes, each a row, are as many requests as lanes, and slower than the MMAs
+      // (8192 x 7168 x 4096: 155 us from registers, 93-100 by asynchronous copies,
+      // 85 by TMA, 78 without any).  The warp that takes the scales from the ring is another
+      // one: its fence for the tensor core's reads would wait for copies in flight.
       const int KG = P.K / 32;
-      uint8_t* ring = tiles + G::STAGES * G::STAGE + 8 * kGrStaging + (w * 32 + lane) * 16;
-      constexpr int ROW = 64 * 16, CHUNK = 6 * ROW;  // a row of both warps' lanes, six of them
-      int ft = unit, fg = 0, fslot = 0;  // what is fetched next: tile, scale of K, slot
-      const uint8_t* src[6];             // its rows; null: no such row
-      auto rows = [&]() {
-        const GrTile tl = gr_tile(ctl, P, ft);
-#pragma unroll
-        for (int i = 0; i < 6; ++i) {
-          if (i < 2) {
-            const int n = tl.n0 + rank * 128 + (w * 2 + i) * 32 + lane;
-            src[i] = n < P.N ? P.w_scale + (static_cast<int64_t>(tl.e) * P.N + n) * KG : nullptr;
-          } else {
-            const int c = (w * 4 + i - 2) * 32 + lane;
-            src[i] = c < tl.T && tl.c0 + c < P.R ? P.x_scale + (tl.c0 + c) * KG : nullptr;
-          }
-        }
-      };
-      // (zeros for rows that are not there and past K, where the codes are zeros: 2^-127)
-      auto fetch = [&]() {
-        if (ft < total) {
-          uint8_t* dst = ring + fslot * CHUNK;
-#pragma unroll
-          for (int i = 0; i < 6; ++i) {
-            const uint8_t* from = src[i] != nullptr ? src[i] + fg : P.w_scale;
-            if (KG % 16 == 0) {
-              ptx::cp_async_16(dst + i * ROW, from, src[i] != nullptr ? 16 : 0);
-            } else if (KG % 4 == 0) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const bool in = src[i] != nullptr && fg + 4 * j < KG;
-                ptx::cp_async_4(dst + i * ROW + 4 * j, in ? from + 4 * j : P.w_scale, in ? 4 : 0);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t v = 0;
-                for (int q = 0; q < 4; ++q)
-                  if (src[i] != nullptr && fg + 4 * j + q < KG)
-                    v |= static_cast<uint32_t>(__ldg(from + 4 * j + q)) << (8 * q);
-                *reinterpret_cast<uint32_t*>(dst + i * ROW + 4 * j) = v;
-              }
-            }
-          }
-          fslot = fslot + 1 == kScaleChunks ? 0 : fslot + 1;
-          fg += 16;
-          if (fg >= KG) {
-            fg = 0;
-            ft += units;
-            if (ft < total) rows();
-          }
-        }
-        ptx::cp_async_commit();  // (of nothing, at the end: the count of groups stays)
-      };
-      if (ft < total) rows();
-#pragma unroll
-      for (int i = 0; i < kScaleChunks; ++i) fetch();
-      int stage = 0, slot = 0;
+      uint8_t* ring = tiles + G::STAGES * G::STAGE;
+      const uint32_t go = ptx::elect_one();
+      int slot = 0;
       uint32_t phase = 0;
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
-        const int KB = ceil_div(P.K, G::BK);
-        for (int kb = 0; kb < KB && ok; kb += 2) {
-          uint4 v[6];
-          ptx::cp_async_wait<kScaleChunks - 1>();
-#pragma unroll
-          for (int i = 0; i < 6; ++i)
-            v[i] = *reinterpret_cast<const uint4*>(ring + slot * CHUNK + i * ROW);
-          slot = slot + 1 == kScaleChunks ? 0 : slot + 1;
-          fetch();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (kb + h >= KB) break;
-            const bool got = dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
-            if (!__all_sync(0xffffffffu, got)) {
-              ok = false;
-              break;
+      for (int t = unit; t < total; t += units) {
+        const GrTile tl = warp_value(gr_tile(ctl, P, t));
+        const int n = tl.n0 + rank * 128;
+        for (int g = 0; g < KG; g += 32) {
+          dense_wait(&ctl.scales_empty[slot], phase ^ 1u, &ctl.abort, P.error_word);
+          uint8_t* dst = ring + slot * kScaleChunkBytes;
+          uint64_t* bar = &ctl.scales_full[slot];
+          if (KG % 16 == 0) {
+            // (rows and scales that are not there are read as zeros, 2^-127; past K the codes
+            // are zeros too)
+            ptx::mbar_arrive_expect_tx_if(go, bar, tl.T > 128 ? 12288 : 8192);
+            ptx::tma_load_3d_if(go, dst, &maps.sa, bar, g, n, tl.e);
+            ptx::tma_load_2d_if(go, dst + 4096, &maps.sb, bar, g, static_cast<int>(tl.c0));
+            if (tl.T > 128)
+              ptx::tma_load_2d_if(go, dst + 8192, &maps.sb, bar, g, static_cast<int>(tl.c0) + 128);
+          } else {
+            for (int i = lane; i < 384 * 2; i += 32) {
+              const int row = i >> 1, col = g + (i & 1) * 16;
+              const bool of_w = row < 128;
+              const bool in = of_w ? n + row < P.N
+                                   : row - 128 < tl.T && tl.c0 + (row - 128) < P.R;
+              const uint8_t* from =
+                  of_w ? P.w_scale + (static_cast<int64_t>(tl.e) * P.N + n + row) * KG + col
+                       : P.x_scale + (tl.c0 + (row - 128)) * KG + col;
+              uint32_t v[4] = {};
+              if (in) {
+                for (int j = 0; j < 4; ++j) {
+                  if (KG % 4 == 0) {
+                    if (col + 4 * j < KG) v[j] = __ldg(reinterpret_cast<const uint32_t*>(from) + j);
+                  } else {
+                    for (int q = 0; q < 4; ++q)
+                      if (col + 4 * j + q < KG)
+                        v[j] |= static_cast<uint32_t>(__ldg(from + 4 * j + q)) << (8 * q);
+                  }
+                }
+              }
+              *reinterpret_cast<uint4*>(dst + (row >> 5) * 1024 + scale_place(row & 31, i & 1)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
             }
-            uint8_t* sc = tiles + stage * G::STAGE + 32768 + lane * 16;
-#pragma unroll
-            for (int i = 0; i < 6; ++i) {
-              uint8_t* at = i < 2 ? sc + (w * 2 + i) * 4 : sc + 1024 + w * 512 + (i - 2) * 4;
-              const int next = i < 2 ? 512 : 1024;  // the second 128 elements of the stage
-              *reinterpret_cast<uint32_t*>(at) = h == 0 ? v[i].x : v[i].z;
-              *reinterpret_cast<uint32_t*>(at + next) = h == 0 ? v[i].y : v[i].w;
-            }
-            ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(rank == 0 ? &ctl.full[stage] : &ctl.tail[stage]);
-            if (++stage == G::STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
+            ptx::mbar_arrive_if(go, bar);
+          }
+          if (++slot == kScaleChunks) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
       }
-      ptx::cp_async_wait<0>();
+    } else if (G::FP4 && warp == 3) {
+      // ---- and on to where the tensor core's copy takes them: there, 16 bytes are 128
+      // elements' scales of a lane's four rows ----
+      const uint8_t* ring = tiles + G::STAGES * G::STAGE;
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, slot_phase = 0;
+      bool ok = true;
+      const int KB = ceil_div(P.K, G::BK);
+      for (int t = unit; t < total && ok; t += units) {
+        for (int kb = 0; kb < KB && ok; kb += 4) {
+          bool got = dense_wait(&ctl.scales_full[slot], slot_phase, &ctl.abort, P.error_word);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int b = 0; b < 4; b += 2) {  // two stages: 16 bytes of a row
+            if (kb + b >= KB) break;
+            uint32_t v[12][4];
+#pragma unroll
+            for (int i = 0; i < 12; ++i) {
+              const uint4 u = *reinterpret_cast<const uint4*>(
+                  ring + slot * kScaleChunkBytes + i * 1024 + scale_place(lane, b >> 1));
+              v[i][0] = u.x;
+              v[i][1] = u.y;
+              v[i][2] = u.z;
+              v[i][3] = u.w;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (kb + b + h >= KB) break;
+              got = dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
+              if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+              }
+              uint8_t* sc = tiles + stage * G::STAGE + 32768 + lane * 16;
+#pragma unroll
+              for (int a = 0; a < 3; ++a)  // the weight's rows, the tile's first 128, its others
+#pragma unroll
+                for (int ka = 0; ka < 2; ++ka) {
+                  const int k = 2 * h + ka;
+                  *reinterpret_cast<uint4*>(
+                      sc + (a == 0 ? ka * 512 : 1024 + ka * 1024 + (a - 1) * 512)) =
+                      make_uint4(v[4 * a][k], v[4 * a + 1][k], v[4 * a + 2][k], v[4 * a + 3][k]);
+                }
+              ptx::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(rank == 0 ? &ctl.full[stage] : &ctl.tail[stage]);
+              if (++stage == G::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+            if (!ok) break;
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl.scales_empty[slot]);
+          if (++slot == kScaleChunks) {
+            slot = 0;
+            slot_phase ^= 1u;
+          }
+        }
+      }
     }
   } else {
     // ---- output: 32 columns n of the weight (lanes) by half of the tile's columns a warp ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGrRegsMany));
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tmem_empty[0]), 0);
-    uint8_t* staging = tiles + G::STAGES * G::STAGE + (warp - 4) * kGrStaging;
     uint32_t acc = 0, turn = 0;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
@@ -581,69 +639,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
         turn ^= acc == 0 ? 1u : 0u;
       }
       if (!ok) break;
-      // 16 rows by the warp's 32 columns at a time through its staging block and out in
-      // 16-byte stores (each lane storing its own column's elements, one warp's store 64 or
-      // 128 bytes, took 60 of 1210 us at 8 x 1024 rows, K 4096, N 28672, and 170 of 880 us
-      // in the weight gradient of 8 x 1024 rows, 14336 x 4096)
+      // a warp's store is 32 neighbouring columns of one row (through shared memory and out
+      // in 16-byte stores: the same times; the MMAs' operands take half of its bandwidth)
       const int first = part * groups * 16;
       const int64_t row0 = (G::WG ? static_cast<int64_t>(tl.e) * P.K : 0) + tl.c0 + first;
       const int left = min(tl.cols - first, groups * 16);
-      const int nw = tl.n0 + rank * 128 + q * 32;  // the warp's first column
-      auto put = [&](auto* out) {
+      auto put = [&](auto* out, auto add) {
         using O = std::remove_pointer_t<decltype(out)>;
-        constexpr bool F32 = sizeof(O) == 4;
-        constexpr int PER = 16 / sizeof(O);        // elements of a store
-        constexpr int LANES = 32 / PER;            // lanes of a row
-        constexpr int STEP = 32 / LANES;           // rows of a store
-        const int ln = lane % LANES * PER, lr = lane / LANES;
-        O* dst = out + (row0 + lr) * P.N + nw + ln;
-        const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+        O* p = out + row0 * P.N + n;
+        auto row = [&](int c) { return p + static_cast<int64_t>(c) * P.N; };
+        auto store = [&](int i, auto whole) {
+          constexpr bool WHOLE = decltype(whole)::value;
+          [[maybe_unused]] float old[16];
+          if constexpr (decltype(add)::value) {
 #pragma unroll
-        for (int i = 0; i < G::TM / 32; ++i) {
-          if (16 * i >= left) break;
-          __syncwarp();
+            for (int j = 0; j < 16; ++j)
+              old[j] = WHOLE || 16 * i + j < left ? static_cast<float>(*row(16 * i + j)) : 0.f;
+          }
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
             float2 o = unpair(sum[8 * i + j / 2]);
-            if (!F32 && G::WG && P.accumulate && nw + lane < P.N) {  // (added before it is rounded)
-              const O* old = out + (row0 + 16 * i + j) * P.N + nw + lane;
-              if (16 * i + j < left) o.x += static_cast<float>(old[0]);
-              if (16 * i + j + 1 < left) o.y += static_cast<float>(old[P.N]);
+            if constexpr (decltype(add)::value) {
+              o.x += old[j];
+              o.y += old[j + 1];
             }
-            if constexpr (F32) {
-              *reinterpret_cast<float*>(staging + j * 128 + lane * 4) = o.x;
-              *reinterpret_cast<float*>(staging + j * 128 + 128 + lane * 4) = o.y;
-            } else {
-              // row j of two columns in even lanes, row j + 1 of them in odd ones
-              const uint32_t mine = pack2(o.x, o.y), other = __shfl_xor_sync(0xffffffffu, mine, 1);
-              *reinterpret_cast<uint32_t*>(staging + (j + (lane & 1)) * 64 + (lane & ~1) * 2) =
-                  __byte_perm(mine, other, sel);
-            }
+            if (WHOLE || 16 * i + j < left) *row(16 * i + j) = static_cast<O>(o.x);
+            if (WHOLE || 16 * i + j + 1 < left) *row(16 * i + j + 1) = static_cast<O>(o.y);
           }
-          __syncwarp();
-          if (nw + ln < P.N) {  // (N is a multiple of 8)
+        };
 #pragma unroll
-            for (int r = 0; r < 16; r += STEP) {
-              if (16 * i + r + lr < left) {
-                uint4 v = *reinterpret_cast<const uint4*>(staging + r * 32 * sizeof(O) + lane * 16);
-                uint4* at = reinterpret_cast<uint4*>(dst + static_cast<int64_t>(16 * i + r) * P.N);
-                if (F32 && G::WG && P.accumulate) {
-                  const uint4 old = *at;
-                  v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(old.x));
-                  v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(old.y));
-                  v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(old.z));
-                  v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(old.w));
-                }
-                *at = v;
-              }
-            }
-          }
+        for (int i = 0; i < G::TM / 32; ++i) {
+          if (16 * i >= left) break;
+          if (16 * i + 16 <= left)
+            store(i, std::true_type{});
+          else
+            store(i, std::false_type{});
         }
       };
-      if (P.out_f32)
-        put(static_cast<float*>(P.out));
-      else
-        put(static_cast<bf16*>(P.out));
+      auto put_as = [&](auto* out) {
+        if constexpr (G::WG) {
+          if (P.accumulate) {
+            put(out, std::true_type{});
+            return;
+          }
+        }
+        put(out, std::false_type{});
+      };
+      if (n < P.N) {
+        if (P.out_f32)
+          put_as(static_cast<float*>(P.out));
+        else
+          put_as(static_cast<bf16*>(P.out));
+      }
+      __syncwarp();
     }
   }
   __syncwarp();
@@ -676,9 +724,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
 int gr_chunk(const GroupedProductArgs& a) { return a.out_f32 ? 8 : 1 << 30; }
 
 template <int MODE>
-moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const CUtensorMap& tmA,
-                            const CUtensorMap& tmB, const CUtensorMap& tmB16, int64_t tiles,
-                            cudaStream_t s) {
+moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const GrMaps& maps,
+                            int64_t tiles, cudaStream_t s) {
   using G = GrGeo<MODE>;
   static PerDevice attr;
   int regs = 0;
@@ -715,7 +762,7 @@ moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const
   P.error_word = a.error_word;
   const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, a.num_sms / 2));
   prof_before(name, s);
-  launch_kernel(grouped_kernel<MODE>, grid, kGrThreads, G::SMEM, s, tmA, tmB, tmB16, P);
+  launch_kernel(grouped_kernel<MODE>, grid, kGrThreads, G::SMEM, s, maps, P);
   prof_after(name, s);
   return check_launch(name);
 }
@@ -726,17 +773,19 @@ int64_t product_tiles(const GroupedProductArgs& a, int TM) {
 }
 
 moe_status_t map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch,
-                    uint32_t box_cols, uint32_t box_rows, CUtensorMapDataType type) {
+                    uint32_t box_cols, uint32_t box_rows, CUtensorMapDataType type,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const uint64_t d[2] = {cols, rows}, st[1] = {pitch};
   const uint32_t box[2] = {box_cols, box_rows};
-  return encode_tensor_map(m, base, 2, d, st, box, type, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_tensor_map(m, base, 2, d, st, box, type, swizzle);
 }
 moe_status_t map_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t mats,
                     uint64_t pitch, uint32_t box_cols, uint32_t box_rows,
-                    CUtensorMapDataType type) {
+                    CUtensorMapDataType type,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const uint64_t d[3] = {cols, rows, mats}, st[2] = {pitch, pitch * rows};
   const uint32_t box[3] = {box_cols, box_rows, 1};
-  return encode_tensor_map(m, base, 3, d, st, box, type, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_tensor_map(m, base, 3, d, st, box, type, swizzle);
 }
 
 constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -746,34 +795,43 @@ constexpr auto kBytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 
 moe_status_t launch_grouped_matmul(const GroupedProductArgs& a, cudaStream_t s) {
   const uint64_t K = a.K, N = a.N, E = a.E, R = static_cast<uint64_t>(a.R);
-  CUtensorMap tmA, tmB, tmB16;
-  if (moe_status_t st = a.transposed ? map_3d(&tmA, a.w, K, N, E, 2 * K, 64, 128, kBf16)
-                                     : map_3d(&tmA, a.w, N, K, E, 2 * N, 64, 64, kBf16))
+  GrMaps m;
+  if (moe_status_t st = a.transposed ? map_3d(&m.a, a.w, K, N, E, 2 * K, 64, 128, kBf16)
+                                     : map_3d(&m.a, a.w, N, K, E, 2 * N, 64, 64, kBf16))
     return st;
-  if (moe_status_t st = map_2d(&tmB, a.x, K, R, 2 * K, 64, 128, kBf16)) return st;
-  if (moe_status_t st = map_2d(&tmB16, a.x, K, R, 2 * K, 64, 16, kBf16)) return st;
+  if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, 128, kBf16)) return st;
+  if (moe_status_t st = map_2d(&m.b16, a.x, K, R, 2 * K, 64, 16, kBf16)) return st;
   const int64_t tiles = product_tiles(a, 256);
   return a.transposed
-             ? launch_grouped<kProductT>("grouped_matmul_t", a, tmA, tmB, tmB16, tiles, s)
-             : launch_grouped<kProduct>("grouped_matmul", a, tmA, tmB, tmB16, tiles, s);
+             ? launch_grouped<kProductT>("grouped_matmul_t", a, m, tiles, s)
+             : launch_grouped<kProduct>("grouped_matmul", a, m, tiles, s);
 }
 
 moe_status_t launch_grouped_weight_grad(const GroupedProductArgs& a, cudaStream_t s) {
   const uint64_t K = a.K, N = a.N, R = static_cast<uint64_t>(a.R);
-  CUtensorMap tmA, tmB;
-  if (moe_status_t st = map_2d(&tmA, a.w, N, R, 2 * N, 64, 64, kBf16)) return st;
-  if (moe_status_t st = map_2d(&tmB, a.x, K, R, 2 * K, 64, 64, kBf16)) return st;
+  GrMaps m;
+  if (moe_status_t st = map_2d(&m.a, a.w, N, R, 2 * N, 64, 64, kBf16)) return st;
+  if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, 64, kBf16)) return st;
+  m.b16 = m.b;
   const int64_t tiles = int64_t(a.E) * ceil_div(a.K, 256) * ceil_div(a.N, 256);
-  return launch_grouped<kWeightGrad>("grouped_weight_grad", a, tmA, tmB, tmB, tiles, s);
+  return launch_grouped<kWeightGrad>("grouped_weight_grad", a, m, tiles, s);
 }
 
 moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s) {
   const uint64_t KB = a.K / 2, N = a.N, E = a.E, R = static_cast<uint64_t>(a.R);
-  CUtensorMap tmA, tmB, tmB16;
-  if (moe_status_t st = map_3d(&tmA, a.w, KB, N, E, KB, 128, 128, kBytes)) return st;
-  if (moe_status_t st = map_2d(&tmB, a.x, KB, R, KB, 128, 112, kBytes)) return st;
-  if (moe_status_t st = map_2d(&tmB16, a.x, KB, R, KB, 128, 16, kBytes)) return st;
-  return launch_grouped<kFp4>("matmul_fp4", a, tmA, tmB, tmB16, product_tiles(a, 224), s);
+  GrMaps m;
+  if (moe_status_t st = map_3d(&m.a, a.w, KB, N, E, KB, 128, 128, kBytes)) return st;
+  if (moe_status_t st = map_2d(&m.b, a.x, KB, R, KB, 128, 112, kBytes)) return st;
+  if (moe_status_t st = map_2d(&m.b16, a.x, KB, R, KB, 128, 16, kBytes)) return st;
+  if (a.K % 512 == 0) {  // (rows of whole 16 bytes)
+    const uint64_t KG = a.K / 32;
+    const auto s32 = CU_TENSOR_MAP_SWIZZLE_32B;
+    if (moe_status_t st = map_3d(&m.sa, a.w_scale, KG, N, E, KG, 32, 128, kBytes, s32)) return st;
+    if (moe_status_t st = map_2d(&m.sb, a.x_scale, KG, R, KG, 32, 128, kBytes, s32)) return st;
+  } else {
+    m.sa = m.sb = m.b;
+  }
+  return launch_grouped<kFp4>("matmul_fp4", a, m, product_tiles(a, 224), s);
 }
 
 }  // namespace gbmoe
