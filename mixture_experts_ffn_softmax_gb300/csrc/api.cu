@@ -1286,10 +1286,8 @@ moe_status_t moe_swiglu(const void* gate_up, const float* row_weights, int64_t R
   if (!gate_up || !z) return set_error(MOE_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(gate_up) || !aligned16(z) || !aligned_to(row_weights, 4))
     return set_error(MOE_ERR_INVALID_ARG, "gate_up and z must be 16-byte aligned");
-  int sms = 0;
-  if (moe_status_t st = check_device(&sms)) return st;
-  const SwigluArgs a{static_cast<const bf16*>(gate_up), row_weights, R, I, static_cast<bf16*>(z),
-                     sms};
+  if (moe_status_t st = check_device(nullptr)) return st;
+  const SwigluArgs a{static_cast<const bf16*>(gate_up), row_weights, R, I, static_cast<bf16*>(z)};
   return launch_swiglu(a, stream);
 }
 

@@ -169,7 +169,6 @@ struct SwigluArgs {
   int64_t R;
   int32_t I;
   bf16* z;               // [R, I]
-  int32_t num_sms;
 };
 moe_status_t launch_swiglu(const SwigluArgs& a, cudaStream_t s);
 struct SwigluBackwardArgs {

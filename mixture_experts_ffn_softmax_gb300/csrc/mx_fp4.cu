@@ -16,12 +16,16 @@
 namespace gbmoe {
 namespace {
 
-constexpr int kQ4Threads = 256, kQ4Blocks = 4;  // threads of a block, blocks of an SM
+constexpr int kQ4Threads = 256;
+constexpr int quant4_blocks(bool swiglu) { return swiglu ? 3 : 4; }  // resident blocks of an SM
 
 // Four lanes per block of 32, 8 columns per lane.  Rows are whole blocks, so that x, the
-// codes and the scales are taken as flat arrays; only gate and up are apart by row.
+// codes and the scales are taken as flat arrays; only gate and up are apart by row.  Bound:
+// HBM for a tensor (8192 x 7168 with the values 43.7 us, 6.1 TB/s), issue slots for SiLU(gate) *
+// up, whose next loads are in flight while it works (8191 x 2048 with the values: 20.6 us, 22.0
+// without; a tensor 46.9 with them ahead and three blocks, 43.7 in four without).
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kQ4Threads, kQ4Blocks)
+__global__ void __launch_bounds__(kQ4Threads, quant4_blocks(SWIGLU))
     quant_mx_fp4_kernel(const bf16* __restrict__ x, int64_t M, int K, uint8_t* __restrict__ q4,
                         uint8_t* __restrict__ scale, bf16* __restrict__ values) {
   pdl_begin();
@@ -38,17 +42,16 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4Blocks)
     step_row = threads / per;
     step_unit = static_cast<int>(threads - step_row * per);
   }
-  // (whole warps stay in the loop for the shuffles)
-  for (int64_t base = first - (threadIdx.x & 31); base < total; base += U * threads) {
-    uint4 a[U], b[SWIGLU ? U : 1];
+  uint4 na[U], nb[SWIGLU ? U : 1];
+  auto load = [&](int64_t base) {  // (SWIGLU: of the units that follow those loaded last)
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t f = base + (threadIdx.x & 31) + i * threads;
       const bool in = f < total;
       if constexpr (SWIGLU) {
         const bf16* src = x + row * 2 * K + unit * 8;
-        a[i] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-        b[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + K)) : make_uint4(0, 0, 0, 0);
+        na[i] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        nb[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + K)) : make_uint4(0, 0, 0, 0);
         row += step_row;
         unit += step_unit;
         if (unit >= per) {
@@ -56,9 +59,22 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4Blocks)
           ++row;
         }
       } else {
-        a[i] = in ? __ldg(reinterpret_cast<const uint4*>(x + f * 8)) : make_uint4(0, 0, 0, 0);
+        na[i] = in ? __ldg(reinterpret_cast<const uint4*>(x + f * 8)) : make_uint4(0, 0, 0, 0);
       }
     }
+  };
+  const int64_t base0 = first - (threadIdx.x & 31);
+  if constexpr (SWIGLU) load(base0);
+  // (whole warps stay in the loop for the shuffles)
+  for (int64_t base = base0; base < total; base += U * threads) {
+    uint4 a[U], b[SWIGLU ? U : 1];
+    if constexpr (!SWIGLU) load(base);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      a[i] = na[i];
+      if constexpr (SWIGLU) b[i] = nb[i];
+    }
+    if constexpr (SWIGLU) load(base + U * threads);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t f = base + (threadIdx.x & 31) + i * threads;
@@ -121,7 +137,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4Blocks)
 moe_status_t launch_quant_mx_fp4(const QuantMxFp4Args& a, cudaStream_t s) {
   const int64_t units = a.M * (a.K / 8);
   const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>(ceil_div<int64_t>(units, kQ4Threads), int64_t(a.num_sms) * kQ4Blocks));
+      std::min<int64_t>(ceil_div<int64_t>(units, kQ4Threads), int64_t(a.num_sms) * quant4_blocks(a.swiglu)));
   prof_before("quant_mx_fp4", s);
   launch_kernel(a.swiglu ? quant_mx_fp4_kernel<true> : quant_mx_fp4_kernel<false>, grid, kQ4Threads,
                 0, s, a.x, a.M, a.K, a.q4, a.scale, a.values);
