@@ -510,9 +510,9 @@ GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const
  *  expert_offsets  device int32 [E + 1], ascending from >= 0 to <= R; experts
  *                  may have no rows.  Rows of x outside all groups take no part;
  *                  rows of out outside all groups are not written.  Offsets that
- *                  descend or leave 0..R are clipped to it and set the error word to
- *                  MOE_ERR_INVALID_ARG (what the rows then hold is not defined, but
- *                  nothing outside the tensors is read or written).
+ *                  descend or leave 0..R set the error word to MOE_ERR_INVALID_ARG;
+ *                  they are clipped to 0..R and to the ends of the experts before, so
+ *                  that no row is computed twice.
  *  error_word      device int32 or NULL; also MOE_ERR_TIMEOUT if a pipeline wait ran
  *                  out of time (the output is then incomplete)
  * Results do not depend on timing.  out must not overlap the inputs; operands, bias,

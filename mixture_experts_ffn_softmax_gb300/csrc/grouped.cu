@@ -78,6 +78,15 @@ struct GrCtl {
 };
 static_assert(GrGeo<kFp4>::SMEM + sizeof(GrCtl<kFp4>) <= 232448, "shared memory budget");
 
+// dense_wait, which also ends at once where a wait of this CTA has run out: the loops of the
+// loading and issuing warps go on to the tile's end then.
+__device__ __forceinline__ bool gr_wait(uint64_t* bar, uint32_t parity, int32_t* abort,
+                                        int32_t* err) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  if (*reinterpret_cast<volatile int32_t*>(abort)) return false;
+  return dense_wait(bar, parity, abort, err);
+}
+
 struct GrParams {
   const int32_t* offsets;  // [E + 1], or null: all R rows are expert 0's
   int64_t R;
@@ -237,22 +246,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
   }
   const int nt = ceil_div(P.N, 256);
   if (warp == 2) {
-    // the experts' rows, clipped to the R there are, and their tiles
+    // the experts' rows and their tiles.  Offsets are clipped to the R rows there are, and to
+    // the ends of the experts before: whatever they hold, no two experts share a row.
     int total = 0;
+    const int R = static_cast<int>(P.R);
+    int end = 0;  // of the experts before
     for (int e0 = 0; e0 < P.E; e0 += 32) {
       const int e = e0 + lane;
-      int n = 0;
+      int n = 0, b0 = 0, c0 = R;
+      if (P.offsets != nullptr && e < P.E) {
+        b0 = __ldg(P.offsets + e);
+        c0 = __ldg(P.offsets + e + 1);
+      }
+      int ends = e < P.E ? min(max(c0, 0), R) : 0;  // the largest of this lane's and those before
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, ends, o);
+        if (lane >= o) ends = max(ends, v);
+      }
+      int before = __shfl_up_sync(0xffffffffu, ends, 1);
+      before = max(end, lane > 0 ? before : 0);
+      end = max(end, __shfl_sync(0xffffffffu, ends, 31));
       if (e < P.E) {
-        int64_t b = 0, c = P.R;
-        if (P.offsets != nullptr) {
-          const int64_t b0 = __ldg(P.offsets + e), c0 = __ldg(P.offsets + e + 1);
-          b = min(max(b0, int64_t(0)), P.R);
-          c = min(max(c0, b), P.R);
-          if (b != b0 || c != c0) record_error(P.error_word, MOE_ERR_INVALID_ARG);
-        }
-        ctl.start[e] = static_cast<int32_t>(b);
-        ctl.count[e] = static_cast<int32_t>(c - b);
-        n = ceil_div(static_cast<int>(c - b), G::TM) * nt;
+        const int b = max(min(max(b0, 0), R), before);
+        const int c = max(min(max(c0, 0), R), b);
+        if (b != b0 || c != c0) record_error(P.error_word, MOE_ERR_INVALID_ARG);
+        ctl.start[e] = b;
+        ctl.count[e] = c - b;
+        n = ceil_div(c - b, G::TM) * nt;
       }
       if constexpr (!G::WG) {
         int sum = n;
@@ -281,7 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
     // branch of one lane an MMA took 70 cycles to issue, the loop 730 for the 512 that a stage
     // of 256 columns computes.  8 x 1024 rows, K 4096, N 28672: 1193 us so, 1077 as here;
     // the weight gradient of 128 x 1024 rows, 2048 x 1536: 726 and 597.  A wait that ran out
-    // does not end a loop: once it has, all others end at once, and the loop runs out.)
+    // does not end a loop before its tile's end: all others end at once then.)
+    auto aborted = [&]() { return warp_value(*reinterpret_cast<volatile int32_t*>(&ctl.abort)) != 0; };
     if (warp == 0) {
       // ---- loads ----
       const uint32_t go = ptx::elect_one();
@@ -291,14 +313,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       int64_t blocks = 0;
       const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(&ctl.full[0]), 0);
       const uint32_t tail0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tail[0]), rank);
-      for (int t = unit; t < total; t += units) {
+      for (int t = unit; t < total && !aborted(); t += units) {
         const GrTile tl = warp_value(gr_tile(ctl, P, t));
         const int KB = gr_blocks<MODE>(P, tl);
         const int half = tl.T / 2;
         const int n = tl.n0 + rank * 128, c = static_cast<int>(tl.c0) + rank * half;
         const uint32_t bytes = 16384u + static_cast<uint32_t>(half) * 128u;
         for (int kb = 0; kb < KB; ++kb) {
-          dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
+          gr_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
           const uint32_t sa = tiles0 + stage * G::STAGE, sb = sa + 16384;
           // both CTAs' copies complete on the even CTA's barrier
           uint32_t bar = full0 + stage * 8;
@@ -355,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       constexpr uint32_t A_LO = (G::A_MN ? 512u : 1u) << 16, B_LO = (G::WG ? 512u : 1u) << 16;
       int stage = 0;
       uint32_t phase = 0, acc = 0, turn = 0, block = 0;
-      for (int t = unit; t < total; t += units) {
+      for (int t = unit; t < total && !aborted(); t += units) {
         const GrTile tl = warp_value(gr_tile(ctl, P, t));
         const int KB = gr_blocks<MODE>(P, tl);
         const uint32_t idesc = ptx::idesc_bf16_f32(256, tl.T, G::A_MN, G::WG);
@@ -364,8 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
         auto stage_mmas = [&](auto rows, bool end) {
           [[maybe_unused]] const int steps = rows;
           if (in_chunk == 0)
-            dense_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word);
-          dense_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word);
+            gr_wait(&ctl.tmem_empty[acc], turn ^ 1u, &ctl.abort, P.error_word);
+          gr_wait(&ctl.full[stage], phase, &ctl.abort, P.error_word);
           ptx::tc_fence_after();
           const uint32_t sa = tiles0 + stage * G::STAGE;
           const uint32_t a = (sa >> 4) + A_LO, b = ((sa + 16384) >> 4) + B_LO;
@@ -417,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       for (int t = unit; t < total && ok; t += units) {
         const int KB = gr_blocks<MODE>(P, gr_tile(ctl, P, t));
         for (int kb = 0; kb < KB; ++kb) {
-          if (!dense_wait(&ctl.tail[stage], phase, &ctl.abort, P.error_word)) {
+          if (!gr_wait(&ctl.tail[stage], phase, &ctl.abort, P.error_word)) {
             ok = false;
             break;
           }
@@ -441,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
         if (tl.rows % 16 == 0) continue;
         const int stage = static_cast<int>((block - 1) % G::STAGES);
         const bool got =
-            dense_wait(&ctl.tail[stage], parity >> stage & 1u, &ctl.abort, P.error_word);
+            gr_wait(&ctl.tail[stage], parity >> stage & 1u, &ctl.abort, P.error_word);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
@@ -477,11 +499,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       const uint32_t go = ptx::elect_one();
       int slot = 0;
       uint32_t phase = 0;
-      for (int t = unit; t < total; t += units) {
+      for (int t = unit; t < total && !aborted(); t += units) {
         const GrTile tl = warp_value(gr_tile(ctl, P, t));
         const int n = tl.n0 + rank * 128;
         for (int g = 0; g < KG; g += 32) {
-          dense_wait(&ctl.scales_empty[slot], phase ^ 1u, &ctl.abort, P.error_word);
+          gr_wait(&ctl.scales_empty[slot], phase ^ 1u, &ctl.abort, P.error_word);
           uint8_t* dst = ring + slot * kScaleChunkBytes;
           uint64_t* bar = &ctl.scales_full[slot];
           if (KG % 16 == 0) {
@@ -535,7 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       const int KB = ceil_div(P.K, G::BK);
       for (int t = unit; t < total && ok; t += units) {
         for (int kb = 0; kb < KB && ok; kb += 4) {
-          bool got = dense_wait(&ctl.scales_full[slot], slot_phase, &ctl.abort, P.error_word);
+          bool got = gr_wait(&ctl.scales_full[slot], slot_phase, &ctl.abort, P.error_word);
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             break;
@@ -556,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (kb + b + h >= KB) break;
-              got = dense_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
+              got = gr_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
               if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
@@ -609,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
 #pragma unroll
       for (int j = 0; j < 64; ++j) sum[j] = pair_of(b, b);
       for (int kb = 0; kb < KB; kb += P.chunk) {
-        const bool got = dense_wait(&ctl.tmem_full[acc], turn, &ctl.abort, P.error_word);
+        const bool got = gr_wait(&ctl.tmem_full[acc], turn, &ctl.abort, P.error_word);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;

@@ -105,6 +105,25 @@ def test_product_of_many_experts_and_ragged_rows():
     assert torch.equal(pkg.moe_grouped_matmul(x, w, off, out=out), reference(x, w, off, out * 0))
 
 
+@pytest.mark.parametrize("transposed", [False, True])
+def test_product_of_many_tiles_per_expert(transposed):
+    """Rows and columns past a raster group of 8 row tiles, twice round every pair."""
+    counts, K, N = [2400, 0, 70, 4500], 136, 1288
+    x, off = ints(1, sum(counts), K), offsets_of(counts)
+    w = ints(2, 4, N, K) if transposed else ints(2, 4, K, N)
+    out = torch.zeros(len(x), N, device="cuda")
+    assert torch.equal(pkg.moe_grouped_matmul(x, w, off, transposed=transposed, out=out),
+                       reference(x, w, off, out * 0, transposed))
+
+
+def test_weight_grad_of_many_tiles_per_expert():
+    counts, K, N = [40, 0, 65, 700], 2312, 1032
+    x, dy, off = ints(1, sum(counts), K), ints(2, sum(counts), N), offsets_of(counts)
+    for dt in (F32, BF16):
+        assert torch.equal(pkg.moe_grouped_weight_grad(x, dy, off, out_dtype=dt),
+                           weight_reference(x, dy, off).to(dt))
+
+
 def test_product_rows_do_not_touch_each_other():
     """A row's NaN or infinity stays in its own output row, an expert's weight in
     its own rows."""
@@ -143,7 +162,8 @@ def test_empty_calls():
     assert (rest == 3).all()
 
 
-@pytest.mark.parametrize("bad", [[0, 5, 3, 8], [-2, 3, 4, 8], [0, 3, 4, 9], [4, 3, 2, 1]])
+@pytest.mark.parametrize("bad", [[0, 5, 3, 8], [-2, 3, 4, 8], [0, 3, 4, 9], [4, 3, 2, 1],
+                                 [0, 8, 0, 8], [-2 ** 31, 2 ** 31 - 1, 5, 2 ** 31 - 1]])
 def test_offsets_out_of_order_or_range_set_the_error_word(bad):
     x, w, dy = ints(1, 8, 64), ints(2, 3, 64, 32), ints(3, 8, 32)
     off = torch.tensor(bad, dtype=torch.int32, device="cuda")
@@ -151,9 +171,22 @@ def test_offsets_out_of_order_or_range_set_the_error_word(bad):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     pkg.moe_grouped_matmul(x, w, off, out=guard[1], error_word=err)
     assert err.item() == 1 and (guard[0] == 7).all() and (guard[2] == 7).all()
+    # clipped to the rows there are and to the ends of the experts before
+    groups, end = [], 0
+    for a, b in zip(bad, bad[1:]):
+        a = max(min(max(a, 0), 8), end)
+        b = max(min(max(b, 0), 8), a)
+        end = max(end, b)
+        groups.append((a, b))
+    ref = torch.full((8, 32), 7.0, device="cuda", dtype=torch.float64)
+    for e, (a, b) in enumerate(groups):
+        ref[a:b] = x[a:b].double() @ w[e].double()
+    assert torch.equal(guard[1].double(), ref)
     err.zero_()
-    pkg.moe_grouped_weight_grad(x, dy, off, error_word=err)
+    g = pkg.moe_grouped_weight_grad(x, dy, off, error_word=err)
     assert err.item() == 1
+    for e, (a, b) in enumerate(groups):
+        assert torch.equal(g[e].double(), x[a:b].double().t() @ dy[a:b].double())
 
 
 # ---------------------------------------------------------- weight gradient --

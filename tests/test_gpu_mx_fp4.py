@@ -167,6 +167,17 @@ def test_grouped_product_exact(counts, K, N):
                                       torch.full_like(out, 7.0)).float())
 
 
+@pytest.mark.parametrize("K", [512, 800])
+def test_grouped_product_of_many_tiles_per_expert(K):
+    counts, N = [2000, 0, 70, 4100], 1288
+    off = offsets_of(counts)
+    a, sa = codes(1, (sum(counts),), K)
+    w, sw = codes(3, (4, N), K)
+    out = torch.zeros(len(a), N, device="cuda")
+    assert torch.equal(pkg.moe_matmul_fp4(a, sa, w, sw, off, out=out),
+                       reference(values64(a, sa), values64(w, sw), off.tolist(), out * 0).float())
+
+
 def test_product_every_scale():
     """Scales over their range, of either operand, the other 1: products of normal
     fp32 size scale exactly."""
