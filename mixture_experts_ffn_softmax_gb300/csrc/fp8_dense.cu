@@ -552,12 +552,6 @@ static_assert(DsGeo<16>::SMEM + sizeof(DsCtl<16>) <= 232448 &&
                   DsGeo<128>::SMEM + sizeof(DsCtl<128>) <= 232448,
               "shared memory budget");
 
-__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
-               "f"(c), "f"(d)
-               : "memory");
-}
-
 template <int T, bool TR>
 __global__ void __launch_bounds__(kDsThreads, 1)
     dense_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA,

@@ -35,18 +35,24 @@ constexpr int kGrRegsLaunch = 168, kGrRegsFew = 88, kGrRegsMany = 208;
 static_assert(128 * kGrRegsFew + 256 * kGrRegsMany <= kGrThreads * kGrRegsLaunch,
               "register split within the launch's registers");
 
-template <int MODE>
+// SPLIT: for up to 32 rows in all, K in parts over the pairs of a cluster.
+constexpr int kGrSplitRows = 32, kGrMaxParts = 4;
+template <int MODE, bool SPLIT = false>
 struct GrGeo {
   static constexpr bool FP4 = MODE == kFp4, WG = MODE == kWeightGrad;
   static constexpr bool A_MN = MODE == kProduct || WG;  // MN-major first operand
   static constexpr int BK = FP4 ? 256 : 64;    // reduced elements of a stage (128 bytes of a row)
   // columns of a tile; FP4: two accumulators and the scales share the 512 TMEM columns
-  static constexpr int TM = FP4 ? 224 : 256;
+  static constexpr int TM = SPLIT ? kGrSplitRows : FP4 ? 224 : 256;
+  static constexpr int ACC = FP4 ? 224 : 256;  // TMEM columns from one accumulator to the other
   static constexpr int SCALES = FP4 ? 3072 : 0;  // of a stage: 128 + 256 rows by 8 bytes
-  static constexpr int STAGE = 32768 + SCALES;
-  static constexpr int STAGES = FP4 ? 5 : 6;
-  static constexpr size_t SMEM =
-      1024 + STAGES * STAGE + (FP4 ? kScaleChunks * kScaleChunkBytes : 0);
+  static constexpr int SCALES_AT = SPLIT ? 18432 : 32768;  // A, then TM / 2 rows or columns of B
+  static constexpr int STAGE = SCALES_AT + SCALES;
+  static constexpr int STAGES = SPLIT ? (FP4 ? 6 : 8) : FP4 ? 5 : 6;
+  // the other parts' sums, [part][4 columns][128 lanes] of 16 bytes
+  static constexpr int PARTS = SPLIT ? (kGrMaxParts - 1) * kGrSplitRows * 128 * 4 : 0;
+  static constexpr int SCALE_RING = FP4 ? kScaleChunks * kScaleChunkBytes : 0;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE + SCALE_RING + PARTS;
 };
 constexpr uint32_t kScaleCol = 448;  // TMEM columns of FP4's scales, 24 for each of two stages
 
@@ -56,9 +62,9 @@ __device__ __forceinline__ int scale_place(int row, int half) {
   return row * 32 + ((half ^ (row >> 2 & 1)) << 4);
 }
 
-template <int MODE>
+template <int MODE, bool SPLIT>
 struct GrCtl {
-  static constexpr int S = GrGeo<MODE>::STAGES;
+  static constexpr int S = GrGeo<MODE, SPLIT>::STAGES;
   uint64_t full[S], empty[S];
   uint64_t tail[S];               // weight grad: the expert's last rows; FP4: the odd CTA's scales
   uint64_t tmem_full[2], tmem_empty[2];
@@ -76,7 +82,11 @@ struct GrCtl {
   int32_t count[kGrMaxExperts];
   int32_t tile0[kGrMaxExperts];   // its first tile (products)
 };
-static_assert(GrGeo<kFp4>::SMEM + sizeof(GrCtl<kFp4>) <= 232448, "shared memory budget");
+static_assert(GrGeo<kFp4>::SMEM + sizeof(GrCtl<kFp4, false>) <= 232448 &&
+                  GrGeo<kFp4, true>::SMEM + sizeof(GrCtl<kFp4, true>) <= 232448 &&
+                  GrGeo<kProduct>::SMEM + sizeof(GrCtl<kProduct, false>) <= 232448 &&
+                  GrGeo<kProduct, true>::SMEM + sizeof(GrCtl<kProduct, true>) <= 232448,
+              "shared memory budget");
 
 // dense_wait, which also ends at once where a wait of this CTA has run out: the loops of the
 // loading and issuing warps go on to the tile's end then.
@@ -96,6 +106,7 @@ struct GrParams {
   const uint8_t* w_scale;
   void* out;
   int out_f32, accumulate;
+  int parts;               // SPLIT: of K
   int chunk;               // stages summed in the tensor core before they go to registers
   int32_t* error_word;
 };
@@ -113,9 +124,9 @@ struct GrTile {
   int r0, rows;     // the expert's rows
 };
 
-template <int MODE>
-__device__ __forceinline__ GrTile gr_tile(const GrCtl<MODE>& ctl, const GrParams& P, int t) {
-  using G = GrGeo<MODE>;
+template <int MODE, bool SPLIT>
+__device__ __forceinline__ GrTile gr_tile(const GrCtl<MODE, SPLIT>& ctl, const GrParams& P, int t) {
+  using G = GrGeo<MODE, SPLIT>;
   const int nt = ceil_div(P.N, 256);
   GrTile tl;
   int r, ct;  // tile within the expert, column tiles (of y's rows or dW's)
@@ -162,9 +173,20 @@ __device__ __forceinline__ GrTile warp_value(const GrTile& t) {  // (all fields 
                 warp_value(t.rows)};
 }
 
-template <int MODE>
-__device__ __forceinline__ int gr_blocks(const GrParams& P, const GrTile& tl) {
-  return ceil_div(GrGeo<MODE>::WG ? tl.rows : P.K, GrGeo<MODE>::BK);
+// Stages of a tile, of the part of K that is this pair's: from the first one on.
+struct GrRange {
+  int first, count;
+};
+template <int MODE, bool SPLIT>
+__device__ __forceinline__ GrRange gr_blocks(const GrParams& P, const GrTile& tl, int part,
+                                             int parts) {
+  using G = GrGeo<MODE, SPLIT>;
+  const int KB = ceil_div(G::WG ? tl.rows : P.K, G::BK);
+  if constexpr (!SPLIT) return GrRange{0, KB};
+  constexpr int UNIT = G::FP4 ? 4 : 1;  // (FP4: whole chunks of scales)
+  const int units = ceil_div(KB, UNIT);
+  const int first = units * part / parts * UNIT, last = min(units * (part + 1) / parts * UNIT, KB);
+  return GrRange{first, last - first};
 }
 
 // ---- MX FP4 instructions ----
@@ -198,20 +220,26 @@ __device__ __forceinline__ uint32_t idesc_mxfp4(int M, int N, uint32_t scale_id)
          static_cast<uint32_t>(M >> 4) << 24 | scale_id << 29;
 }
 
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
+template <int MODE, bool SPLIT>
+__global__ void __launch_bounds__(kGrThreads, 1)
     grouped_kernel(const __grid_constant__ GrMaps maps, const GrParams P) {
-  using G = GrGeo<MODE>;
+  using G = GrGeo<MODE, SPLIT>;
   pdl_begin();
   extern __shared__ uint8_t smem_raw[];
-  __shared__ GrCtl<MODE> ctl;
+  __shared__ GrCtl<MODE, SPLIT> ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  // the pair's rank in the cluster, this CTA's in the pair
+  const int cta = SPLIT ? warp_value(static_cast<int>(ptx::cluster_ctarank()))
+                        : static_cast<int>(ptx::cluster_ctarank());
+  const int even = SPLIT ? cta & ~1 : 0;  // the even CTA of the pair
+  const int rank = cta - even;
+  const int part = even / 2, parts = SPLIT ? P.parts : 1;
+  const uint16_t both = static_cast<uint16_t>(3u << even);
   uint8_t* tiles = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   // the odd CTA's word that stage's part of it is in place
   auto relay = [&](int stage) {
-    ptx::bulk_copy_to_cluster(ptx::mapa_shared(ptx::smem_u32(ctl.relay[stage]), 0), ctl.relay_src,
-                              kGrRelay, ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), 0));
+    ptx::bulk_copy_to_cluster(ptx::mapa_shared(ptx::smem_u32(ctl.relay[stage]), even), ctl.relay_src,
+                              kGrRelay, ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), even));
   };
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::STAGES; ++i) {
@@ -294,10 +322,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = warp_value(ctl.tmem_base);
   const int total = warp_value(ctl.total);
-  const int unit = static_cast<int>(blockIdx.x >> 1), units = static_cast<int>(gridDim.x >> 1);
+  // (SPLIT: as many clusters as tiles at least)
+  const int unit = static_cast<int>(blockIdx.x) / (2 * parts);
+  const int units = static_cast<int>(gridDim.x) / (2 * parts);
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGrRegsFew));
+    if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGrRegsFew));
     // (The loading and the issuing warp run their loops as one, an elected lane issuing: in a
     // branch of one lane an MMA took 70 cycles to issue, the loop 730 for the 512 that a stage
     // of 256 columns computes.  8 x 1024 rows, K 4096, N 28672: 1193 us so, 1077 as here;
@@ -311,11 +341,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       int64_t blocks = 0;
-      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(&ctl.full[0]), 0);
-      const uint32_t tail0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tail[0]), rank);
+      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(&ctl.full[0]), even);
+      const uint32_t tail0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tail[0]), cta);
       for (int t = unit; t < total && !aborted(); t += units) {
         const GrTile tl = warp_value(gr_tile(ctl, P, t));
-        const int KB = gr_blocks<MODE>(P, tl);
+        const GrRange range = gr_blocks<MODE, SPLIT>(P, tl, part, parts);
+        const int KB = range.count;
         const int half = tl.T / 2;
         const int n = tl.n0 + rank * 128, c = static_cast<int>(tl.c0) + rank * half;
         const uint32_t bytes = 16384u + static_cast<uint32_t>(half) * 128u;
@@ -344,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
               if (i < half / 64)
                 ptx::tma_load_2d_pair_if(go, sb + i * 8192, &maps.b, bar, c + i * 64, r);
           } else {
-            const int k = kb * (G::FP4 ? 128 : 64);  // bytes, or elements
+            const int k = (range.first + kb) * (G::FP4 ? 128 : 64);  // bytes, or elements
             if constexpr (MODE == kProduct) {
 #pragma unroll
               for (int i = 0; i < 2; ++i)
@@ -352,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             } else {
               ptx::tma_load_3d_pair_if(go, sa, &maps.a, bar, k, n, tl.e);
             }
-            if (tl.T == G::TM) {
+            if (SPLIT || tl.T == G::TM) {
               ptx::tma_load_2d_pair_if(go, sb, &maps.b, bar, k, c);
             } else {
               for (int i = 0; i < half; i += 16)
@@ -370,7 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
     } else if (warp == 1 && rank == 0) {
       // ---- MMAs ----
       const uint32_t go = ptx::elect_one();
-      const uint32_t tiles0 = ptx::smem_u32(tiles);
+      // (descriptors hold 18 bits of an address; above them is the CTA's place in the cluster)
+      const uint32_t tiles0 = ptx::smem_u32(tiles) & 0x3ffffu;
       constexpr uint32_t HI = 64u | 1u << 14 | 2u << 29;  // (8-row groups 1024 bytes apart)
       // K-major: 32 bytes of a row per step; MN-major: 16 rows, chunks of 64 columns 8192 apart
       constexpr uint32_t A_STEP = G::A_MN ? 128 : 2, B_STEP = G::WG ? 128 : 2;
@@ -379,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       uint32_t phase = 0, acc = 0, turn = 0, block = 0;
       for (int t = unit; t < total && !aborted(); t += units) {
         const GrTile tl = warp_value(gr_tile(ctl, P, t));
-        const int KB = gr_blocks<MODE>(P, tl);
+        const int KB = gr_blocks<MODE, SPLIT>(P, tl, part, parts).count;
         const uint32_t idesc = ptx::idesc_bf16_f32(256, tl.T, G::A_MN, G::WG);
         int in_chunk = 0;
         // one stage's MMAs, of `rows` of K; end: the tile's last
@@ -391,9 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
           ptx::tc_fence_after();
           const uint32_t sa = tiles0 + stage * G::STAGE;
           const uint32_t a = (sa >> 4) + A_LO, b = ((sa + 16384) >> 4) + B_LO;
-          const uint32_t d = tmem + acc * static_cast<uint32_t>(G::TM);
+          const uint32_t d = tmem + acc * static_cast<uint32_t>(G::ACC);
           if constexpr (G::FP4) {
-            const uint32_t sc = tmem + kScaleCol + (block & 1u) * 24u, ss = sa + 32768;
+            const uint32_t sc = tmem + kScaleCol + (block & 1u) * 24u, ss = sa + G::SCALES_AT;
 #pragma unroll
             for (int ka = 0; ka < 2; ++ka) {
               copy_scales_pair_if(go, sc + ka * 4, ss + ka * 512);
@@ -412,8 +444,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
                                     HI, idesc, (in_chunk | ks) != 0);
           }
           const bool last = ++in_chunk == P.chunk || end;
-          if (last) ptx::mma_commit_pair_if(go, &ctl.tmem_full[acc], 0x3);
-          ptx::mma_commit_pair_if(go, &ctl.empty[stage], 0x3);
+          if (last) ptx::mma_commit_pair_if(go, &ctl.tmem_full[acc], both);
+          ptx::mma_commit_pair_if(go, &ctl.empty[stage], both);
           if (last) {
             in_chunk = 0;
             acc ^= 1u;
@@ -437,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        const int KB = gr_blocks<MODE>(P, gr_tile(ctl, P, t));
+        const int KB = gr_blocks<MODE, SPLIT>(P, gr_tile(ctl, P, t), part, parts).count;
         for (int kb = 0; kb < KB; ++kb) {
           if (!gr_wait(&ctl.tail[stage], phase, &ctl.abort, P.error_word)) {
             ok = false;
@@ -458,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         const GrTile tl = gr_tile(ctl, P, t);
-        const int KB = gr_blocks<MODE>(P, tl);
+        const int KB = gr_blocks<MODE, SPLIT>(P, tl, part, parts).count;
         block += KB;
         if (tl.rows % 16 == 0) continue;
         const int stage = static_cast<int>((block - 1) % G::STAGES);
@@ -502,7 +534,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       for (int t = unit; t < total && !aborted(); t += units) {
         const GrTile tl = warp_value(gr_tile(ctl, P, t));
         const int n = tl.n0 + rank * 128;
-        for (int g = 0; g < KG; g += 32) {
+        const GrRange range = gr_blocks<MODE, SPLIT>(P, tl, part, parts);
+        const int last = min((range.first + range.count) * 8, KG);
+        for (int g = range.first * 8; g < last; g += 32) {
           gr_wait(&ctl.scales_empty[slot], phase ^ 1u, &ctl.abort, P.error_word);
           uint8_t* dst = ring + slot * kScaleChunkBytes;
           uint64_t* bar = &ctl.scales_full[slot];
@@ -515,29 +549,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
             if (tl.T > 128)
               ptx::tma_load_2d_if(go, dst + 8192, &maps.sb, bar, g, static_cast<int>(tl.c0) + 128);
           } else {
-            for (int i = lane; i < 384 * 2; i += 32) {
-              const int row = i >> 1, col = g + (i & 1) * 16;
-              const bool of_w = row < 128;
-              const bool in = of_w ? n + row < P.N
-                                   : row - 128 < tl.T && tl.c0 + (row - 128) < P.R;
-              const uint8_t* from =
-                  of_w ? P.w_scale + (static_cast<int64_t>(tl.e) * P.N + n + row) * KG + col
-                       : P.x_scale + (tl.c0 + (row - 128)) * KG + col;
-              uint32_t v[4] = {};
-              if (in) {
-                for (int j = 0; j < 4; ++j) {
-                  if (KG % 4 == 0) {
-                    if (col + 4 * j < KG) v[j] = __ldg(reinterpret_cast<const uint32_t*>(from) + j);
-                  } else {
-                    for (int q = 0; q < 4; ++q)
-                      if (col + 4 * j + q < KG)
-                        v[j] |= static_cast<uint32_t>(__ldg(from + 4 * j + q)) << (8 * q);
+            // 16 bytes of a row per lane, in loads as wide as the rows' alignment, BATCH of
+            // them in flight
+            auto rows = [&](auto width) {
+              using W = decltype(width);
+              constexpr int PER = 16 / sizeof(W), BATCH = 32 / PER;
+              const int col = g + (lane & 1) * 16;
+              for (int r0 = lane >> 1; r0 < 384; r0 += 16 * BATCH) {
+                W v[BATCH][PER];
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                  const int row = r0 + 16 * b;
+                  const bool of_w = row < 128;
+                  const bool in = of_w ? n + row < P.N
+                                       : row - 128 < tl.T && tl.c0 + (row - 128) < P.R;
+                  const W* from = reinterpret_cast<const W*>(
+                      (of_w ? P.w_scale + (static_cast<int64_t>(tl.e) * P.N + n + row) * KG
+                            : P.x_scale + (tl.c0 + (row - 128)) * KG) + col);
+#pragma unroll
+                  for (int j = 0; j < PER; ++j)
+                    v[b][j] = in && row < 384 && col + j * int(sizeof(W)) < KG ? __ldg(from + j) : W(0);
+                }
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                  const int row = r0 + 16 * b;
+                  if (row < 384) {
+                    W* to = reinterpret_cast<W*>(dst + (row >> 5) * 1024 +
+                                                 scale_place(row & 31, lane & 1));
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) to[j] = v[b][j];
                   }
                 }
               }
-              *reinterpret_cast<uint4*>(dst + (row >> 5) * 1024 + scale_place(row & 31, i & 1)) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
-            }
+            };
+            if (KG % 8 == 0)
+              rows(uint64_t{});
+            else if (KG % 4 == 0)
+              rows(uint32_t{});
+            else
+              rows(uint8_t{});
             __syncwarp();
             ptx::mbar_arrive_if(go, bar);
           }
@@ -554,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
       int stage = 0, slot = 0;
       uint32_t phase = 0, slot_phase = 0;
       bool ok = true;
-      const int KB = ceil_div(P.K, G::BK);
+      const int KB = gr_blocks<MODE, SPLIT>(P, GrTile{}, part, parts).count;
       for (int t = unit; t < total && ok; t += units) {
         for (int kb = 0; kb < KB && ok; kb += 4) {
           bool got = gr_wait(&ctl.scales_full[slot], slot_phase, &ctl.abort, P.error_word);
@@ -583,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
                 ok = false;
                 break;
               }
-              uint8_t* sc = tiles + stage * G::STAGE + 32768 + lane * 16;
+              uint8_t* sc = tiles + stage * G::STAGE + G::SCALES_AT + lane * 16;
 #pragma unroll
               for (int a = 0; a < 3; ++a)  // the weight's rows, the tile's first 128, its others
 #pragma unroll
@@ -614,22 +664,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
     }
   } else {
     // ---- output: 32 columns n of the weight (lanes) by half of the tile's columns a warp ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGrRegsMany));
-    const int q = warp & 3, part = (warp - 4) >> 2;
-    const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tmem_empty[0]), 0);
+    if constexpr (!SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGrRegsMany));
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    [[maybe_unused]] uint8_t* sums = tiles + G::STAGES * G::STAGE + G::SCALE_RING;
+    const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tmem_empty[0]), even);
     uint32_t acc = 0, turn = 0;
     bool ok = true;
+    if (SPLIT && unit >= total) ptx::cluster_sync();  // (for the others of the CTA: theirs below)
     for (int t = unit; t < total && ok; t += units) {
       const GrTile tl = gr_tile(ctl, P, t);
-      const int KB = gr_blocks<MODE>(P, tl);
+      const int KB = gr_blocks<MODE, SPLIT>(P, tl, part, parts).count;
       const int n = tl.n0 + rank * 128 + q * 32 + lane;
       const int groups = tl.T / 32;  // of 16 columns
       const float b = P.bias != nullptr && n < P.N
                           ? __bfloat162float(P.bias[static_cast<int64_t>(tl.e) * P.N + n])
                           : 0.f;
-      uint64_t sum[64];
+      uint64_t sum[G::TM / 4];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) sum[j] = pair_of(b, b);
+      for (int j = 0; j < G::TM / 4; ++j) sum[j] = part == 0 ? pair_of(b, b) : 0;
       for (int kb = 0; kb < KB; kb += P.chunk) {
         const bool got = gr_wait(&ctl.tmem_full[acc], turn, &ctl.abort, P.error_word);
         if (!__all_sync(0xffffffffu, got)) {
@@ -638,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
         }
         ptx::tc_fence_after();
         const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                            acc * static_cast<uint32_t>(G::TM) + part * groups * 16;
+                            acc * static_cast<uint32_t>(G::ACC) + half * groups * 16;
         uint32_t v[2][16];
         ptx::tmem_ld_16cols(ta, v[0]);
 #pragma unroll
@@ -660,10 +712,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
         acc ^= 1u;
         turn ^= acc == 0 ? 1u : 0u;
       }
+      if constexpr (SPLIT) {
+        // the other parts' sums to the first part's CTA of this rank, which adds them in order
+        if (part > 0) {
+          const uint32_t to = ptx::mapa_shared(
+              ptx::smem_u32(sums + ((part - 1) * 8 + half * 4) * 2048 + (q * 32 + lane) * 16), rank);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = unpair(sum[2 * j]), y = unpair(sum[2 * j + 1]);
+            st_cluster_f32x4(to + j * 2048, x.x, x.y, y.x, y.y);
+          }
+        }
+        __syncwarp();
+        ptx::cluster_sync();
+        if (part > 0) break;
+        for (int p = 1; p < parts; ++p) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(
+                sums + ((p - 1) * 8 + half * 4 + j) * 2048 + (q * 32 + lane) * 16);
+            sum[2 * j] = add2(sum[2 * j], pair_of(v.x, v.y));
+            sum[2 * j + 1] = add2(sum[2 * j + 1], pair_of(v.z, v.w));
+          }
+        }
+      }
       if (!ok) break;
       // a warp's store is 32 neighbouring columns of one row (through shared memory and out
       // in 16-byte stores: the same times; the MMAs' operands take half of its bandwidth)
-      const int first = part * groups * 16;
+      const int first = half * groups * 16;
       const int64_t row0 = (G::WG ? static_cast<int64_t>(tl.e) * P.K : 0) + tl.c0 + first;
       const int left = min(tl.cols - first, groups * 16);
       auto put = [&](auto* out, auto add) {
@@ -717,6 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
     }
   }
   __syncwarp();
+  if (SPLIT && warp < 4) ptx::cluster_sync();  // the exchange of the parts' sums
   ptx::cluster_sync();
   // the commits of the last use of every stage have to arrive before the barriers' memory
   // goes: each of them (see the dense FP8 pairs)
@@ -745,27 +822,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGrThreads, 1)
 // deep).  Sums that leave in bf16 lose 4e-3 in their own rounding, and go there once.
 int gr_chunk(const GroupedProductArgs& a) { return a.out_f32 ? 8 : 1 << 30; }
 
-template <int MODE>
-moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const GrMaps& maps,
-                            int64_t tiles, cudaStream_t s) {
-  using G = GrGeo<MODE>;
+// A launch with clusters of `ctas` (cfg.attrs: room for two).
+void grouped_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, int ctas, unsigned grid,
+                    size_t smem) {
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kGrThreads);
+  cfg.dynamicSmemBytes = smem;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+}
+
+template <int MODE, bool SPLIT>
+cudaError_t grouped_prepare(int* regs) {  // once per device
   static PerDevice attr;
+  return attr.get(
+      [](int* v) {
+        cudaFuncAttributes fa;
+        const cudaError_t e = cudaFuncGetAttributes(&fa, grouped_kernel<MODE, SPLIT>);
+        if (e != cudaSuccess) return e;
+        *v = fa.numRegs;
+        return cudaFuncSetAttribute(grouped_kernel<MODE, SPLIT>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(GrGeo<MODE, SPLIT>::SMEM));
+      },
+      regs);
+}
+
+// Parts of K for a product of up to 32 rows, of `tiles` tiles at most and `units` that a part
+// can be made of: as many as leave all clusters resident, where one part of K leaves
+// SMs idle.  1 x 7168 x 4096: bf16 25.4 us in one part, 11.8 so; FP4 12.6 and 10.0; 2 x
+// 14336 x 4096, an expert each: 49.1 and 37.4.
+template <int MODE>
+int grouped_parts(const GroupedProductArgs& a, int64_t tiles, int units) {
+  if (a.R > kGrSplitRows || tiles * 4 > a.num_sms) return 1;
+  int dev = 0, regs = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || grouped_prepare<MODE, true>(&regs) != cudaSuccess) {
+    cudaGetLastError();
+    return 1;
+  }
+  thread_local int room_dev = -1, room[kGrMaxParts + 1];
+  if (dev != room_dev) {  // how many clusters fit: asked once per host thread and device
+    for (int c = 2; c <= kGrMaxParts; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute at[2];
+      grouped_config(cfg, at, 2 * c, 2 * c, GrGeo<MODE, true>::SMEM);
+      if (cudaOccupancyMaxActiveClusters(&room[c], grouped_kernel<MODE, true>, &cfg) !=
+          cudaSuccess) {
+        cudaGetLastError();
+        room[c] = 0;
+      }
+    }
+    room_dev = dev;
+  }
+  int parts = 1;
+  for (int c = 2; c <= kGrMaxParts && c <= units && tiles <= room[c]; ++c) parts = c;
+  return parts;
+}
+
+template <int MODE, bool SPLIT>
+moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const GrMaps& maps,
+                            int64_t tiles, int parts, cudaStream_t s) {
   int regs = 0;
-  if (attr.get(
-          [](int* v) {
-            cudaFuncAttributes fa;
-            const cudaError_t e = cudaFuncGetAttributes(&fa, grouped_kernel<MODE>);
-            if (e != cudaSuccess) return e;
-            *v = fa.numRegs;
-            return cudaFuncSetAttribute(grouped_kernel<MODE>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(G::SMEM));
-          },
-          &regs) != cudaSuccess)
+  if (grouped_prepare<MODE, SPLIT>(&regs) != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "attributes of %s: %s", name,
                      cudaGetErrorString(cudaGetLastError()));
   // fewer registers at launch would leave the output warps waiting for more
-  if (regs < kGrRegsLaunch)
+  if (!SPLIT && regs < kGrRegsLaunch)
     return set_error(MOE_ERR_CUDA, "%s was compiled to %d registers, %d needed", name, regs,
                      kGrRegsLaunch);
   GrParams P{};
@@ -780,11 +908,17 @@ moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const
   P.out = a.out;
   P.out_f32 = a.out_f32;
   P.accumulate = a.accumulate;
+  P.parts = parts;
   P.chunk = gr_chunk(a);
   P.error_word = a.error_word;
-  const unsigned grid = 2u * static_cast<unsigned>(std::min<int64_t>(tiles, a.num_sms / 2));
+  const int64_t clusters = SPLIT ? tiles : std::min<int64_t>(tiles, a.num_sms / 2);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  grouped_config(cfg, at, 2 * parts, static_cast<unsigned>(2 * parts * clusters),
+                 GrGeo<MODE, SPLIT>::SMEM);
+  cfg.stream = s;
   prof_before(name, s);
-  launch_kernel(grouped_kernel<MODE>, grid, kGrThreads, G::SMEM, s, maps, P);
+  cudaLaunchKernelEx(&cfg, grouped_kernel<MODE, SPLIT>, maps, P);
   prof_after(name, s);
   return check_launch(name);
 }
@@ -817,16 +951,24 @@ constexpr auto kBytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 
 moe_status_t launch_grouped_matmul(const GroupedProductArgs& a, cudaStream_t s) {
   const uint64_t K = a.K, N = a.N, E = a.E, R = static_cast<uint64_t>(a.R);
+  const int64_t tiles = product_tiles(a, 256);
+  const int units = ceil_div(a.K, 64) / 4;
+  const int parts = a.transposed ? grouped_parts<kProductT>(a, tiles, units)
+                                 : grouped_parts<kProduct>(a, tiles, units);
   GrMaps m;
   if (moe_status_t st = a.transposed ? map_3d(&m.a, a.w, K, N, E, 2 * K, 64, 128, kBf16)
                                      : map_3d(&m.a, a.w, N, K, E, 2 * N, 64, 64, kBf16))
     return st;
-  if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, 128, kBf16)) return st;
+  const uint32_t half = parts > 1 ? kGrSplitRows / 2 : 128;
+  if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, half, kBf16)) return st;
+  m.b16 = m.b;
+  if (parts > 1)
+    return a.transposed
+               ? launch_grouped<kProductT, true>("grouped_matmul_t_split", a, m, tiles, parts, s)
+               : launch_grouped<kProduct, true>("grouped_matmul_split", a, m, tiles, parts, s);
   if (moe_status_t st = map_2d(&m.b16, a.x, K, R, 2 * K, 64, 16, kBf16)) return st;
-  const int64_t tiles = product_tiles(a, 256);
-  return a.transposed
-             ? launch_grouped<kProductT>("grouped_matmul_t", a, m, tiles, s)
-             : launch_grouped<kProduct>("grouped_matmul", a, m, tiles, s);
+  return a.transposed ? launch_grouped<kProductT, false>("grouped_matmul_t", a, m, tiles, 1, s)
+                      : launch_grouped<kProduct, false>("grouped_matmul", a, m, tiles, 1, s);
 }
 
 moe_status_t launch_grouped_weight_grad(const GroupedProductArgs& a, cudaStream_t s) {
@@ -836,15 +978,20 @@ moe_status_t launch_grouped_weight_grad(const GroupedProductArgs& a, cudaStream_
   if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, 64, kBf16)) return st;
   m.b16 = m.b;
   const int64_t tiles = int64_t(a.E) * ceil_div(a.K, 256) * ceil_div(a.N, 256);
-  return launch_grouped<kWeightGrad>("grouped_weight_grad", a, m, tiles, s);
+  return launch_grouped<kWeightGrad, false>("grouped_weight_grad", a, m, tiles, 1, s);
 }
 
 moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s) {
   const uint64_t KB = a.K / 2, N = a.N, E = a.E, R = static_cast<uint64_t>(a.R);
+  const int64_t tiles = product_tiles(a, 224);
+  const int parts = grouped_parts<kFp4>(a, tiles, ceil_div(a.K, 1024));
   GrMaps m;
   if (moe_status_t st = map_3d(&m.a, a.w, KB, N, E, KB, 128, 128, kBytes)) return st;
-  if (moe_status_t st = map_2d(&m.b, a.x, KB, R, KB, 128, 112, kBytes)) return st;
-  if (moe_status_t st = map_2d(&m.b16, a.x, KB, R, KB, 128, 16, kBytes)) return st;
+  const uint32_t half = parts > 1 ? kGrSplitRows / 2 : 112;
+  if (moe_status_t st = map_2d(&m.b, a.x, KB, R, KB, 128, half, kBytes)) return st;
+  m.b16 = m.b;
+  if (parts == 1)
+    if (moe_status_t st = map_2d(&m.b16, a.x, KB, R, KB, 128, 16, kBytes)) return st;
   if (a.K % 512 == 0) {  // (rows of whole 16 bytes)
     const uint64_t KG = a.K / 32;
     const auto s32 = CU_TENSOR_MAP_SWIZZLE_32B;
@@ -853,7 +1000,8 @@ moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s) {
   } else {
     m.sa = m.sb = m.b;
   }
-  return launch_grouped<kFp4>("matmul_fp4", a, m, product_tiles(a, 224), s);
+  return parts > 1 ? launch_grouped<kFp4, true>("matmul_fp4_split", a, m, tiles, parts, s)
+                   : launch_grouped<kFp4, false>("matmul_fp4", a, m, tiles, 1, s);
 }
 
 }  // namespace gbmoe

@@ -142,12 +142,69 @@ def test_product_rows_do_not_touch_each_other():
 
 def test_product_same_rows_in_any_company():
     """A row's result does not depend on the rows beside it (as a padded batch
-    and its unpadded form have to agree)."""
-    w = torch.randn(1, 256, 264, generator=gen(8), device="cuda").to(BF16)
-    x = torch.randn(700, 256, generator=gen(9), device="cuda").to(BF16)
+    and its unpadded form have to agree), but for K being summed in parts in
+    calls of up to 32 rows in all: those agree among themselves."""
+    w = torch.randn(1, 1024, 264, generator=gen(8), device="cuda").to(BF16)
+    x = torch.randn(700, 1024, generator=gen(9), device="cuda").to(BF16)
     full = pkg.moe_grouped_matmul(x, w, offsets_of([700]))
-    for n in (1, 33, 256, 511):
+    for n in (33, 256, 511):
         assert torch.equal(pkg.moe_grouped_matmul(x[:n].clone(), w, offsets_of([n])), full[:n])
+    few = pkg.moe_grouped_matmul(x[:32].clone(), w, offsets_of([32]))
+    for n in (1, 7, 31):
+        assert torch.equal(pkg.moe_grouped_matmul(x[:n].clone(), w, offsets_of([n])), few[:n])
+
+
+def name_of(call):
+    pkg.profiler_start()
+    try:
+        call()
+    finally:
+        took = pkg.profiler_stop()
+    return list(took)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("counts,K,N,split", [
+    ([1], 7168, 4096, True), ([1, 0, 1], 14336, 520, True), ([8, 0, 8, 8, 8], 4096, 264, True),
+    ([32], 1000, 2056, True), ([5] * 6, 2048, 1288, True), ([31, 1], 264, 8, False),
+    ([1] * 30, 1024, 520, False), ([33], 7168, 4096, False)])
+def test_product_of_few_rows_in_parts_of_K(counts, K, N, split, transposed):
+    E, R = len(counts), sum(counts) + 3
+    off = offsets_of(counts, 1)
+    x = ints(1, R, K)
+    x[0], x[-2:] = float("nan"), float("inf")
+    w = ints(2, E, N, K) if transposed else ints(2, E, K, N)
+    bias = ints(3, E, N)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    # (rows of nobody count among the 32)
+    few = split and R <= 32
+    for dt, b in ((BF16, None), (F32, bias)):
+        out = torch.full((R, N), 7.0, device="cuda", dtype=dt)
+        name = name_of(lambda: pkg.moe_grouped_matmul(x, w, off, bias=b, transposed=transposed,
+                                                      out=out, error_word=err))
+        assert name == ["grouped_matmul" + "_t" * transposed + "_split" * few]
+        assert torch.equal(out, reference(x, w, off, torch.full_like(out, 7.0), transposed, b))
+    inner = slice(1, R - 2)
+    out = torch.full((R - 3, N), 7.0, device="cuda")
+    name = name_of(lambda: pkg.moe_grouped_matmul(x[inner].clone(), w, off - 1, transposed=transposed,
+                                                  out=out, error_word=err))
+    assert name == ["grouped_matmul" + "_t" * transposed + "_split" * split]
+    assert torch.equal(out, reference(x[inner], w, off - 1, out, transposed))
+    assert err.item() == 0
+
+
+def test_few_rows_back_to_back():
+    """Calls whose clusters follow one another, of other parts and sizes."""
+    cases = []
+    for i, (counts, K, N) in enumerate([([1], 7168, 4096), ([2, 3], 1024, 264), ([32], 2048, 2056),
+                                        ([1, 1], 4096, 1032), ([9], 520, 520)]):
+        x, w, off = ints(i, sum(counts), K), ints(9 + i, len(counts), K, N), offsets_of(counts)
+        ref = reference(x, w, off, torch.zeros(len(x), N, device="cuda"))
+        cases.append((x, w, off, ref, [torch.zeros(len(x), N, device="cuda") for _ in range(8)]))
+    for r in range(8):
+        for x, w, off, _, outs in cases:
+            pkg.moe_grouped_matmul(x, w, off, out=outs[r])
+    assert all(torch.equal(o, ref) for _, _, _, ref, outs in cases for o in outs)
 
 
 def test_empty_calls():

@@ -230,8 +230,31 @@ def test_rows_do_not_depend_on_company():
     w, sw = codes(3, (264,), 640, 110, 140)
     a, sa = codes(1, (700,), 640, 110, 140)
     full = pkg.moe_matmul_fp4(a, sa, w, sw)
-    for n in (1, 33, 224, 511):
+    for n in (33, 224, 511):
         assert torch.equal(pkg.moe_matmul_fp4(a[:n].clone(), sa[:n].clone(), w, sw), full[:n])
+    few = pkg.moe_matmul_fp4(a[:32].clone(), sa[:32].clone(), w, sw)  # (K may be in parts)
+    for n in (1, 7, 31):
+        assert torch.equal(pkg.moe_matmul_fp4(a[:n].clone(), sa[:n].clone(), w, sw), few[:n])
+
+
+@pytest.mark.parametrize("counts,K,N,split", [
+    ([1], 7168, 4096, True), ([1, 0, 1], 14336, 520, True), ([8, 0, 8, 8, 8], 4096, 264, True),
+    ([32], 2080, 2056, True), ([5] * 6, 3104, 1288, True), ([31, 1], 1024, 8, False),
+    ([1] * 30, 2048, 520, False), ([33], 7168, 4096, False)])
+def test_product_of_few_rows_in_parts_of_K(counts, K, N, split):
+    E, R = len(counts), sum(counts)
+    off = offsets_of(counts)
+    a, sa = codes(1, (R,), K, 127, 128)
+    w, sw = codes(3, (E, N), K, 127, 128)
+    ref = reference(values64(a, sa), values64(w, sw), off.tolist(), torch.zeros(R, N, device="cuda"))
+    for dt in (F32, BF16):
+        out = torch.full((R + 2, N), 7.0, device="cuda", dtype=dt)
+        for _ in range(5):
+            pkg.moe_matmul_fp4(a, sa, w, sw, off, out=out[1:-1])
+        assert torch.equal(out[1:-1], ref.to(dt)) and (out[0] == 7).all() and (out[-1] == 7).all()
+    pkg.profiler_start()
+    pkg.moe_matmul_fp4(a, sa, w, sw, off)
+    assert list(pkg.profiler_stop()) == ["matmul_fp4" + "_split" * split]
 
 
 def test_experts_forward_and_the_gradient_of_their_weight():
