@@ -21,13 +21,21 @@
 namespace gbmoe {
 namespace {
 
-enum Mode { kProduct, kProductT, kWeightGrad, kFp4 };  // W [E, K, N], [E, N, K]; FP4: [E, N, K]
+// W [E, K, N], [E, N, K]; FP4: [E, N, K], rows of scales of whole 16 bytes, and of any size
+enum Mode { kProduct, kProductT, kWeightGrad, kFp4, kFp4Rows };
 
 constexpr int kGrThreads = 128 + 256;  // TMA, MMA, two helper warps; 8 output warps
 constexpr int kGrMaxExperts = 1024;
 constexpr int kGrGroup = 8;            // row tiles of a raster group
 constexpr int kScaleChunks = 3;        // FP4: chunks of 1024 elements whose scales are on their way
 constexpr int kScaleChunkBytes = 384 * 32;
+// Rows of scales that are not whole 16 bytes: the 48 bytes, aligned, that hold a row's 32; or
+// for K up to 1024 the rows as they lie in memory, the weight's and then the tile's.
+constexpr int kRawChunks = 2, kRawChunkBytes = 384 * 48;
+constexpr int kRawTile = 128 * 32 + 256;
+static_assert(kRawChunks * kRawChunkBytes <= kScaleChunks * kScaleChunkBytes &&
+                  kRawTile + 256 * 32 + 32 <= kRawChunkBytes,
+              "in the same ring");
 constexpr int kGrRelay = 16;           // bytes by which the odd CTA signals the even one
 // Registers: as in the dense FP8 pairs, the first warpgroup gives up what the output
 // warps, with up to 128 sums each, need.
@@ -39,7 +47,7 @@ static_assert(128 * kGrRegsFew + 256 * kGrRegsMany <= kGrThreads * kGrRegsLaunch
 constexpr int kGrSplitRows = 32, kGrMaxParts = 4;
 template <int MODE, bool SPLIT = false>
 struct GrGeo {
-  static constexpr bool FP4 = MODE == kFp4, WG = MODE == kWeightGrad;
+  static constexpr bool FP4 = MODE == kFp4 || MODE == kFp4Rows, WG = MODE == kWeightGrad;
   static constexpr bool A_MN = MODE == kProduct || WG;  // MN-major first operand
   static constexpr int BK = FP4 ? 256 : 64;    // reduced elements of a stage (128 bytes of a row)
   // columns of a tile; FP4: two accumulators and the scales share the 512 TMEM columns
@@ -250,7 +258,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
       ptx::mbar_init(&ctl.tail[i], 1);
     }
     for (int i = 0; i < kScaleChunks; ++i) {
-      ptx::mbar_init(&ctl.scales_full[i], 1);
+      ptx::mbar_init(&ctl.scales_full[i], MODE == kFp4Rows && P.K > 1024 ? 32 : 1);
       ptx::mbar_init(&ctl.scales_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -521,8 +529,10 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     } else if (G::FP4 && warp == 2) {
       // ---- scales into shared memory, of the weight's 128 rows and the tile's 256, 32 bytes
       // of a row (a chunk: 1024 elements, four stages) at a time, into a ring ----
-      // By TMA where rows of scales are whole 16 bytes (K a multiple of 512).  Loads by the
-      // warp's lanes, each a row, are as many requests as lanes, and slower than the MMAs
+      // By TMA where rows of scales are whole 16 bytes (K a multiple of 512); else for K up to
+      // 1024 as the rows lie in memory, in bulk copies; else by the warp's lanes, a row
+      // each, in asynchronous copies (8192 x 7200 x 4096: 184 us).  Those are as many
+      // requests as lanes, and slower than the MMAs
       // (8192 x 7168 x 4096: 155 us from registers, 93-100 by asynchronous copies,
       // 85 by TMA, 78 without any).  The warp that takes the scales from the ring is another
       // one: its fence for the tensor core's reads would wait for copies in flight.
@@ -538,65 +548,74 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         const int last = min((range.first + range.count) * 8, KG);
         for (int g = range.first * 8; g < last; g += 32) {
           gr_wait(&ctl.scales_empty[slot], phase ^ 1u, &ctl.abort, P.error_word);
-          uint8_t* dst = ring + slot * kScaleChunkBytes;
           uint64_t* bar = &ctl.scales_full[slot];
-          if (KG % 16 == 0) {
+          if constexpr (MODE == kFp4) {
             // (rows and scales that are not there are read as zeros, 2^-127; past K the codes
             // are zeros too)
+            uint8_t* dst = ring + slot * kScaleChunkBytes;
             ptx::mbar_arrive_expect_tx_if(go, bar, tl.T > 128 ? 12288 : 8192);
             ptx::tma_load_3d_if(go, dst, &maps.sa, bar, g, n, tl.e);
             ptx::tma_load_2d_if(go, dst + 4096, &maps.sb, bar, g, static_cast<int>(tl.c0));
             if (tl.T > 128)
               ptx::tma_load_2d_if(go, dst + 8192, &maps.sb, bar, g, static_cast<int>(tl.c0) + 128);
-          } else {
-            // 16 bytes of a row per lane, in loads as wide as the rows' alignment, BATCH of
-            // them in flight
-            auto rows = [&](auto width) {
-              using W = decltype(width);
-              constexpr int PER = 16 / sizeof(W), BATCH = 32 / PER;
-              const int col = g + (lane & 1) * 16;
-              for (int r0 = lane >> 1; r0 < 384; r0 += 16 * BATCH) {
-                W v[BATCH][PER];
+          } else if (KG <= 32) {
+            // the rows that are there, in one piece each of the two tensors, from a multiple
+            // of 16 bytes on and to one, but not past the tensor
+            if (go) {
+              uint8_t* dst = ring + slot * kRawChunkBytes;
+              const int64_t wrow = static_cast<int64_t>(tl.e) * P.N + n;
+              const int64_t from[2] = {wrow * KG, tl.c0 * KG};
+              const int64_t to[2] = {(wrow + max(min(128, P.N - n), 0)) * KG,
+                                     min(tl.c0 + tl.T, P.R) * KG};
+              const int64_t end[2] = {static_cast<int64_t>(P.E) * P.N * KG, P.R * KG};
+              uint32_t bytes[2];
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                  const int row = r0 + 16 * b;
-                  const bool of_w = row < 128;
-                  const bool in = of_w ? n + row < P.N
-                                       : row - 128 < tl.T && tl.c0 + (row - 128) < P.R;
-                  const W* from = reinterpret_cast<const W*>(
-                      (of_w ? P.w_scale + (static_cast<int64_t>(tl.e) * P.N + n + row) * KG
-                            : P.x_scale + (tl.c0 + (row - 128)) * KG) + col);
-#pragma unroll
-                  for (int j = 0; j < PER; ++j)
-                    v[b][j] = in && row < 384 && col + j * int(sizeof(W)) < KG ? __ldg(from + j) : W(0);
-                }
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                  const int row = r0 + 16 * b;
-                  if (row < 384) {
-                    W* to = reinterpret_cast<W*>(dst + (row >> 5) * 1024 +
-                                                 scale_place(row & 31, lane & 1));
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) to[j] = v[b][j];
-                  }
-                }
+              for (int i = 0; i < 2; ++i) {
+                const uint8_t* src = i == 0 ? P.w_scale : P.x_scale;
+                const int64_t a = from[i] & ~int64_t(15);
+                const int64_t z = min((to[i] + 15) & ~int64_t(15), end[i] & ~int64_t(15));
+                bytes[i] = to[i] > from[i] && z > a ? static_cast<uint32_t>(z - a) : 0u;
+                for (int64_t q = max(z, a); q < to[i]; ++q)  // (a tensor's last bytes)
+                  dst[i * kRawTile + static_cast<int>(q - a)] = __ldg(src + q);
               }
-            };
-            if (KG % 8 == 0)
-              rows(uint64_t{});
-            else if (KG % 4 == 0)
-              rows(uint32_t{});
-            else
-              rows(uint8_t{});
+              ptx::mbar_arrive_expect_tx(bar, bytes[0] + bytes[1]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (bytes[i] > 0)
+                  ptx::bulk_load(dst + i * kRawTile,
+                                 (i == 0 ? P.w_scale : P.x_scale) + (from[i] & ~int64_t(15)),
+                                 bytes[i], bar);
+            }
             __syncwarp();
-            ptx::mbar_arrive_if(go, bar);
+          } else {
+            // row lane + 32 i: zeros where it is not there, and nothing read past the tensor
+            uint8_t* dst = ring + slot * kRawChunkBytes + lane * 16;
+            const int64_t wrow = static_cast<int64_t>(tl.e) * P.N + n;
+            const int64_t wend = static_cast<int64_t>(P.E) * P.N * KG, xend = P.R * KG;
+#pragma unroll 4
+            for (int i = 0; i < 12; ++i) {
+              const int r = lane + 32 * (i < 4 ? i : i - 4);
+              const bool in = i < 4 ? n + r < P.N : r < tl.T && tl.c0 + r < P.R;
+              const uint8_t* base = i < 4 ? P.w_scale : P.x_scale;
+              const int64_t at = ((i < 4 ? wrow : tl.c0) + r) * KG + g, from = at & ~int64_t(15);
+              const int64_t need = at + min(32, KG - g), end = i < 4 ? wend : xend;
+#pragma unroll
+              for (int j = 0; j < 3; ++j) {
+                const int64_t f = from + 16 * j;
+                const bool there = in && f < need;
+                ptx::cp_async_16(dst + (i * 3 + j) * 512, there ? base + f : base,
+                                 there ? static_cast<uint32_t>(min(end - f, int64_t(16))) : 0u);
+              }
+            }
+            ptx::cp_async_arrive(bar);
           }
-          if (++slot == kScaleChunks) {
+          if (++slot == (MODE == kFp4 ? kScaleChunks : kRawChunks)) {
             slot = 0;
             phase ^= 1u;
           }
         }
       }
+      ptx::cp_async_wait_all();
     } else if (G::FP4 && warp == 3) {
       // ---- and on to where the tensor core's copy takes them: there, 16 bytes are 128
       // elements' scales of a lane's four rows ----
@@ -604,62 +623,140 @@ __global__ void __launch_bounds__(kGrThreads, 1)
       int stage = 0, slot = 0;
       uint32_t phase = 0, slot_phase = 0;
       bool ok = true;
-      const int KB = gr_blocks<MODE, SPLIT>(P, GrTile{}, part, parts).count;
-      for (int t = unit; t < total && ok; t += units) {
-        for (int kb = 0; kb < KB && ok; kb += 4) {
-          bool got = gr_wait(&ctl.scales_full[slot], slot_phase, &ctl.abort, P.error_word);
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
+      const GrRange range = gr_blocks<MODE, SPLIT>(P, GrTile{}, part, parts);
+      const int KB = range.count;
+      auto chunk_in = [&]() {
+        const bool got = gr_wait(&ctl.scales_full[slot], slot_phase, &ctl.abort, P.error_word);
+        return __all_sync(0xffffffffu, got);
+      };
+      auto chunk_out = [&]() {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ctl.scales_empty[slot]);
+        if (++slot == (MODE == kFp4 ? kScaleChunks : kRawChunks)) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
+      };
+      // a stage's scales: of row lane + 32 i of the weight (i < 4) and of the tile, two words
+      auto put_stage = [&](auto word) {
+        const bool got = gr_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
+        if (!__all_sync(0xffffffffu, got)) return false;
+        uint8_t* sc = tiles + stage * G::STAGE + G::SCALES_AT + lane * 16;
 #pragma unroll
-          for (int b = 0; b < 4; b += 2) {  // two stages: 16 bytes of a row
-            if (kb + b >= KB) break;
-            uint32_t v[12][4];
+        for (int a = 0; a < 3; ++a)  // the weight's rows, the tile's first 128, its others
 #pragma unroll
-            for (int i = 0; i < 12; ++i) {
-              const uint4 u = *reinterpret_cast<const uint4*>(
-                  ring + slot * kScaleChunkBytes + i * 1024 + scale_place(lane, b >> 1));
-              v[i][0] = u.x;
-              v[i][1] = u.y;
-              v[i][2] = u.z;
-              v[i][3] = u.w;
+          for (int ka = 0; ka < 2; ++ka)
+            *reinterpret_cast<uint4*>(sc + (a == 0 ? ka * 512 : 1024 + ka * 1024 + (a - 1) * 512)) =
+                make_uint4(word(4 * a, ka), word(4 * a + 1, ka), word(4 * a + 2, ka),
+                           word(4 * a + 3, ka));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(rank == 0 ? &ctl.full[stage] : &ctl.tail[stage]);
+        if (++stage == G::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return true;
+      };
+      if constexpr (MODE == kFp4) {
+        for (int t = unit; t < total && ok; t += units) {
+          for (int kb = 0; kb < KB && ok; kb += 4) {
+            if (!chunk_in()) {
+              ok = false;
+              break;
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (kb + b + h >= KB) break;
-              got = gr_wait(&ctl.empty[stage], phase ^ 1u, &ctl.abort, P.error_word);
-              if (!__all_sync(0xffffffffu, got)) {
+            for (int b = 0; b < 4; b += 2) {  // two stages: 16 bytes of a row
+              if (kb + b >= KB || !ok) break;
+              uint32_t v[12][4];
+#pragma unroll
+              for (int i = 0; i < 12; ++i) {
+                const uint4 u = *reinterpret_cast<const uint4*>(
+                    ring + slot * kScaleChunkBytes + i * 1024 + scale_place(lane, b >> 1));
+                v[i][0] = u.x;
+                v[i][1] = u.y;
+                v[i][2] = u.z;
+                v[i][3] = u.w;
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (kb + b + h >= KB || !ok) break;
+                ok = put_stage([&](int i, int ka) { return v[i][2 * h + ka]; });
+              }
+            }
+            chunk_out();
+          }
+        }
+      } else {
+        // from rows at any place: the 8 bytes of a stage, from two aligned 8s, by bytes, or
+        // by words where all rows begin at whole ones
+        const int KG = P.K / 32;
+        auto run = [&](auto unit_bytes) {
+          constexpr uint32_t UNIT = decltype(unit_bytes)::value;
+          for (int t = unit; t < total && ok; t += units) {
+            const GrTile tl = gr_tile(ctl, P, t);
+            const int n = tl.n0 + rank * 128;
+            // where the first row of the weight and of the tile begins, mod 16
+            const uint32_t w0 = (static_cast<uint32_t>(tl.e) * P.N + n) * static_cast<uint32_t>(KG);
+            const uint32_t x0 = static_cast<uint32_t>(tl.c0) * static_cast<uint32_t>(KG);
+            for (int kb = 0; kb < KB && ok; ++kb) {
+              const int h = kb & 3, g = (range.first + kb - h) * 8;  // stage of the chunk, its start
+              if (h == 0 && !chunk_in()) {
                 ok = false;
                 break;
               }
-              uint8_t* sc = tiles + stage * G::STAGE + G::SCALES_AT + lane * 16;
+              uint32_t v[12][2];
 #pragma unroll
-              for (int a = 0; a < 3; ++a)  // the weight's rows, the tile's first 128, its others
-#pragma unroll
-                for (int ka = 0; ka < 2; ++ka) {
-                  const int k = 2 * h + ka;
-                  *reinterpret_cast<uint4*>(
-                      sc + (a == 0 ? ka * 512 : 1024 + ka * 1024 + (a - 1) * 512)) =
-                      make_uint4(v[4 * a][k], v[4 * a + 1][k], v[4 * a + 2][k], v[4 * a + 3][k]);
+              for (int i = 0; i < 12; ++i) {
+                const int r = lane + 32 * (i < 4 ? i : i - 4);
+                const uint8_t* raw = ring + slot * kRawChunkBytes;
+                uint32_t at;  // of the stage's bytes, from raw on
+                bool in = true;
+                if (KG <= 32) {
+                  at = ((i < 4 ? w0 : x0) & 15u) + r * KG + 8 * h;
+                  raw += i < 4 ? 0 : kRawTile;
+                  in = i < 4 ? n + r < P.N : r < tl.T && tl.c0 + r < P.R;
+                } else {
+                  at = (((i < 4 ? w0 : x0) + r * KG + g) & 15u) + 8 * h;
+                  raw += i * 1536 + lane * 16;
                 }
-              ptx::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(rank == 0 ? &ctl.full[stage] : &ctl.tail[stage]);
-              if (++stage == G::STAGES) {
-                stage = 0;
-                phase ^= 1u;
+                auto eight = [&](uint32_t o) {  // at a multiple of 8
+                  const uint8_t* from = raw + (KG <= 32 ? o : (o >> 4) * 512 + (o & 8u));
+                  return in ? *reinterpret_cast<const uint2*>(from) : make_uint2(0, 0);
+                };
+                const uint2 lo = eight(at & ~7u);
+                if constexpr (UNIT == 8) {
+                  v[i][0] = lo.x;
+                  v[i][1] = lo.y;
+                } else {
+                  const uint2 hi = eight((at & ~7u) + 8);
+                  const uint32_t a = at & 4u ? lo.y : lo.x, b = at & 4u ? hi.x : lo.y;
+                  const uint32_t c = at & 4u ? hi.y : hi.x;
+                  v[i][0] = UNIT == 4 ? a : __funnelshift_r(a, b, 8 * (at & 3u));
+                  v[i][1] = UNIT == 4 ? b : __funnelshift_r(b, c, 8 * (at & 3u));
+                }
               }
+              const int left = KG - g - 8 * h;  // scales of the row from here on (past them: 0)
+              if (left < 8) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int bytes = min(max(left - 4 * k, 0), 4);
+                  const uint32_t mask = bytes == 4 ? ~0u : (1u << (8 * bytes)) - 1u;
+#pragma unroll
+                  for (int i = 0; i < 12; ++i) v[i][k] &= mask;
+                }
+              }
+              ok = put_stage([&](int i, int ka) { return v[i][ka]; });
+              if (h == 3 || kb == KB - 1) chunk_out();
             }
-            if (!ok) break;
           }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&ctl.scales_empty[slot]);
-          if (++slot == kScaleChunks) {
-            slot = 0;
-            slot_phase ^= 1u;
-          }
-        }
+        };
+        if (KG % 8 == 0)
+          run(std::integral_constant<uint32_t, 8>{});
+        else if (KG % 4 == 0)
+          run(std::integral_constant<uint32_t, 4>{});
+        else
+          run(std::integral_constant<uint32_t, 1>{});
       }
     }
   } else {
@@ -984,7 +1081,10 @@ moe_status_t launch_grouped_weight_grad(const GroupedProductArgs& a, cudaStream_
 moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s) {
   const uint64_t KB = a.K / 2, N = a.N, E = a.E, R = static_cast<uint64_t>(a.R);
   const int64_t tiles = product_tiles(a, 224);
-  const int parts = grouped_parts<kFp4>(a, tiles, ceil_div(a.K, 1024));
+  const bool rows16 = a.K % 512 == 0;  // rows of scales of whole 16 bytes
+  const int units = ceil_div(a.K, 1024);
+  const int parts = rows16 ? grouped_parts<kFp4>(a, tiles, units)
+                           : grouped_parts<kFp4Rows>(a, tiles, units);
   GrMaps m;
   if (moe_status_t st = map_3d(&m.a, a.w, KB, N, E, KB, 128, 128, kBytes)) return st;
   const uint32_t half = parts > 1 ? kGrSplitRows / 2 : 112;
@@ -992,7 +1092,7 @@ moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s) {
   m.b16 = m.b;
   if (parts == 1)
     if (moe_status_t st = map_2d(&m.b16, a.x, KB, R, KB, 128, 16, kBytes)) return st;
-  if (a.K % 512 == 0) {  // (rows of whole 16 bytes)
+  if (rows16) {
     const uint64_t KG = a.K / 32;
     const auto s32 = CU_TENSOR_MAP_SWIZZLE_32B;
     if (moe_status_t st = map_3d(&m.sa, a.w_scale, KG, N, E, KG, 32, 128, kBytes, s32)) return st;
@@ -1000,8 +1100,11 @@ moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s) {
   } else {
     m.sa = m.sb = m.b;
   }
-  return parts > 1 ? launch_grouped<kFp4, true>("matmul_fp4_split", a, m, tiles, parts, s)
-                   : launch_grouped<kFp4, false>("matmul_fp4", a, m, tiles, 1, s);
+  if (parts > 1)
+    return rows16 ? launch_grouped<kFp4, true>("matmul_fp4_split", a, m, tiles, parts, s)
+                  : launch_grouped<kFp4Rows, true>("matmul_fp4_split", a, m, tiles, parts, s);
+  return rows16 ? launch_grouped<kFp4, false>("matmul_fp4", a, m, tiles, 1, s)
+                : launch_grouped<kFp4Rows, false>("matmul_fp4", a, m, tiles, 1, s);
 }
 
 }  // namespace gbmoe

@@ -167,7 +167,24 @@ def test_grouped_product_exact(counts, K, N):
                                       torch.full_like(out, 7.0)).float())
 
 
-@pytest.mark.parametrize("K", [512, 800])
+@pytest.mark.parametrize("N", [8, 24, 136, 520])
+@pytest.mark.parametrize("K", [32 * j for j in (1, 3, 7, 10, 13, 17, 24, 27, 31, 33, 36, 39, 62, 65, 97)])
+def test_grouped_product_exact_for_any_row_of_scales(K, N):
+    """Rows of scales of any length and place in memory; the tensors' last bytes
+    are those of a larger one, whose others are NaN scales."""
+    counts = [5, 0, 33, 1, 230]
+    E, R, KG, off = len(counts), sum(counts), K // 32, offsets_of([5, 0, 33, 1, 230])
+    a, sa = codes(1, (R,), K)
+    w, sw = codes(3, (E, N), K)
+    big = [torch.full((t.numel() + 512,), 255, device="cuda", dtype=torch.uint8) for t in (sa, sw)]
+    ga, gw = (b[256:256 + t.numel()].view(t.shape).copy_(t) for b, t in zip(big, (sa, sw)))
+    ref = reference(values64(a, sa), values64(w, sw), off.tolist(), torch.zeros(R, N, device="cuda"))
+    out = torch.zeros(R, N, device="cuda")
+    pkg.moe_matmul_fp4(a, ga, w, gw, off, out=out)
+    assert torch.equal(out, ref.float())
+
+
+@pytest.mark.parametrize("K", [512, 800, 1312])
 def test_grouped_product_of_many_tiles_per_expert(K):
     counts, N = [2000, 0, 70, 4100], 1288
     off = offsets_of(counts)
