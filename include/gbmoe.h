@@ -167,7 +167,7 @@ GBMOE_API moe_status_t moe_route_biased(const void* router_logits, int32_t logit
  * they hold.
  * grad_weights[t, j] is the product of the layer's output gradient with the
  * output of the token's j-th expert; the library's forward does not keep those
- * outputs, so that it comes from the caller's own backward pass of the experts.
+ * outputs, so that it comes from a backward pass of the experts (moe_swiglu_backward).
  * The pages have no counterpart to this entry point.
  *  grad_weights   device fp32 [M, top_k]
  *  router_logits  device fp32 or (logits_bf16 = 1) bf16 [M, E]
@@ -515,7 +515,9 @@ GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const
  *                  that no row is computed twice.
  *  error_word      device int32 or NULL; also MOE_ERR_TIMEOUT if a pipeline wait ran
  *                  out of time (the output is then incomplete)
- * Results do not depend on timing.  out must not overlap the inputs; operands, bias,
+ * Results do not depend on timing.  A row's do not depend on the rows beside it, but
+ * that calls of up to 32 rows may sum K in parts (the profiler's names then end in
+ * _split).  out must not overlap the inputs; operands, bias,
  * scales and out 16-byte aligned.  Limits: E <= 1024, R <= 2^31 - 1024, K and N up to
  * 2^22, R * N <= 2^44, E ceil(K/256) ceil(N/256) < 2^30.
  *

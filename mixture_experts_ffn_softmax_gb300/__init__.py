@@ -9,6 +9,7 @@ PyTorch supplies device memory and the current stream.
     y = moe_forward(hidden, w, ids, w13, w2)            # [M, H] bf16
     y = fused_moe(hidden, logits, w13, w2, top_k, ...)  # route + forward
     y = moe_shared_expert_fp8(hidden, w13_q, w2_q, s13, s2)  # dense, FP8 block scales
+    h = moe_grouped_matmul(rows, w13, expert_offsets)   # the experts step by step, for training
 """
 from __future__ import annotations
 
@@ -228,7 +229,7 @@ def moe_route_backward(grad_weights: torch.Tensor, router_logits: torch.Tensor,
     experts topk_ids int32 [M, k] -> grad_logits [M, E] in the logits' type.
     The choice of experts is held fixed.  grad_weights are the products of the
     layer's output gradient with the chosen experts' outputs, which the forward
-    does not keep: they come from the caller's backward pass of the experts.
+    does not keep: a backward pass of the experts gives them (moe_swiglu_backward).
     error_word: int32 [1], set where an id is outside [0, E) (such items take
     no part, nor do those of masked experts)."""
     M, E = _matrix(router_logits, "router_logits")

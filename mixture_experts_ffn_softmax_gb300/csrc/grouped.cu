@@ -11,6 +11,16 @@
 // the ragged side in the MMA's N, a tile takes as many columns as it has rows, rounded up to
 // 32: experts of 1, 40 or 300 rows cost what they have, and one kernel serves a decode step's
 // few rows (bound by the weights' bytes) and a long prefill (bound by the tensor cores).
+//
+// Measured on a GB300, floors at 6.79 TB/s and 1954 TFLOP/s (FP4 four times that):
+//   product 8192 rows of 8 experts, 4096 x 28672        1279-1320 us (floor 985; 1115 at the
+//     tensor cores' sustained rate: back to back the clock is down to 1.4 GHz)
+//   product 32 rows of 8 experts, 14336 x 4096          130-134 us (137: HBM)
+//   weight grad 8192 rows of 8, 14336 x 4096 to fp32    740-766 us (492: the output warps)
+//   weight grad 131064 rows of 128, 2048 x 1536, bf16   677-680 us (422; 478 sustained)
+//   FP4 8192 x 7168 x 4096                              83-87 us (62: the round trip of the
+//     five stages that shared memory holds)
+//   FP4 64 rows of 32 experts, 7168 x 4096              71-73 us with the rows' quantisation (64)
 #include <algorithm>
 #include <type_traits>
 
@@ -53,7 +63,7 @@ struct GrGeo {
   // columns of a tile; FP4: two accumulators and the scales share the 512 TMEM columns
   static constexpr int TM = SPLIT ? kGrSplitRows : FP4 ? 224 : 256;
   static constexpr int ACC = FP4 ? 224 : 256;  // TMEM columns from one accumulator to the other
-  static constexpr int SCALES = FP4 ? 3072 : 0;  // of a stage: 128 + 256 rows by 8 bytes
+  static constexpr int SCALES = FP4 ? (128 + 256) * 8 : 0;  // of a stage: 128 + 256 rows by 8 bytes
   static constexpr int SCALES_AT = SPLIT ? 18432 : 32768;  // A, then TM / 2 rows or columns of B
   static constexpr int STAGE = SCALES_AT + SCALES;
   static constexpr int STAGES = SPLIT ? (FP4 ? 6 : 8) : FP4 ? 5 : 6;
@@ -531,11 +541,12 @@ __global__ void __launch_bounds__(kGrThreads, 1)
       // of a row (a chunk: 1024 elements, four stages) at a time, into a ring ----
       // By TMA where rows of scales are whole 16 bytes (K a multiple of 512); else for K up to
       // 1024 as the rows lie in memory, in bulk copies; else by the warp's lanes, a row
-      // each, in asynchronous copies (8192 x 7200 x 4096: 184 us).  Those are as many
-      // requests as lanes, and slower than the MMAs
-      // (8192 x 7168 x 4096: 155 us from registers, 93-100 by asynchronous copies,
-      // 85 by TMA, 78 without any).  The warp that takes the scales from the ring is another
-      // one: its fence for the tensor core's reads would wait for copies in flight.
+      // each, in asynchronous copies.  Those are as many requests as lanes, and slower
+      // than the MMAs (8192 x 7168 x 4096: 155 us from registers, 93-100 by asynchronous
+      // copies, 83-87 by TMA, 78 without any; 8192 x 7200 x 4096: 195; a bulk copy for each
+      // row 849; 32768 rows of 64 experts, K 768, N 2048: 109 by the lanes, 87 in bulk).
+      // The warp that takes the scales from the ring is another one: its fence for the
+      // tensor core's reads would wait for copies in flight.
       const int KG = P.K / 32;
       uint8_t* ring = tiles + G::STAGES * G::STAGE;
       const uint32_t go = ptx::elect_one();
