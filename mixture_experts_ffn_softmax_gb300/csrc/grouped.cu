@@ -115,6 +115,21 @@ __device__ __forceinline__ bool gr_wait(uint64_t* bar, uint32_t parity, int32_t*
   return dense_wait(bar, parity, abort, err);
 }
 
+// n / d for 0 <= n < 2^31: with d in (2^(l-1), 2^l] and m = ceil(2^(31+l) / d), n m is
+// 2^(31+l) n / d + n e, 0 <= e < d, and n e < 2^(31+l) carries it to no next whole number.
+struct GrDiv {
+  uint32_t m = 0, shift = 0;
+  GrDiv() = default;
+  explicit GrDiv(int64_t d) {
+    while ((int64_t(1) << shift) < d) ++shift;
+    shift += 31;
+    m = static_cast<uint32_t>(((uint64_t(1) << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> shift);
+  }
+};
+
 struct GrParams {
   const int32_t* offsets;  // [E + 1], or null: all R rows are expert 0's
   int64_t R;
@@ -126,6 +141,7 @@ struct GrParams {
   int out_f32, accumulate;
   int parts;               // SPLIT: of K
   int chunk;               // stages summed in the tensor core before they go to registers
+  GrDiv raster;            // by the tiles of a raster group (products)
   int32_t* error_word;
 };
 
@@ -142,6 +158,9 @@ struct GrTile {
   int r0, rows;     // the expert's rows
 };
 
+// By whole warps: their lanes look for the expert together.  (Products, without divisions in
+// most calls: 650 cycles of each tile before, a seventh of a short sum's tile.  The weight
+// gradient's short sums were 3 % slower so.)
 template <int MODE, bool SPLIT>
 __device__ __forceinline__ GrTile gr_tile(const GrCtl<MODE, SPLIT>& ctl, const GrParams& P, int t) {
   using G = GrGeo<MODE, SPLIT>;
@@ -153,25 +172,29 @@ __device__ __forceinline__ GrTile gr_tile(const GrCtl<MODE, SPLIT>& ctl, const G
     tl.e = t / (ct * nt);
     r = t - tl.e * (ct * nt);
   } else {
-    int lo = 0, hi = P.E;  // the last expert whose first tile is not behind t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (ctl.tile0[mid] <= t) lo = mid;
-      else hi = mid;
+    // the last expert whose first tile is not behind t: of each 32nd, then of 32
+    const int lane = threadIdx.x & 31;
+    int e = 0;
+#pragma unroll
+    for (int step = 32; step > 0; step -= 31) {
+      if (step == 32 && P.E <= 32) continue;
+      const int i = e + lane * step;
+      e += (__popc(__ballot_sync(0xffffffffu, i < P.E && ctl.tile0[min(i, P.E - 1)] <= t)) - 1) * step;
     }
-    tl.e = lo;
-    r = t - ctl.tile0[lo];
-    ct = ceil_div(ctl.count[lo], G::TM);
+    tl.e = e;
+    r = t - ctl.tile0[e];
+    ct = ceil_div(ctl.count[e], G::TM);
   }
   tl.r0 = ctl.start[tl.e];
   tl.rows = ctl.count[tl.e];
   // raster groups of kGrGroup column tiles by all weight tiles, columns innermost: tiles in
   // flight together share the weight's columns and the rows in L2
   const int per = kGrGroup * nt;
-  const int g = r / per, q = r - g * per;
+  const int g = G::WG ? r / per : P.raster(r), q = r - g * per;
   const int in_group = min(kGrGroup, ct - g * kGrGroup);
-  const int c = (g * kGrGroup + q % in_group) * G::TM;
-  tl.n0 = q / in_group * 256;
+  const int nq = !G::WG && in_group == kGrGroup ? q / kGrGroup : q / in_group;
+  const int c = (g * kGrGroup + q - nq * in_group) * G::TM;
+  tl.n0 = nq * 256;
   tl.cols = min(G::TM, (G::WG ? P.K : tl.rows) - c);
   tl.c0 = G::WG ? c : static_cast<int64_t>(tl.r0) + c;
   // (MN-major columns come in swizzled chunks of 64 per CTA)
@@ -486,8 +509,8 @@ __global__ void __launch_bounds__(kGrThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      const int KB = gr_blocks<MODE, SPLIT>(P, GrTile{}, part, parts).count;
       for (int t = unit; t < total && ok; t += units) {
-        const int KB = gr_blocks<MODE, SPLIT>(P, gr_tile(ctl, P, t), part, parts).count;
         for (int kb = 0; kb < KB; ++kb) {
           if (!gr_wait(&ctl.tail[stage], phase, &ctl.abort, P.error_word)) {
             ok = false;
@@ -845,11 +868,59 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         }
       }
       if (!ok) break;
-      // a warp's store is 32 neighbouring columns of one row (through shared memory and out
-      // in 16-byte stores: the same times; the MMAs' operands take half of its bandwidth)
       const int first = half * groups * 16;
       const int64_t row0 = (G::WG ? static_cast<int64_t>(tl.e) * P.K : 0) + tl.c0 + first;
       const int left = min(tl.cols - first, groups * 16);
+      // Products: the sums change lanes among fours, so that a store is four rows of 32
+      // neighbouring columns n, four columns a lane (FP4 64287 x 320 x 960 to bf16 83.6 -> 70.8
+      // us, 14765 x 288 x 3456 64.2 -> 58.4; long sums the same to 3 % less.  Eight rows,
+      // 16 bytes of bf16 a lane: 79.7 and 66.8).  Weight gradients: a store is 32 columns of one
+      // row (short sums to bf16 10 % slower than by fours, longer ones to fp32 1.5 % faster,
+      // accumulating ones 6 %; through shared memory and out in 16-byte stores: the same).
+      auto put4 = [&](auto* out) {
+        using O = std::remove_pointer_t<decltype(out)>;
+        const int col = n & ~3;
+        const int64_t step = 4 * static_cast<int64_t>(P.N);
+        const bool b0 = lane & 1, b1 = lane & 2;
+        O* p = out + (row0 + (lane & 3)) * P.N + col;
+#pragma unroll
+        for (int i = 0; i < G::TM / 32; ++i) {
+          if (16 * i >= left) break;
+          auto in = [&](int j) { return 16 * i + 4 * j + (lane & 3) < left && col < P.N; };
+          if constexpr (sizeof(O) == 2) {  // two columns' values of a row a word first
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 o = unpair(sum[8 * i + j]);
+              const uint32_t own = pack2(o.x, o.y);
+              h[j] = __byte_perm(own, __shfl_xor_sync(0xffffffffu, own, 1), b0 ? 0x3276 : 0x5410);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? h[2 * j] : h[2 * j + 1], 2);
+              if (in(j))
+                *reinterpret_cast<uint2*>(p) =
+                    b1 ? make_uint2(got, h[2 * j + 1]) : make_uint2(h[2 * j], got);
+              p += step;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 x = unpair(sum[8 * i + 2 * j]), y = unpair(sum[8 * i + 2 * j + 1]);
+              const float gx = __shfl_xor_sync(0xffffffffu, b0 ? x.x : x.y, 1);
+              const float gy = __shfl_xor_sync(0xffffffffu, b0 ? y.x : y.y, 1);
+              const float2 u = b0 ? make_float2(gx, x.y) : make_float2(x.x, gx);
+              const float2 v = b0 ? make_float2(gy, y.y) : make_float2(y.x, gy);
+              const float g0 = __shfl_xor_sync(0xffffffffu, b1 ? u.x : v.x, 2);
+              const float g1 = __shfl_xor_sync(0xffffffffu, b1 ? u.y : v.y, 2);
+              if (in(j))
+                *reinterpret_cast<float4*>(p) =
+                    b1 ? make_float4(g0, g1, v.x, v.y) : make_float4(u.x, u.y, g0, g1);
+              p += step;
+            }
+          }
+        }
+      };
       auto put = [&](auto* out, auto add) {
         using O = std::remove_pointer_t<decltype(out)>;
         O* p = out + row0 * P.N + n;
@@ -883,15 +954,17 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         }
       };
       auto put_as = [&](auto* out) {
-        if constexpr (G::WG) {
-          if (P.accumulate) {
-            put(out, std::true_type{});
-            return;
-          }
-        }
-        put(out, std::false_type{});
+        if (P.accumulate)
+          put(out, std::true_type{});
+        else
+          put(out, std::false_type{});
       };
-      if (n < P.N) {
+      if constexpr (!G::WG) {
+        if (P.out_f32)
+          put4(static_cast<float*>(P.out));
+        else
+          put4(static_cast<bf16*>(P.out));
+      } else if (n < P.N) {
         if (P.out_f32)
           put_as(static_cast<float*>(P.out));
         else
@@ -1018,6 +1091,7 @@ moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const
   P.accumulate = a.accumulate;
   P.parts = parts;
   P.chunk = gr_chunk(a);
+  P.raster = GrDiv(int64_t(kGrGroup) * ceil_div(a.N, 256));
   P.error_word = a.error_word;
   const int64_t clusters = SPLIT ? tiles : std::min<int64_t>(tiles, a.num_sms / 2);
   cudaLaunchConfig_t cfg = {};
