@@ -100,6 +100,7 @@ struct GrCtl {
   int32_t count[kGrMaxExperts];
   int32_t tile0[kGrMaxExperts];   // its first tile (products)
 };
+static_assert(kGrSplitRows / 2 == 16, "the boxes of 16 rows are a CTA's half of these tiles");
 static_assert(GrGeo<kFp4>::SMEM + sizeof(GrCtl<kFp4, false>) <= 232448 &&
                   GrGeo<kFp4, true>::SMEM + sizeof(GrCtl<kFp4, true>) <= 232448 &&
                   GrGeo<kProduct>::SMEM + sizeof(GrCtl<kProduct, false>) <= 232448 &&
@@ -145,8 +146,9 @@ struct GrParams {
   int32_t* error_word;
 };
 
-// Tensor maps: the weight (or dy), the rows in boxes of half a tile's columns and of 16, and
-// FP4's scales of both.
+// Tensor maps: the weight (or dy), the rows in boxes of half a tile's columns (only calls of
+// more rows than tiles with one less 32 take have such tiles; the others go without the map,
+// whose making is part of a small call's time) and of 16, and FP4's scales of both.
 struct GrMaps {
   CUtensorMap a, b, b16, sa, sb;
 };
@@ -1141,14 +1143,14 @@ moe_status_t launch_grouped_matmul(const GroupedProductArgs& a, cudaStream_t s) 
   if (moe_status_t st = a.transposed ? map_3d(&m.a, a.w, K, N, E, 2 * K, 64, 128, kBf16)
                                      : map_3d(&m.a, a.w, N, K, E, 2 * N, 64, 64, kBf16))
     return st;
-  const uint32_t half = parts > 1 ? kGrSplitRows / 2 : 128;
-  if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, half, kBf16)) return st;
-  m.b16 = m.b;
+  if (moe_status_t st = map_2d(&m.b16, a.x, K, R, 2 * K, 64, 16, kBf16)) return st;
+  m.b = m.b16;
   if (parts > 1)
     return a.transposed
                ? launch_grouped<kProductT, true>("grouped_matmul_t_split", a, m, tiles, parts, s)
                : launch_grouped<kProduct, true>("grouped_matmul_split", a, m, tiles, parts, s);
-  if (moe_status_t st = map_2d(&m.b16, a.x, K, R, 2 * K, 64, 16, kBf16)) return st;
+  if (a.R > 256 - 32)
+    if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, 128, kBf16)) return st;
   return a.transposed ? launch_grouped<kProductT, false>("grouped_matmul_t", a, m, tiles, 1, s)
                       : launch_grouped<kProduct, false>("grouped_matmul", a, m, tiles, 1, s);
 }
@@ -1172,11 +1174,10 @@ moe_status_t launch_matmul_fp4(const GroupedProductArgs& a, cudaStream_t s) {
                            : grouped_parts<kFp4Rows>(a, tiles, units);
   GrMaps m;
   if (moe_status_t st = map_3d(&m.a, a.w, KB, N, E, KB, 128, 128, kBytes)) return st;
-  const uint32_t half = parts > 1 ? kGrSplitRows / 2 : 112;
-  if (moe_status_t st = map_2d(&m.b, a.x, KB, R, KB, 128, half, kBytes)) return st;
-  m.b16 = m.b;
-  if (parts == 1)
-    if (moe_status_t st = map_2d(&m.b16, a.x, KB, R, KB, 128, 16, kBytes)) return st;
+  if (moe_status_t st = map_2d(&m.b16, a.x, KB, R, KB, 128, 16, kBytes)) return st;
+  m.b = m.b16;
+  if (parts == 1 && a.R > 224 - 32)
+    if (moe_status_t st = map_2d(&m.b, a.x, KB, R, KB, 128, 112, kBytes)) return st;
   if (rows16) {
     const uint64_t KG = a.K / 32;
     const auto s32 = CU_TENSOR_MAP_SWIZZLE_32B;
