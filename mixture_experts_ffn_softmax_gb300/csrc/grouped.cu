@@ -53,22 +53,24 @@ constexpr int kGrRegsLaunch = 168, kGrRegsFew = 88, kGrRegsMany = 208;
 static_assert(128 * kGrRegsFew + 256 * kGrRegsMany <= kGrThreads * kGrRegsLaunch,
               "register split within the launch's registers");
 
-// SPLIT: for up to 32 rows in all, K in parts over the pairs of a cluster.
-constexpr int kGrSplitRows = 32, kGrMaxParts = 4;
+// SPLIT, over the pairs of a cluster: products of up to 32 rows in all, K in parts; weight
+// gradients of few tiles, an expert's rows in parts.
+constexpr int kGrSplitRows = 32, kGrMaxParts = 4, kGrPartStages = 12;
 template <int MODE, bool SPLIT = false>
 struct GrGeo {
   static constexpr bool FP4 = MODE == kFp4 || MODE == kFp4Rows, WG = MODE == kWeightGrad;
   static constexpr bool A_MN = MODE == kProduct || WG;  // MN-major first operand
   static constexpr int BK = FP4 ? 256 : 64;    // reduced elements of a stage (128 bytes of a row)
   // columns of a tile; FP4: two accumulators and the scales share the 512 TMEM columns
-  static constexpr int TM = SPLIT ? kGrSplitRows : FP4 ? 224 : 256;
+  static constexpr bool FEW = SPLIT && !WG;    // rows
+  static constexpr int TM = FEW ? kGrSplitRows : FP4 ? 224 : 256;
   static constexpr int ACC = FP4 ? 224 : 256;  // TMEM columns from one accumulator to the other
   static constexpr int SCALES = FP4 ? (128 + 256) * 8 : 0;  // of a stage: 128 + 256 rows by 8 bytes
-  static constexpr int SCALES_AT = SPLIT ? 18432 : 32768;  // A, then TM / 2 rows or columns of B
+  static constexpr int SCALES_AT = FEW ? 18432 : 32768;  // A, then TM / 2 rows or columns of B
   static constexpr int STAGE = SCALES_AT + SCALES;
-  static constexpr int STAGES = SPLIT ? (FP4 ? 6 : 8) : FP4 ? 5 : 6;
-  // the other parts' sums, [part][4 columns][128 lanes] of 16 bytes
-  static constexpr int PARTS = SPLIT ? (kGrMaxParts - 1) * kGrSplitRows * 128 * 4 : 0;
+  static constexpr int STAGES = FEW ? (FP4 ? 6 : 8) : FP4 ? 5 : 6;
+  // the other parts' sums, [part][4 columns][128 lanes] of 16 bytes (weight grad: the stages')
+  static constexpr int PARTS = FEW ? (kGrMaxParts - 1) * kGrSplitRows * 128 * 4 : 0;
   static constexpr int SCALE_RING = FP4 ? kScaleChunks * kScaleChunkBytes : 0;
   static constexpr size_t SMEM = 1024 + STAGES * STAGE + SCALE_RING + PARTS;
 };
@@ -104,7 +106,9 @@ static_assert(kGrSplitRows / 2 == 16, "the boxes of 16 rows are a CTA's half of 
 static_assert(GrGeo<kFp4>::SMEM + sizeof(GrCtl<kFp4, false>) <= 232448 &&
                   GrGeo<kFp4, true>::SMEM + sizeof(GrCtl<kFp4, true>) <= 232448 &&
                   GrGeo<kProduct>::SMEM + sizeof(GrCtl<kProduct, false>) <= 232448 &&
-                  GrGeo<kProduct, true>::SMEM + sizeof(GrCtl<kProduct, true>) <= 232448,
+                  GrGeo<kProduct, true>::SMEM + sizeof(GrCtl<kProduct, true>) <= 232448 &&
+                  GrGeo<kWeightGrad>::SMEM + sizeof(GrCtl<kWeightGrad, false>) <= 232448 &&
+                  GrGeo<kWeightGrad, true>::SMEM + sizeof(GrCtl<kWeightGrad, true>) <= 232448,
               "shared memory budget");
 
 // dense_wait, which also ends at once where a wait of this CTA has run out: the loops of the
@@ -157,7 +161,7 @@ struct GrTile {
   int e, n0;        // expert, first column of the weight
   int64_t c0;       // first row of y, or of dW[e]
   int cols, T;      // how many, and rounded up to what the MMA takes
-  int r0, rows;     // the expert's rows
+  int r0, rows;     // the expert's rows (weight grad in parts: the part's)
 };
 
 // By whole warps: their lanes look for the expert together.  (Products, without divisions in
@@ -189,6 +193,13 @@ __device__ __forceinline__ GrTile gr_tile(const GrCtl<MODE, SPLIT>& ctl, const G
   }
   tl.r0 = ctl.start[tl.e];
   tl.rows = ctl.count[tl.e];
+  if constexpr (G::WG && SPLIT) {  // this part's of them, whole stages but for the last
+    const int part = static_cast<int>(ptx::cluster_ctarank()) / 2, blocks = ceil_div(tl.rows, G::BK);
+    const int first = static_cast<int>(int64_t(blocks) * part / P.parts) * G::BK;
+    const int end = static_cast<int>(int64_t(blocks) * (part + 1) / P.parts) * G::BK;
+    tl.rows = min(tl.rows, end) - first;
+    tl.r0 += first;
+  }
   // raster groups of kGrGroup column tiles by all weight tiles, columns innermost: tiles in
   // flight together share the weight's columns and the rows in L2
   const int per = kGrGroup * nt;
@@ -225,7 +236,7 @@ __device__ __forceinline__ GrRange gr_blocks(const GrParams& P, const GrTile& tl
                                              int parts) {
   using G = GrGeo<MODE, SPLIT>;
   const int KB = ceil_div(G::WG ? tl.rows : P.K, G::BK);
-  if constexpr (!SPLIT) return GrRange{0, KB};
+  if constexpr (!G::FEW) return GrRange{0, KB};
   constexpr int UNIT = G::FP4 ? 4 : 1;  // (FP4: whole chunks of scales)
   const int units = ceil_div(KB, UNIT);
   const int first = units * part / parts * UNIT, last = min(units * (part + 1) / parts * UNIT, KB);
@@ -370,7 +381,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
   const int units = static_cast<int>(gridDim.x) / (2 * parts);
 
   if (warp < 4) {
-    if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGrRegsFew));
+    if constexpr (!G::FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGrRegsFew));
     // (The loading and the issuing warp run their loops as one, an elected lane issuing: in a
     // branch of one lane an MMA took 70 cycles to issue, the loop 730 for the 512 that a stage
     // of 256 columns computes.  8 x 1024 rows, K 4096, N 28672: 1193 us so, 1077 as here;
@@ -797,13 +808,16 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     }
   } else {
     // ---- output: 32 columns n of the weight (lanes) by half of the tile's columns a warp ----
-    if constexpr (!SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGrRegsMany));
+    if constexpr (!G::FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGrRegsMany));
     const int q = warp & 3, half = (warp - 4) >> 2;
     [[maybe_unused]] uint8_t* sums = tiles + G::STAGES * G::STAGE + G::SCALE_RING;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&ctl.tmem_empty[0]), even);
     uint32_t acc = 0, turn = 0;
     bool ok = true;
-    if (SPLIT && unit >= total) ptx::cluster_sync();  // (for the others of the CTA: theirs below)
+    if (SPLIT && unit >= total) {  // (for the others of the CTA: theirs below)
+      ptx::cluster_sync();
+      if (G::WG) ptx::cluster_sync();
+    }
     for (int t = unit; t < total && ok; t += units) {
       const GrTile tl = gr_tile(ctl, P, t);
       const int KB = gr_blocks<MODE, SPLIT>(P, tl, part, parts).count;
@@ -845,7 +859,50 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         acc ^= 1u;
         turn ^= acc == 0 ? 1u : 0u;
       }
-      if constexpr (SPLIT) {
+      // in parts: the groups of 16 columns go round the parts, each of which takes the others'
+      // sums of its groups, where the stages were, adds them in order and writes them
+      auto mine = [&](int i) { return !(G::WG && SPLIT) || (i & (parts - 1)) == part; };
+      if constexpr (G::WG && SPLIT) {
+        constexpr int GROUPS = G::TM / 32;
+        const int each = GROUPS / parts;
+        auto place = [&](int i, int from) {  // group i of part `from`, 16 bytes of a lane's 64
+          const int owner = i & (parts - 1), slot = from - (from > owner ? 1 : 0);
+          return ((((slot * each + i / parts) * 2 + half) * 4 + q) * 128 + lane) * 16;
+        };
+        static_assert((kGrMaxParts - 1) * (GROUPS / kGrMaxParts) * 8 * 2048 <= G::STAGES * G::STAGE &&
+                          GROUPS / 2 * 8 * 2048 <= G::STAGES * G::STAGE, "room for the sums");
+        __syncwarp();
+        ptx::cluster_sync();  // every part's MMAs are through, its stages free
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+          if (i < groups && !mine(i)) {
+            const uint32_t to = ptx::mapa_shared(ptx::smem_u32(tiles + place(i, part)),
+                                                 2 * (i & (parts - 1)) + rank);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 x = unpair(sum[8 * i + 2 * j]), y = unpair(sum[8 * i + 2 * j + 1]);
+              st_cluster_f32x4(to + j * 512, x.x, x.y, y.x, y.y);
+            }
+          }
+        }
+        __syncwarp();
+        ptx::cluster_sync();
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+          if (i < groups && mine(i)) {
+            for (int p = 0; p < parts; ++p) {
+              if (p == part) continue;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 v = *reinterpret_cast<const float4*>(tiles + place(i, p) + j * 512);
+                sum[8 * i + 2 * j] = add2(sum[8 * i + 2 * j], pair_of(v.x, v.y));
+                sum[8 * i + 2 * j + 1] = add2(sum[8 * i + 2 * j + 1], pair_of(v.z, v.w));
+              }
+            }
+          }
+        }
+      }
+      if constexpr (G::FEW) {
         // the other parts' sums to the first part's CTA of this rank, which adds them in order
         if (part > 0) {
           const uint32_t to = ptx::mapa_shared(
@@ -949,6 +1006,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
 #pragma unroll
         for (int i = 0; i < G::TM / 32; ++i) {
           if (16 * i >= left) break;
+          if (!mine(i)) continue;
           if (16 * i + 16 <= left)
             store(i, std::true_type{});
           else
@@ -976,7 +1034,10 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     }
   }
   __syncwarp();
-  if (SPLIT && warp < 4) ptx::cluster_sync();  // the exchange of the parts' sums
+  if (SPLIT && warp < 4) {  // the exchange of the parts' sums
+    ptx::cluster_sync();
+    if (G::WG) ptx::cluster_sync();
+  }
   ptx::cluster_sync();
   // the commits of the last use of every stage have to arrive before the barriers' memory
   // goes: each of them (see the dense FP8 pairs)
@@ -1037,17 +1098,13 @@ cudaError_t grouped_prepare(int* regs) {  // once per device
       regs);
 }
 
-// Parts of K for a product of up to 32 rows, of `tiles` tiles at most and `units` that a part
-// can be made of: as many as leave all clusters resident, where one part of K leaves
-// SMs idle.  1 x 7168 x 4096: bf16 25.4 us in one part, 11.8 so; FP4 12.6 and 10.0; 2 x
-// 14336 x 4096, an expert each: 49.1 and 37.4.
+// How many clusters of `parts` pairs fit on the GPU at a time.
 template <int MODE>
-int grouped_parts(const GroupedProductArgs& a, int64_t tiles, int units) {
-  if (a.R > kGrSplitRows || tiles * 4 > a.num_sms) return 1;
+int clusters_that_fit(int parts) {
   int dev = 0, regs = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || grouped_prepare<MODE, true>(&regs) != cudaSuccess) {
     cudaGetLastError();
-    return 1;
+    return 0;
   }
   thread_local int room_dev = -1, room[kGrMaxParts + 1];
   if (dev != room_dev) {  // how many clusters fit: asked once per host thread and device
@@ -1063,8 +1120,18 @@ int grouped_parts(const GroupedProductArgs& a, int64_t tiles, int units) {
     }
     room_dev = dev;
   }
+  return room[parts];
+}
+
+// Parts of K for a product of up to 32 rows, of `tiles` tiles at most and `units` that a part
+// can be made of: as many as leave all clusters resident, where one part of K leaves
+// SMs idle.  1 x 7168 x 4096: bf16 25.4 us in one part, 11.8 so; FP4 12.6 and 10.0; 2 x
+// 14336 x 4096, an expert each: 49.1 and 37.4.
+template <int MODE>
+int grouped_parts(const GroupedProductArgs& a, int64_t tiles, int units) {
+  if (a.R > kGrSplitRows || tiles * 4 > a.num_sms) return 1;
   int parts = 1;
-  for (int c = 2; c <= kGrMaxParts && c <= units && tiles <= room[c]; ++c) parts = c;
+  for (int c = 2; c <= kGrMaxParts && c <= units && tiles <= clusters_that_fit<MODE>(c); ++c) parts = c;
   return parts;
 }
 
@@ -1076,7 +1143,7 @@ moe_status_t launch_grouped(const char* name, const GroupedProductArgs& a, const
     return set_error(MOE_ERR_CUDA, "attributes of %s: %s", name,
                      cudaGetErrorString(cudaGetLastError()));
   // fewer registers at launch would leave the output warps waiting for more
-  if (!SPLIT && regs < kGrRegsLaunch)
+  if (!GrGeo<MODE, SPLIT>::FEW && regs < kGrRegsLaunch)
     return set_error(MOE_ERR_CUDA, "%s was compiled to %d registers, %d needed", name, regs,
                      kGrRegsLaunch);
   GrParams P{};
@@ -1162,6 +1229,18 @@ moe_status_t launch_grouped_weight_grad(const GroupedProductArgs& a, cudaStream_
   if (moe_status_t st = map_2d(&m.b, a.x, K, R, 2 * K, 64, 64, kBf16)) return st;
   m.b16 = m.b;
   const int64_t tiles = int64_t(a.E) * ceil_div(a.K, 256) * ceil_div(a.N, 256);
+  // Rows in parts where the tiles leave half of the pairs idle, and an expert's rows are
+  // kGrPartStages stages of each part at least (by the mean: their offsets are on the
+  // device).  49722 x 3856 x 72 to fp32 242 -> 129 us, 8192 x 512 x 1024 41.3 -> 21.2, 4096 x
+  // 1024 x 1024 24.7 -> 19.0; the exchange takes 2 us: in parts of 4 stages 1024 x 1024 x 1024
+  // would take 12.6 instead of 12.1, 512 x 1024 x 2048 12.3 instead of 10.2.
+  int parts = 1;
+  for (int c = 2; c <= kGrMaxParts; c *= 2)
+    if (tiles * 2 * c <= a.num_sms && a.R >= int64_t(a.E) * c * 64 * kGrPartStages &&
+        tiles <= clusters_that_fit<kWeightGrad>(c))
+      parts = c;
+  if (parts > 1)
+    return launch_grouped<kWeightGrad, true>("grouped_weight_grad_split", a, m, tiles, parts, s);
   return launch_grouped<kWeightGrad, false>("grouped_weight_grad", a, m, tiles, 1, s);
 }
 

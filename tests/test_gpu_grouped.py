@@ -277,6 +277,38 @@ def test_weight_grad_exact(counts, K, N):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("counts,K,N,split", [
+    ([1536], 520, 264, True), ([1601], 1000, 1032, True), ([5000, 1, 0], 264, 136, True),
+    ([0, 3500], 72, 8, True), ([5, 6000, 77, 500], 512, 520, True), ([1535], 264, 264, False),
+    ([4000], 2560, 2048, False), ([4096] * 2, 1536, 768, True)])
+def test_weight_grad_of_few_tiles_in_parts_of_the_rows(counts, K, N, split):
+    """Sums over rows that the pairs of a cluster share: parts without rows, rows
+    that end inside a stage, tiles of 128 columns and of fewer, both output
+    types, added to what is there, the same bits in calls one behind the other."""
+    E, R = len(counts), sum(counts)
+    off = offsets_of(counts, 3)
+    x, dy = ints(1, R + 5, K, top=1), ints(2, R + 5, N, top=1)
+    for t in (x, dy):
+        t[:3], t[-2:] = float("nan"), float("inf")
+    ref = weight_reference(x, dy, off)
+    name = name_of(lambda: pkg.moe_grouped_weight_grad(x, dy, off))
+    # (rows of nobody count among those that decide)
+    assert name == ["grouped_weight_grad" + "_split" * (split or R == 1535)]
+    x2, dy2, off2 = x[3:-2].clone(), dy[3:-2].clone(), off - 3
+    assert name_of(lambda: pkg.moe_grouped_weight_grad(x2, dy2, off2)) == [
+        "grouped_weight_grad" + "_split" * split]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (F32, BF16):
+        outs = [torch.full((E, K, N), 9.0, device="cuda", dtype=dt) for _ in range(6)]
+        for i, out in enumerate(outs):
+            a = (x, dy, off) if i % 2 else (x2, dy2, off2)
+            pkg.moe_grouped_weight_grad(*a, out=out, error_word=err)
+        assert all(torch.equal(out, ref.to(dt)) for out in outs)
+        pkg.moe_grouped_weight_grad(x, dy, off, out=outs[0], accumulate=True, error_word=err)
+        assert torch.equal(outs[0], (ref.to(dt).double() + ref).to(dt))
+    assert err.item() == 0
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_weight_grad_within_rounding(dtype):
     """As for the product, the reduced side being an expert's rows: up to 20000."""
