@@ -13,14 +13,14 @@
 // few rows (bound by the weights' bytes) and a long prefill (bound by the tensor cores).
 //
 // Measured on a GB300, floors at 6.79 TB/s and 1954 TFLOP/s (FP4 four times that):
-//   product 8192 rows of 8 experts, 4096 x 28672        1279-1294 us (floor 985; 1115 at the
+//   product 8192 rows of 8 experts, 4096 x 28672        1276-1294 us (floor 985; 1115 at the
 //     tensor cores' sustained rate: back to back the clock is down to 1.4 GHz)
 //   product 32 rows of 8 experts, 14336 x 4096          130-136 us (137: HBM)
-//   weight grad 8192 rows of 8, 14336 x 4096 to fp32    740-766 us (492: the output's stores)
-//   weight grad 131064 rows of 128, 2048 x 1536, bf16   653-681 us (422; 478 sustained)
+//   weight grad 8192 rows of 8, 14336 x 4096 to fp32    736-766 us (492: the output's stores)
+//   weight grad 131064 rows of 128, 2048 x 1536, bf16   643-681 us (422; 478 sustained)
 //   FP4 8192 x 7168 x 4096                              83-87 us (62: the round trip of the
 //     five stages that shared memory holds)
-//   FP4 64 rows of 32 experts, 7168 x 4096              71-76 us with the rows' quantisation (64)
+//   FP4 64 rows of 32 experts, 7168 x 4096              68-76 us with the rows' quantisation (64)
 #include <algorithm>
 #include <type_traits>
 
