@@ -27,6 +27,7 @@
 #include "common.cuh"
 #include "dense.cuh"
 #include "ptx.cuh"
+#include "raw_scales.cuh"
 
 namespace gbmoe {
 namespace {
@@ -606,32 +607,24 @@ __global__ void __launch_bounds__(kGrThreads, 1)
             if (tl.T > 128)
               ptx::tma_load_2d_if(go, dst + 8192, &maps.sb, bar, g, static_cast<int>(tl.c0) + 128);
           } else if (KG <= 32) {
-            // the rows that are there, in one piece each of the two tensors, from a multiple
-            // of 16 bytes on and to one, but not past the tensor
+            // the rows that are there, in one piece each of the two tensors
             if (go) {
               uint8_t* dst = ring + slot * kRawChunkBytes;
-              const int64_t wrow = static_cast<int64_t>(tl.e) * P.N + n;
-              const int64_t from[2] = {wrow * KG, tl.c0 * KG};
-              const int64_t to[2] = {(wrow + max(min(128, P.N - n), 0)) * KG,
-                                     min(tl.c0 + tl.T, P.R) * KG};
-              const int64_t end[2] = {static_cast<int64_t>(P.E) * P.N * KG, P.R * KG};
-              uint32_t bytes[2];
+              const RawSpan span[2] = {weight_scale_span(P.E, P.N, KG, tl.e, n),
+                                       row_scale_span(P.R, KG, tl.c0, tl.T)};
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const uint8_t* src = i == 0 ? P.w_scale : P.x_scale;
-                const int64_t a = from[i] & ~int64_t(15);
-                const int64_t z = min((to[i] + 15) & ~int64_t(15), end[i] & ~int64_t(15));
-                bytes[i] = to[i] > from[i] && z > a ? static_cast<uint32_t>(z - a) : 0u;
-                for (int64_t q = max(z, a); q < to[i]; ++q)  // (a tensor's last bytes)
-                  dst[i * kRawTile + static_cast<int>(q - a)] = __ldg(src + q);
+                // (a tensor's last bytes)
+                for (int64_t q = span[i].begin + span[i].bulk; q < span[i].end; ++q)
+                  dst[i * kRawTile + static_cast<int>(q - span[i].begin)] = __ldg(src + q);
               }
-              ptx::mbar_arrive_expect_tx(bar, bytes[0] + bytes[1]);
+              ptx::mbar_arrive_expect_tx(bar, span[0].bulk + span[1].bulk);
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                if (bytes[i] > 0)
+                if (span[i].bulk > 0)
                   ptx::bulk_load(dst + i * kRawTile,
-                                 (i == 0 ? P.w_scale : P.x_scale) + (from[i] & ~int64_t(15)),
-                                 bytes[i], bar);
+                                 (i == 0 ? P.w_scale : P.x_scale) + span[i].begin, span[i].bulk, bar);
             }
             __syncwarp();
           } else {

@@ -2,6 +2,8 @@
 against independent computations, and the refusals of the C ABI and of the
 binding."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -193,3 +195,51 @@ def test_binding_refusals_of_grouped_products():
     _raises("w_scale has shape", m, u8(8, 32), u8(8, 2), u8(2, 8, 32), u8(8, 2), off)
     _raises("whole blocks", m, u8(4, 24), u8(4, 1), u8(8, 24), u8(8, 1))
     _raises("CUDA device", m, u8(8, 32), u8(8, 2), u8(2, 8, 32), u8(2, 8, 2), off)
+
+
+# ------------------------------------------------------ ranges that are read --
+SPANS = r"""
+#include <algorithm>
+#include <cstdio>
+#include "raw_scales.cuh"
+using namespace gbmoe;
+// within the tensor, in whole aligned 16 bytes, every byte of [from, to) and none before
+// the 16 that hold the first
+static bool good(const RawSpan& s, int64_t from, int64_t to, int64_t total) {
+  if (to <= from) return s.bulk == 0 && s.begin + s.bulk >= s.end;
+  const int64_t past = s.begin + s.bulk;
+  return s.begin % 16 == 0 && s.bulk % 16 == 0 && s.begin <= from && from - s.begin < 16 &&
+         past <= total && s.end <= total && std::max(past, s.end) >= to &&
+         std::max(past, s.end) < to + 16 && s.end - past < 16;
+}
+int main() {
+  for (int KG = 1; KG <= 32; ++KG) {
+    for (int E = 1; E <= 3; ++E)
+      for (int N = 8; N <= 528; N += 8)
+        for (int e = 0; e < E; ++e)
+          for (int n = 0; n < (N + 255) / 256 * 256; n += 128) {
+            const int64_t row = int64_t(e) * N + n, rows = std::min(std::max(N - n, 0), 128);
+            if (!good(weight_scale_span(E, N, KG, e, n), row * KG, (row + rows) * KG, int64_t(E) * N * KG))
+              return std::printf("weight KG=%d E=%d N=%d e=%d n=%d\n", KG, E, N, e, n), 1;
+          }
+    for (int64_t R : {1, 2, 5, 31, 32, 33, 230, 700, 2147482624})
+      for (int64_t c0 : {int64_t(0), int64_t(1), int64_t(7), int64_t(224), R - 1, R - 31, R - 225})
+        for (int T = 32; T <= 224 && c0 >= 0 && c0 < R; T += 32)
+          if (!good(row_scale_span(R, KG, c0, T), c0 * KG, std::min(c0 + T, R) * KG, R * KG))
+            return std::printf("rows KG=%d R=%lld c0=%lld T=%d\n", KG, (long long)R, (long long)c0, T), 1;
+  }
+  return 0;
+}
+"""
+
+
+def test_scales_are_read_inside_their_tensors(tmp_path):
+    """The bulk copies of MX FP4 scales for every row length up to 32, both CTAs of a
+    tile (the second may have no column at all), every expert."""
+    csrc = os.path.join(os.path.dirname(pkg.__file__), "csrc")
+    (tmp_path / "spans.cpp").write_text(SPANS)
+    exe = str(tmp_path / "spans")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-x", "c++", "-I", csrc, str(tmp_path / "spans.cpp"),
+                    "-o", exe], check=True, timeout=300)
+    p = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stdout
