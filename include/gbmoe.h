@@ -515,6 +515,9 @@ GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const
  *                  that no row is computed twice.
  *  error_word      device int32 or NULL; also MOE_ERR_TIMEOUT if a pipeline wait ran
  *                  out of time (the output is then incomplete)
+ * Sums are held in fp32.  The tensor core adds 16 products (FP4: 64) at a time and truncates;
+ * at least every 512 (2048) of a sum for fp32 outputs and every 1024 (4096) for bf16 ones it
+ * is rounded to nearest, so that what truncation drops does not grow with its length.
  * Results do not depend on timing.  A row's do not depend on the rows beside it, but
  * that calls of up to 32 rows may sum K in parts, and weight gradients of few tiles their
  * rows (the profiler's names then end in _split).  out must not overlap the inputs; operands, bias,
@@ -526,8 +529,7 @@ GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const
  *  w     w_transposed = 0: device bf16 [E, K, N], the orientation of w13 and w2;
  *        1: [E, N, K].  One stored weight so serves y = x W and dx = dy W^T.
  *  bias  device bf16 [E, N] or NULL
- *  out   device bf16 [R, N], or fp32 with out_f32 = 1 (sums rounded to nearest at
- *        least every 512 of K)
+ *  out   device bf16 [R, N], or fp32 with out_f32 = 1
  * K and N multiples of 8.
  */
 GBMOE_API moe_status_t moe_grouped_matmul(const void* x, const void* w,

@@ -1054,10 +1054,14 @@ __global__ void __launch_bounds__(kGrThreads, 1)
 
 // Stages per accumulation.  The tensor core's accumulator drops what lies below its last bit
 // at every addition instead of rounding (measured: a product of K = 14336 comes out 1.4e-5
-// too small, in proportion to K), so that sums that leave in fp32 go to registers, where they
-// are rounded to nearest, every 512 rows or columns (FP4: 2048; an MMA is four times as
-// deep).  Sums that leave in bf16 lose 4e-3 in their own rounding, and go there once.
-int gr_chunk(const GroupedProductArgs& a) { return a.out_f32 ? 8 : 1 << 30; }
+// too small, in proportion to K), so that sums go to registers, where they are rounded to
+// nearest, every 512 rows or columns where they leave in fp32 (FP4: 2048; an MMA is four
+// times as deep), and every 1024 (4096) where they leave in bf16: 64 MMAs drop 1.5e-5 at
+// most, whatever the sum's length, beside the output's own rounding of 4e-3 (2^22 positive
+// products in the tensor core alone come out 2.4 % too small).  Against the whole sum there: 8192 rows of 8, 4096 x 28672, 1326 -> 1332 us, 131064 rows of 128, 1536 x
+// 2048, 582 -> 575, their weight gradient 681 -> 684, 1 x 7168 x 4096 11.6 -> 11.7 (every
+// 512: 1336, 578, 692 and 11.8).
+int gr_chunk(const GroupedProductArgs& a) { return a.out_f32 ? 8 : 16; }
 
 // A launch with clusters of `ctas` (cfg.attrs: room for two).
 void grouped_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* at, int ctas, unsigned grid,

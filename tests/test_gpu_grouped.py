@@ -485,3 +485,60 @@ def test_weight_grad_past_32_bits():
     x, dy = ints(3, E * 2, K), ints(4, E * 2, N)
     got = pkg.moe_grouped_weight_grad(x, dy, offsets_of([2] * E), out_dtype=BF16)
     assert torch.equal(got[-1], (x[-2:].double().t() @ dy[-2:].double()).to(BF16))
+
+
+# --------------------------------------------------------------- long sums --
+def long_sum_error(y, ref, adds, rounded):
+    """Of a bf16 result whose summands all have one sign: it is the rounded fp32
+    sum, whose own error is `adds` additions within an accumulation that drop at
+    most 2^-23 each and `rounded` of those behind one another, 2^-24 each.  The mean
+    over results of many different mantissas: their roundings, of either sign, go
+    out of it (2^-8 / sqrt(3) / sqrt(elements): 4e-5 for 4096, 1.3e-4 for 320)."""
+    err = (y.double() - ref) / ref
+    slack = adds * 2 * U32 + rounded * U32
+    assert (err.abs() <= U16 * (1 + 1e-3) + slack).all()
+    assert err.mean().abs().item() < 2.0 ** -10
+
+
+def positive(seed, *shape):
+    """bf16 in [0.5, 1.5), made in pieces."""
+    t = torch.empty(*shape, device="cuda", dtype=BF16)
+    g = gen(seed)
+    for p in t.view(-1).split(1 << 27):
+        p.copy_(torch.rand(p.shape, generator=g, device="cuda") + 0.5)
+    return t
+
+
+@pytest.mark.parametrize("counts", [[1 << 23], [1 << 22, 0, (1 << 23) - 77]])
+def test_weight_grad_of_millions_of_rows_to_bf16(counts):
+    """An accumulation takes 1024 rows, 64 MMAs: the error does not grow with the rows
+    as that of the tensor core's truncating sum does (8e-3 for 2^23)."""
+    K = N = 64
+    x, dy = positive(1, sum(counts), K), positive(2, sum(counts), N)
+    x[:, 1::2] *= 0.7109375
+    dy[:, 1::2] *= 0.8515625
+    off = offsets_of(counts)
+    y = pkg.moe_grouped_weight_grad(x, dy, off, out_dtype=BF16)
+    o = off.tolist()
+    for e, (a, b) in enumerate(zip(o, o[1:])):
+        if a == b:
+            assert (y[e] == 0).all()
+            continue
+        ref = sum(x[i:min(i + (1 << 20), b)].double().t() @ dy[i:min(i + (1 << 20), b)].double()
+                  for i in range(a, b, 1 << 20))
+        long_sum_error(y[e], ref, 2 * 64, counts[e] / 1024 + 4)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("R", [32, 40])
+def test_product_of_millions_of_K_to_bf16(R, transposed):
+    """As above, K in parts (32 rows) and not; rows of different lengths, so that their
+    sums' mantissas differ."""
+    K, N = 1 << 22, 8
+    x = positive(1, R, K)
+    for r in range(R):
+        x[r, K - r * (K // 128):] = 0
+    w = positive(2, 1, N, K) if transposed else positive(2, 1, K, N)
+    y = pkg.moe_grouped_matmul(x, w, offsets_of([R]), transposed=transposed)
+    m = w[0].double()
+    long_sum_error(y, x.double() @ (m.t() if transposed else m), 2 * 64, K / 1024 + 4)

@@ -337,3 +337,25 @@ def test_product_past_32_bits(R, N, K):
     m, n = min(R, 40), min(N, 136)
     ref = values64(a[-m:], sa[-m:]) @ values64(w[-n:], sw[-n:]).t()
     assert torch.equal(y[-m:, -n:], ref.to(BF16))
+
+
+@pytest.mark.parametrize("R", [32, 40])
+def test_product_of_millions_of_K_to_bf16(R):
+    """Positive codes: an accumulation takes 4096 of K, 64 MMAs of a sum and an addition
+    that drop at most 2^-23 each; those are added with 2^-24 each.  The mean over rows of
+    different lengths, whose sums' mantissas differ, leaves the results' own roundings
+    out (2^-8 / sqrt(3) / sqrt(256) = 1.4e-4); a sum of 2^22 in the tensor core alone is
+    1e-3 too small."""
+    K, N = 1 << 22, 8
+    a, sa = codes(1, (R,), K, 127, 128)
+    w, sw = codes(3, (N,), K, 127, 128)
+    a &= 0x77
+    w &= 0x77
+    for r in range(R):
+        a[r, K // 2 - r * (K // 256):] = 0
+    y = pkg.moe_matmul_fp4(a, sa, w, sw).double()
+    w64 = values64(w, sw)
+    ref = torch.cat([values64(a[r:r + 1], sa[r:r + 1]) @ w64.t() for r in range(R)])
+    err = (y - ref) / ref
+    assert (err.abs() <= U16 * (1 + 1e-3) + 2 * 64 * 2 * U32 + (K / 4096 + 4) * U32).all()
+    assert err.mean().abs().item() < 2.0 ** -11
