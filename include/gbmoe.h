@@ -520,7 +520,9 @@ GBMOE_API moe_status_t moe_matmul_fp8(const void* a, const float* a_scale, const
  * is rounded to nearest, so that what truncation drops does not grow with its length.
  * Results do not depend on timing.  A row's do not depend on the rows beside it, but
  * that calls of up to 32 rows may sum K in parts, and weight gradients of few tiles their
- * rows (the profiler's names then end in _split).  out must not overlap the inputs; operands, bias,
+ * rows (the profiler's names then end in _split).  For one expert the parts of K go by K and N
+ * alone; for several also by how many of them R rows can reach, so that a row's last bits may
+ * differ between calls of other R.  out must not overlap the inputs; operands, bias,
  * scales and out 16-byte aligned.  Limits: E <= 1024, R <= 2^31 - 1024, K and N up to
  * 2^22, R * N <= 2^44, E ceil(K/256) ceil(N/256) < 2^30.
  *

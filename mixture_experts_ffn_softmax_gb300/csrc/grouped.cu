@@ -1123,7 +1123,8 @@ int clusters_that_fit(int parts) {
 // Parts of K for a product of up to 32 rows, of `tiles` tiles at most and `units` that a part
 // can be made of: as many as leave all clusters resident, where one part of K leaves
 // SMs idle.  1 x 7168 x 4096: bf16 25.4 us in one part, 11.8 so; FP4 12.6 and 10.0; 2 x
-// 14336 x 4096, an expert each: 49.1 and 37.4.
+// 14336 x 4096, an expert each: 49.1 and 37.4.  (The tiles are those of the experts that R rows
+// can reach: counted by E, calls of fewer rows than experts would have fewer parts.)
 template <int MODE>
 int grouped_parts(const GroupedProductArgs& a, int64_t tiles, int units) {
   if (a.R > kGrSplitRows || tiles * 4 > a.num_sms) return 1;

@@ -542,3 +542,26 @@ def test_product_of_millions_of_K_to_bf16(R, transposed):
     y = pkg.moe_grouped_matmul(x, w, offsets_of([R]), transposed=transposed)
     m = w[0].double()
     long_sum_error(y, x.double() @ (m.t() if transposed else m), 2 * 64, K / 1024 + 4)
+
+
+def test_rows_of_calls_in_parts_of_K_agree():
+    """One weight, up to 32 rows: the parts go by K and N alone.  With several experts
+    they go by R too; a row's sum is then within its bound (see
+    test_product_within_rounding) in either company."""
+    K, N = 4096, 520
+    w = torch.randn(8, K, N, generator=gen(1), device="cuda").to(BF16)
+    x = torch.randn(32, K, generator=gen(2), device="cuda").to(BF16)
+    z = torch.zeros(32, N, device="cuda", dtype=torch.float64)
+    one = offsets_of([32])
+    few = pkg.moe_grouped_matmul(x, w[:1], one, out_dtype=F32)
+    ref, size = reference(x, w, one, z), reference(x.abs(), w.abs(), one, z)
+    assert not torch.equal(few, ref.float())
+    bound = U32 * ref.abs() + (2 * 32 + K / 512 + 3 + 2) * 2 * U32 * size
+    for n in (1, 7, 31, 32):
+        got = []
+        assert name_of(lambda: got.append(pkg.moe_grouped_matmul(
+            x[:n].clone(), w[:1], offsets_of([n]), out_dtype=F32))) == ["grouped_matmul_split"]
+        assert torch.equal(got[0], few[:n])
+    for counts in ([1] + [0] * 7, [2] * 8, [4] * 8):
+        y = pkg.moe_grouped_matmul(x[:sum(counts)].clone(), w, offsets_of(counts), out_dtype=F32)
+        assert ((y[0].double() - ref[0]).abs() <= bound[0]).all()

@@ -359,3 +359,52 @@ def test_product_of_millions_of_K_to_bf16(R):
     err = (y - ref) / ref
     assert (err.abs() <= U16 * (1 + 1e-3) + 2 * 64 * 2 * U32 + (K / 4096 + 4) * U32).all()
     assert err.mean().abs().item() < 2.0 ** -11
+
+
+def name_of(call):
+    pkg.profiler_start()
+    try:
+        call()
+    finally:
+        took = pkg.profiler_stop()
+    return list(took)
+
+
+@pytest.mark.parametrize("K", [2048, 4128, 7168])
+def test_rows_of_calls_in_parts_of_K_agree(K):
+    """One weight, up to 32 rows: the parts go by K and N alone, and a row's sum, inexact
+    here, is the same in any company."""
+    N = 264
+    w, sw = codes(3, (N,), K, 100, 150)
+    a, sa = codes(1, (32,), K, 100, 150)
+    few = pkg.moe_matmul_fp4(a, sa, w, sw, out_dtype=F32)
+    ref = values64(a, sa) @ values64(w, sw).t()
+    assert not torch.equal(few, ref.float())
+    for n in (1, 7, 31, 32):
+        got = []
+        name = name_of(lambda: got.append(pkg.moe_matmul_fp4(a[:n].clone(), sa[:n].clone(), w, sw,
+                                                             out_dtype=F32)))
+        assert name == ["matmul_fp4_split"] and torch.equal(got[0], few[:n])
+
+
+def test_rows_of_several_experts_in_other_numbers_of_parts():
+    """Of E experts as many count as have rows at most: the parts, and with them the order
+    of a row's sum, go by R too.  Either sum is within its bound (an MMA's 64 products and its
+    addition drop at most 2^-23 each, 2048 of K at a time; those sums and the parts'
+    are rounded to nearest)."""
+    E, N, K = 8, 2056, 7168
+    w, sw = codes(3, (E, N), K, 110, 140)
+    a, sa = codes(1, (24,), K, 110, 140)
+    off = offsets_of([3] * E)
+    alone = offsets_of([1] + [0] * (E - 1))
+    rows = []
+    for r, o in ((24, off), (1, alone)):
+        got = []
+        name = name_of(lambda: got.append(pkg.moe_matmul_fp4(a[:r].clone(), sa[:r].clone(), w, sw, o,
+                                                             out_dtype=F32)))
+        assert name == ["matmul_fp4" + "_split" * (r == 1)]
+        rows.append(got[0][:1].double())
+    a64, w64 = values64(a[:1], sa[:1]), values64(w[0], sw[0])
+    ref, size = a64 @ w64.t(), a64.abs() @ w64.abs().t()
+    for y in rows:
+        assert ((y - ref).abs() <= U32 * ref.abs() + (2 * 32 + K / 2048 + 3 + 2) * 2 * U32 * size).all()
