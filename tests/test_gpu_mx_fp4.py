@@ -408,3 +408,33 @@ def test_rows_of_several_experts_in_other_numbers_of_parts():
     ref, size = a64 @ w64.t(), a64.abs() @ w64.abs().t()
     for y in rows:
         assert ((y - ref).abs() <= U32 * ref.abs() + (2 * 32 + K / 2048 + 3 + 2) * 2 * U32 * size).all()
+
+
+def test_quant_swiglu_not_finite():
+    """A block whose SiLU(gate) * up has a NaN or an infinity, from the inputs or by leaving
+    fp32, has the NaN scale and codes of 0; blocks with far gates are those of z in 64
+    bits; the blocks beside keep theirs."""
+    inf, nan = float("inf"), float("nan")
+    K, base = 96, 1.0
+    bad = [(inf, 1.0), (-inf, 1.0), (nan, 1.0), (1.0, inf), (1.0, nan), (0.0, inf), (1e30, 1e30),
+           (3e38, -3e38)]
+    far = [(79.0, 2.0), (-79.0, 2.0), (81.0, 2.0), (300.0, 2.0), (-300.0, 2.0), (3e38, 0.5), (-3e38, 3.0),
+           (1e30, 2.0)]
+    M = len(bad) + len(far)
+    x = torch.full((M, 2 * K), base, device="cuda", dtype=BF16)
+    clean = pkg.moe_quant_mx_fp4(x, swiglu=True)
+    for r, (g, u) in enumerate(bad + far):
+        x[r, 40], x[r, K + 40] = g, u
+    values = torch.empty(M, K, device="cuda", dtype=BF16)
+    q, s = pkg.moe_quant_mx_fp4(x, swiglu=True, values=values)
+    for t, c, per in ((q, clean[0], 16), (s, clean[1], 1)):
+        assert torch.equal(t[:, :per], c[:, :per]) and torch.equal(t[:, 2 * per:], c[:, 2 * per:])
+    n = len(bad)
+    assert (s[:n, 1] == 255).all() and (q[:n, 16:32] == 0).all()
+    assert torch.isnan(values[:n, 32:64]).all() and torch.isfinite(values[:n, :32]).all()
+    # (no z here is within 8 * 2^-24 of a border)
+    code, scale = oracle.quant_mx_fp4(oracle.swiglu(x[n:].double().cpu().numpy()))
+    assert np.array_equal(s[n:].cpu().numpy(), scale)
+    got = oracle.mx_fp4_values(q[n:].cpu().numpy(), scale)
+    assert np.array_equal(got, oracle.mx_fp4_values(oracle.pack_fp4(code), scale))
+    assert np.array_equal(values[n:].double().cpu().numpy(), got)

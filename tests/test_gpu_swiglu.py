@@ -96,3 +96,59 @@ def test_swiglu_past_32_bits():
     assert torch.equal(z[-9:], pkg.moe_swiglu(small[0], small[2]))
     sd, sdw = pkg.moe_swiglu_backward(small[1], small[0], small[2])
     assert torch.equal(d[-9:], sd) and torch.equal(dw[-9:], sdw)
+
+
+INF, NAN = float("inf"), float("nan")
+# gates, up and grad_z that meet in one column: not finite, either side of where e^-g and the
+# fast form end, products that leave fp32
+GATES = [INF, -INF, NAN, 79.0, -79.0, 80.0, -80.0, 88.0, -88.0, 3e38, -3e38, 1e30, 1.0, 0.0, 1.0, 2.0]
+UPS = [1.0, 1.0, 1.0, 2.0, 2.0, 2.0, 2.0, 1.5, 1.5, 0.5, 0.5, 1e30, INF, INF, NAN, -INF]
+
+
+def same_as_formula(got, ref, tol):
+    """NaN where the formula has it, the same infinities, finite values within tol."""
+    got, ref = got.double(), ref.to(got.dtype).double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+    fine = torch.isfinite(ref)
+    assert torch.isfinite(got[fine]).all()
+    assert ((got - ref)[fine].abs() <= tol * ref[fine].abs() + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("I", [24, 264, 2056])
+def test_swiglu_not_finite(I):
+    """As the formulas in fp32.  Both sides are rounded to bf16 from values that are apart by
+    12 * 2^-24 at most: by a step at most.  The rows beside keep their bits, as do
+    the row's columns that are not among the same eight."""
+    R = 5
+    gu = (torch.randn(R, 2 * I, generator=gen(1), device="cuda")).to(BF16)
+    dz = torch.randn(R, I, generator=gen(2), device="cuda").to(BF16)
+    w = torch.rand(R, generator=gen(3), device="cuda") + 0.5
+    z0, (d0, dw0) = pkg.moe_swiglu(gu, w), pkg.moe_swiglu_backward(dz, gu, w)
+    gu2 = gu.clone()
+    gu2[2, I - 16:I] = torch.tensor(GATES, device="cuda").to(BF16)
+    gu2[2, 2 * I - 16:] = torch.tensor(UPS, device="cuda").to(BF16)
+    z, (d, dw) = pkg.moe_swiglu(gu2, w), pkg.moe_swiglu_backward(dz, gu2, w)
+    g, u = gu2[:, :I].float(), gu2[:, I:].float()
+    s = 1 / (1 + torch.exp(-g))
+    silu, dl = g * s, dz.float() * w[:, None]
+    tol = 2 * U16 + 12 * U32
+    same_as_formula(z[2, -16:], (silu * u * w[:, None])[2, -16:], tol)
+    # (the gradient's factor 1 + g (1 - s) of these gates has no cancellation)
+    same_as_formula(d[2, I - 16:I], (dl * u * (s * (1 + g * (1 - s))))[2, -16:], tol)
+    same_as_formula(d[2, 2 * I - 16:], (dl * silu)[2, -16:], tol)
+    assert torch.isnan(dw[2])
+    rows, cols = [0, 1, 3, 4], list(range(I - 16)) + list(range(I, 2 * I - 16))
+    assert torch.equal(z[rows], z0[rows]) and torch.equal(z[2, :I - 16], z0[2, :I - 16])
+    assert torch.equal(d[rows], d0[rows]) and torch.equal(d[2, cols], d0[2, cols])
+    assert torch.equal(dw[rows], dw0[rows])
+
+
+def test_swiglu_backward_sums_that_are_infinite():
+    """dw of one infinite summand is infinite, of two opposite ones NaN."""
+    gu = torch.ones(3, 32, device="cuda", dtype=BF16)
+    dz = torch.ones(3, 16, device="cuda", dtype=BF16)
+    gu[1, 3] = INF
+    gu[2, 16 + 3], gu[2, 16 + 5] = INF, -INF
+    _, dw = pkg.moe_swiglu_backward(dz, gu, torch.ones(3, device="cuda"))
+    assert torch.isfinite(dw[0]) and dw[1].item() == INF and torch.isnan(dw[2])
