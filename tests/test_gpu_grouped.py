@@ -1,6 +1,7 @@
 """GPU parity of the products of rows sorted by expert and their weight
 gradients: bit-exact on integers whose sums are exact, within rounding bounds
 otherwise; and the training step of a layer made of them."""
+import os
 import threading
 
 import numpy as np
@@ -565,3 +566,36 @@ def test_rows_of_calls_in_parts_of_K_agree():
     for counts in ([1] + [0] * 7, [2] * 8, [4] * 8):
         y = pkg.moe_grouped_matmul(x[:sum(counts)].clone(), w, offsets_of(counts), out_dtype=F32)
         assert ((y[0].double() - ref[0]).abs() <= bound[0]).all()
+
+
+def test_training_step_as_documented():
+    """The README's step: against autograd in 64 bits (1.5 % in the norm, see
+    test_training_step_of_a_layer), and the same bits in every run: a token's rows are
+    added in a fixed order, in fp32."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        text = f.read()
+    code = text[text.index("# the experts of a training step"):text.index("# rows and weights")]
+    M, H, I, E = 70, 136, 72, 32
+    f = lambda s, *shape: (torch.randn(*shape, generator=gen(s), device="cuda") * 0.3).to(BF16)  # noqa: E731
+    logits = f(4, M, E).float() * 4
+    w, ids = pkg.moe_route(logits, 8, "sigmoid", k_group=4, group_count=8, group_select_mode=1,
+                           routed_scaling_factor=2.5)
+    env = dict(moe=pkg, torch=torch, E=E, hidden=f(1, M, H), w13=f(2, E, H, 2 * I), w2=f(3, E, I, H),
+               router_logits=logits, w=w, ids=ids, grad_out=f(5, M, H))
+    names = ("y", "grad_hidden", "grad_w13", "grad_w2", "grad_logits")
+    runs = []
+    for _ in range(3):
+        exec(code, dict(env), local := dict(env))
+        runs.append([local[n] for n in names])
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))
+    t = [env[n].double().requires_grad_() for n in ("hidden", "w13", "w2", "router_logits")]
+    p = torch.sigmoid(t[3]).gather(1, ids.long())
+    p = 2.5 * p / p.sum(1, keepdim=True)          # (sigmoid weights are divided by their sum)
+    assert ((p.detach() - w).abs() < 1e-5).all()
+    h = torch.einsum("mh,mkhi->mki", t[0], t[1][ids.long()])
+    a = torch.nn.functional.silu(h[..., :I]) * h[..., I:] * p[..., None]
+    ry = torch.einsum("mki,mkih->mh", a, t[2][ids.long()])
+    (ry * env["grad_out"].double()).sum().backward()
+    for got, ref in zip(runs[0], (ry.detach(), *(v.grad for v in t))):
+        assert ((got.double() - ref).norm() / ref.norm()).item() < 0.015
