@@ -12,15 +12,18 @@
 // 32: experts of 1, 40 or 300 rows cost what they have, and one kernel serves a decode step's
 // few rows (bound by the weights' bytes) and a long prefill (bound by the tensor cores).
 //
-// Measured on a GB300, floors at 6.79 TB/s and 1954 TFLOP/s (FP4 four times that):
-//   product 8192 rows of 8 experts, 4096 x 28672        1276-1294 us (floor 985; 1115 at the
-//     tensor cores' sustained rate: back to back the clock is down to 1.4 GHz)
-//   product 32 rows of 8 experts, 14336 x 4096          130-136 us (137: HBM)
-//   weight grad 8192 rows of 8, 14336 x 4096 to fp32    736-766 us (492: the output's stores)
-//   weight grad 131064 rows of 128, 2048 x 1536, bf16   643-681 us (422; 478 sustained)
-//   FP4 8192 x 7168 x 4096                              83-87 us (62: the round trip of the
+// Measured on a GB300; in brackets the operands' and outputs' bytes at a copy's 6.79 TB/s (reads
+// alone reach 7.0), or the operations at cuBLAS's 1912 TFLOP/s (FP4 four times that), 1711 in
+// calls back to back, where the clock is down to 1.4 GHz:
+//   product 8192 rows of 8 experts, 4096 x 28672        1272-1300 us (1006; 1125 sustained)
+//   product 32 rows of 8 experts, 14336 x 4096          133-136 us (137: HBM)
+//   weight grad 8192 rows of 8, 14336 x 4096 to fp32    750-756 us (503; 562 sustained: the
+//     output's stores)
+//   weight grad 131064 rows of 128, 2048 x 1536, bf16   655-666 us (431; 482 sustained: tiles of
+//     unequal cost go to the pairs in turn)
+//   FP4 8192 x 7168 x 4096                              83 us (63: the round trip of the
 //     five stages that shared memory holds)
-//   FP4 64 rows of 32 experts, 7168 x 4096              68-76 us with the rows' quantisation (64)
+//   FP4 64 rows of 32 experts, 7168 x 4096              72-76 us with the rows' quantisation (64)
 #include <algorithm>
 #include <type_traits>
 
@@ -291,7 +294,13 @@ __global__ void __launch_bounds__(kGrThreads, 1)
   const int part = even / 2, parts = SPLIT ? P.parts : 1;
   const uint16_t both = static_cast<uint16_t>(3u << even);
   uint8_t* tiles = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  // the odd CTA's word that stage's part of it is in place
+  // The odd CTA's word that stage's part of it is in place: its scales, or its cleared tail.
+  // Their writers fence them to the async proxy before they arrive on the tail barrier that
+  // the sender of this copy waits for (or sent it themselves), and the copy is of that proxy
+  // and behind them.  That its completion on the even CTA's barrier makes them visible to the
+  // pair's MMA rests on this: they are read by the tensor core of the SM that wrote them, as what
+  // TMA loads there is, whose completion reaches the even CTA the same way.  The PTX memory
+  // model itself promises a completed copy's own bytes only.
   auto relay = [&](int stage) {
     ptx::bulk_copy_to_cluster(ptx::mapa_shared(ptx::smem_u32(ctl.relay[stage]), even), ctl.relay_src,
                               kGrRelay, ptx::mapa_shared(ptx::smem_u32(&ctl.full[stage]), even));
@@ -580,8 +589,8 @@ __global__ void __launch_bounds__(kGrThreads, 1)
       // 1024 as the rows lie in memory, in bulk copies; else by the warp's lanes, a row
       // each, in asynchronous copies.  Those are as many requests as lanes, and slower
       // than the MMAs (8192 x 7168 x 4096: 155 us from registers, 93-100 by asynchronous
-      // copies, 83-87 by TMA, 78 without any; 8192 x 7200 x 4096: 195; a bulk copy for each
-      // row 849; 32768 rows of 64 experts, K 768, N 2048: 109 by the lanes, 87 in bulk).
+      // copies, 83 by TMA, 78 without any; 8192 x 7200 x 4096: 209; a bulk copy for each
+      // row 849; 32768 rows of 64 experts, K 768, N 2048: 88 by the lanes, 74 in bulk).
       // The warp that takes the scales from the ring is another one: its fence for the
       // tensor core's reads would wait for copies in flight.
       const int KG = P.K / 32;
@@ -1058,9 +1067,10 @@ __global__ void __launch_bounds__(kGrThreads, 1)
 // nearest, every 512 rows or columns where they leave in fp32 (FP4: 2048; an MMA is four
 // times as deep), and every 1024 (4096) where they leave in bf16: 64 MMAs drop 1.5e-5 at
 // most, whatever the sum's length, beside the output's own rounding of 4e-3 (2^22 positive
-// products in the tensor core alone come out 2.4 % too small).  Against the whole sum there: 8192 rows of 8, 4096 x 28672, 1326 -> 1332 us, 131064 rows of 128, 1536 x
-// 2048, 582 -> 575, their weight gradient 681 -> 684, 1 x 7168 x 4096 11.6 -> 11.7 (every
-// 512: 1336, 578, 692 and 11.8).
+// products in the tensor core alone come out 2.4 % too small).  Against the whole sum there:
+// 8192 rows of 8, 4096 x 28672, 1326 -> 1332 us; 131064 rows of 128, 1536 x 2048, 582 -> 575,
+// their weight gradient 681 -> 684; 1 x 7168 x 4096 11.6 -> 11.7 (every 512: 1336, 578, 692
+// and 11.8).
 int gr_chunk(const GroupedProductArgs& a) { return a.out_f32 ? 8 : 16; }
 
 // A launch with clusters of `ctas` (cfg.attrs: room for two).
